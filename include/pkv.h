@@ -48,7 +48,12 @@
 extern "C" {
 #endif
 
-typedef enum { PKV_F32 = 0, PKV_F16 = 1, PKV_BF16 = 2 } pkv_dtype;
+typedef enum {
+    PKV_F32 = 0,
+    PKV_F16 = 1,
+    PKV_BF16 = 2,
+    PKV_E4M3 = 3   /* 8-bit cache values (see pkv_append_cache_q8); only where a call names it */
+} pkv_dtype;
 
 typedef enum {
     PKV_OK = 0,
@@ -381,6 +386,178 @@ int pkv_swap_blocks(void *const *gpu_k, void *const *gpu_v, void *const *host_k,
                     void *const *host_v, int num_layers, const int64_t *pairs, int num_pairs,
                     size_t block_bytes, int64_t gpu_blocks, int64_t host_blocks, int direction,
                     uint32_t *device_status, void *stream);
+
+/*
+ * append_cache_q8 -- write each sequence's new key/value rows into a cache of
+ * 8-bit values with one scale per block and kv head.  (The pages keep the
+ * cache in the model's type; an 8-bit cache halves the bytes that decode
+ * attention has to read.)
+ *
+ * The cache.  k_cache, v_cache: e4m3 [num_blocks, num_kv_heads, block_size,
+ * head_dim] (1 sign, 4 exponent, 3 mantissa bits, largest value 448, no
+ * infinity).  k_scales, v_scales: float [num_blocks, S], S = num_kv_heads
+ * rounded up to a multiple of 4 (entries past num_kv_heads are not used).  A
+ * row of block b and kv head h stands for its e4m3 values times the block's
+ * scale, a power of two: the smallest 2^e, e >= -126, with
+ * max|x| <= 448 * 2^e over the values of the block's rows of that head.
+ *
+ * The call.  Sequence s gets n_s = query_start[s + 1] - query_start[s] new
+ * tokens, which are its last ones: context_lens[s] counts them, and token
+ * query_start[s] + i sits at position context_lens[s] - n_s + i.  For every
+ * block they touch, and every kv head, for K and for V:
+ *   - if the new tokens start the block, the scale is set from them;
+ *   - if the block holds rows of the sequence already, the scale becomes the
+ *     larger of its own and what the new rows need; where it grows, the rows
+ *     held are written again as round(v * old / new);
+ *   - new values are round(x / scale).
+ * Rounding is to the nearest e4m3 value, halves to even.  NaN and infinities
+ * are stored as NaN and take no part in the scale.  Rows behind the last new
+ * one keep their bytes.  The result depends on no order of execution.
+ *
+ *   key, value   [num_tokens, num_kv_heads, head_dim] of dtype (PKV_F16 or
+ *                PKV_BF16; PKV_F32: PKV_EUNSUPPORTED), 16-byte aligned
+ *   block_tables int32 [num_seqs, max_blocks_per_seq]
+ *   context_lens int32 [num_seqs], new tokens included
+ *   query_start  int32 [num_seqs + 1], ascending; tokens before
+ *                query_start[0] and from query_start[num_seqs] on are padding.
+ *                NULL: a decode step, token s is sequence s's only new one
+ *                (num_tokens == num_seqs); a sequence of length 0 is padding
+ * Device errors, the sequence's (or the block's) tokens skipped: a length
+ * below n_s or beyond the table, or token ranges outside [0, num_tokens]:
+ * PKV_DEV_BAD_CONTEXT_LEN; a block id outside the pool: PKV_DEV_BAD_BLOCK.
+ * Caller contract: no two sequences of a call write into the same block (copy
+ * a shared block first).  To copy or swap blocks, pass the caches and then
+ * the scale arrays to pkv_copy_blocks / pkv_swap_blocks (block_bytes of the
+ * scales: S * 4).  head_dim 64 or 128, block_size 8, 16 or 32.
+ */
+int pkv_append_cache_q8(const void *key, const void *value, int dtype, void *k_cache, void *v_cache,
+                        float *k_scales, float *v_scales, const int32_t *block_tables,
+                        int max_blocks_per_seq, const int32_t *context_lens,
+                        const int32_t *query_start, int num_seqs, int num_tokens, int num_kv_heads,
+                        int head_dim, int block_size, int64_t num_blocks, uint32_t *device_status,
+                        void *stream);
+
+/*
+ * paged_attention_decode_q8 -- pkv_paged_attention_decode over a cache that
+ * pkv_append_cache_q8 wrote:
+ *     out[s,h,:] = sum_i softmax_i(scale * q[s,h,:] . (ks k_i)) * (vs v_i)
+ * with ks, vs the scales of token i's block.  L = 0 gives a zero row.
+ *
+ *   q          [num_seqs, num_heads, head_dim] of q_dtype (PKV_F16 or
+ *              PKV_BF16; PKV_F32: PKV_EUNSUPPORTED), 16-byte aligned
+ *   out        [num_seqs, num_heads, head_dim] of out_dtype (any)
+ *   k_scales, v_scales  as pkv_append_cache_q8 leaves them
+ *   max_context_len  host bound of context_lens (at most max_blocks_per_seq *
+ *              block_size)
+ *   partition_size  0 = automatic; else tokens per partition of the context,
+ *              a multiple of 32 and of block_size (1024 blocks at most, unless
+ *              the whole context is shorter: PKV_EUNSUPPORTED)
+ *   workspace  at least pkv_paged_attention_list_workspace_bytes(num_seqs,
+ *              num_heads, num_kv_heads, head_dim, block_size,
+ *              ceil(max_context_len / block_size), partition_size) bytes,
+ *              16-byte aligned (may be NULL where that is 0)
+ * head_dim 64 or 128; block_size 8, 16 or 32; num_heads / num_kv_heads 1 to 8;
+ * num_seqs and num_kv_heads up to 65,535.  Device errors as for
+ * pkv_paged_attention_decode: the rows they concern are zero.
+ */
+int pkv_paged_attention_decode_q8(void *out, int out_dtype, const void *q, int q_dtype,
+                                  const void *k_cache, const void *v_cache, const float *k_scales,
+                                  const float *v_scales, const int32_t *block_tables,
+                                  int max_blocks_per_seq, const int32_t *context_lens, int num_seqs,
+                                  int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                  int64_t num_blocks, int max_context_len, float scale,
+                                  int partition_size, void *workspace, size_t workspace_bytes,
+                                  uint32_t *device_status, void *stream);
+
+/*
+ * Bytes of workspace of pkv_paged_attention_decode_q8 and
+ * pkv_paged_attention_decode_selected on the current device.
+ * max_list_blocks: ceil(max_context_len / block_size), or num_selected.
+ * 0 if none is needed or on invalid sizes.
+ */
+size_t pkv_paged_attention_list_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads,
+                                                int head_dim, int block_size, int max_list_blocks,
+                                                int partition_size);
+
+/*
+ * summarize_blocks -- the range of the keys of every block that a call's new
+ * tokens touched, for pkv_select_blocks: per kv head and key dimension the
+ * smallest and the largest value over the rows the block holds now.  Called
+ * after pkv_reshape_and_cache or pkv_append_cache_q8 with the same tables,
+ * lengths and query_start; it reads the rows from the cache, so it may be
+ * repeated, and a block copied with its summary stays right.
+ *
+ *   k_cache      [num_blocks, num_kv_heads, block_size, head_dim] of
+ *                cache_dtype: PKV_F16, PKV_BF16, or PKV_E4M3 with k_scales
+ *                (NULL otherwise)
+ *   summaries    [num_blocks, num_kv_heads, 2, head_dim] of summary_dtype:
+ *                the cache's type, PKV_BF16 for an e4m3 cache; row 0 the
+ *                minima, row 1 the maxima.  A NaN key makes both NaN.
+ *   num_tokens   host bound of query_start[num_seqs]
+ * Other arguments, device errors and shapes as for pkv_append_cache_q8.
+ */
+int pkv_summarize_blocks(const void *k_cache, int cache_dtype, const float *k_scales,
+                         void *summaries, int summary_dtype, const int32_t *block_tables,
+                         int max_blocks_per_seq, const int32_t *context_lens,
+                         const int32_t *query_start, int num_seqs, int num_tokens,
+                         int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                         uint32_t *device_status, void *stream);
+
+/*
+ * select_blocks -- for every sequence and kv head, the num_selected blocks
+ * that a decode step should attend to: the first keep_first, the last
+ * keep_last, and of the others those with the highest score
+ *     sum over the kv head's query heads g, sum_d max(q_gd lo_d, q_gd hi_d),
+ * an upper bound on the sum of the heads' largest q . k in the block (lo, hi:
+ * the block's summary).  The selection is that of the exact scores, whatever
+ * the rounding of intermediate sums; equal scores go to the lower block, a
+ * NaN score counts as +infinity.  (For a softmax scale > 0.)
+ *
+ *   selected     int32 [num_seqs, num_kv_heads, num_selected] (written):
+ *                logical block numbers in ascending order; all blocks, then
+ *                -1, where the sequence has fewer
+ *   q            [num_seqs, num_heads, head_dim] of q_dtype
+ *   summaries    as pkv_summarize_blocks leaves them
+ *   keep_first, keep_last  >= 0, together at most num_selected
+ * q_dtype and summary_dtype: PKV_F16 or PKV_BF16 (PKV_F32: PKV_EUNSUPPORTED).
+ * Shapes as for pkv_paged_attention_decode_q8; contexts of at most 131,072
+ * blocks.  A length outside [0, max_context_len] (PKV_DEV_BAD_CONTEXT_LEN) or
+ * a block id outside the pool (PKV_DEV_BAD_BLOCK) selects nothing: all -1.
+ */
+int pkv_select_blocks(int32_t *selected, const void *q, int q_dtype, const void *summaries,
+                      int summary_dtype, const int32_t *block_tables, int max_blocks_per_seq,
+                      const int32_t *context_lens, int num_seqs, int num_heads, int num_kv_heads,
+                      int head_dim, int block_size, int64_t num_blocks, int max_context_len,
+                      int num_selected, int keep_first, int keep_last, uint32_t *device_status,
+                      void *stream);
+
+/*
+ * paged_attention_decode_selected -- single-query attention of every sequence
+ * over the selected blocks of its context: the softmax runs over their tokens
+ * alone.  With all blocks selected it is the attention over the whole context.
+ *
+ *   selected   int32 [num_seqs, num_kv_heads, num_selected]: logical block
+ *              numbers, strictly ascending, -1 behind the last one (as
+ *              pkv_select_blocks writes them).  A list that is not, or that
+ *              names a block beyond the context: PKV_DEV_BAD_BLOCK, zero rows.
+ *              An empty list: zero rows.
+ *   kv_dtype   PKV_F16 or PKV_BF16 (then q_dtype is the same), or PKV_E4M3
+ *              with k_scales and v_scales (NULL otherwise)
+ *   workspace  as for pkv_paged_attention_decode_q8, max_list_blocks =
+ *              num_selected
+ * Everything else as for pkv_paged_attention_decode_q8.
+ */
+int pkv_paged_attention_decode_selected(void *out, int out_dtype, const void *q, int q_dtype,
+                                        const void *k_cache, const void *v_cache, int kv_dtype,
+                                        const float *k_scales, const float *v_scales,
+                                        const int32_t *block_tables, int max_blocks_per_seq,
+                                        const int32_t *context_lens, const int32_t *selected,
+                                        int num_selected, int num_seqs, int num_heads,
+                                        int num_kv_heads, int head_dim, int block_size,
+                                        int64_t num_blocks, int max_context_len, float scale,
+                                        int partition_size, void *workspace,
+                                        size_t workspace_bytes, uint32_t *device_status,
+                                        void *stream);
 
 /*
  * paged_attention_decode_static -- the same attention as

@@ -11,6 +11,12 @@ PagedAttention Algorithm" and "Advanced Features"):
   paged_attention_decode  single-query attention over a block-table-mapped cache
   reshape_and_cache       scatter of new tokens' K/V into their slots
   copy_blocks             copy-on-write copy of shared blocks
+and, for caches that are held in 8 bits or read in part:
+  append_cache_q8                  new tokens' K/V into e4m3 blocks with scales
+  paged_attention_decode_q8        attention over such a cache
+  summarize_blocks                 the range of each block's keys
+  select_blocks                    the blocks that bound says matter to a query
+  paged_attention_decode_selected  attention over the selected blocks
 """
 from __future__ import annotations
 
@@ -31,12 +37,14 @@ __all__ = [
     "SWAP_OUT", "SWAP_IN", "BlockPool",
     "DEV_BAD_BLOCK", "DEV_BAD_SLOT", "DEV_TIMEOUT", "DEV_BAD_CONTEXT_LEN", "DEV_DRAIN_TIMEOUT",
     "HEADER_PATH", "bounded_wait_hook",
+    "append_cache_q8", "summarize_blocks", "select_blocks", "paged_attention_decode_q8",
+    "paged_attention_decode_selected", "paged_attention_list_workspace_bytes", "q8_scales",
 ]
 
 HEADER_PATH = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                            "include", "pkv.h")
 
-PKV_F32, PKV_F16, PKV_BF16 = 0, 1, 2
+PKV_F32, PKV_F16, PKV_BF16, PKV_E4M3 = 0, 1, 2, 3
 _DTYPE = {torch.float32: PKV_F32, torch.float16: PKV_F16, torch.bfloat16: PKV_BF16}
 
 DEV_BAD_BLOCK, DEV_BAD_SLOT, DEV_TIMEOUT, DEV_BAD_CONTEXT_LEN, DEV_DRAIN_TIMEOUT = 1, 2, 4, 8, 16
@@ -113,6 +121,24 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     L.pkv_copy_blocks.restype = i32
     L.pkv_swap_blocks.argtypes = [vp, vp, vp, vp, i32, vp, i32, u64, i64, i64, i32, vp, vp]
     L.pkv_swap_blocks.restype = i32
+    L.pkv_append_cache_q8.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32,
+                                      i32, i64, vp, vp]
+    L.pkv_append_cache_q8.restype = i32
+    L.pkv_summarize_blocks.argtypes = [vp, i32, vp, vp, i32, vp, i32, vp, vp, i32, i32, i32, i32, i32,
+                                       i64, vp, vp]
+    L.pkv_summarize_blocks.restype = i32
+    L.pkv_select_blocks.argtypes = [vp, vp, i32, vp, i32, vp, i32, vp, i32, i32, i32, i32, i32, i64,
+                                    i32, i32, i32, i32, vp, vp]
+    L.pkv_select_blocks.restype = i32
+    L.pkv_paged_attention_list_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+    L.pkv_paged_attention_list_workspace_bytes.restype = u64
+    L.pkv_paged_attention_decode_q8.argtypes = [vp, i32, vp, i32, vp, vp, vp, vp, vp, i32, vp, i32, i32,
+                                                i32, i32, i32, i64, i32, f32, i32, vp, u64, vp, vp]
+    L.pkv_paged_attention_decode_q8.restype = i32
+    L.pkv_paged_attention_decode_selected.argtypes = [vp, i32, vp, i32, vp, vp, i32, vp, vp, vp, i32, vp,
+                                                      vp, i32, i32, i32, i32, i32, i32, i64, i32, f32,
+                                                      i32, vp, u64, vp, vp]
+    L.pkv_paged_attention_decode_selected.restype = i32
     L.pkv_status_string.argtypes = [i32]
     L.pkv_status_string.restype = ctypes.c_char_p
     L.pkv_last_decode_launches.argtypes = []
@@ -539,3 +565,278 @@ def swap_blocks(gpu_k: Sequence[torch.Tensor], gpu_v: Sequence[torch.Tensor],
                                         gshape[0], hshape[0], int(direction),
                                         _ptr(device_status), _stream(stream))
     _check(rc, "pkv_swap_blocks")
+
+
+# ------------------------------------------- caches held in 8 bits, or read in part
+
+
+def q8_scales(num_blocks: int, num_kv_heads: int, device=None) -> torch.Tensor:
+    """Zeroed scales of an 8-bit cache: float32 [num_blocks, S], S =
+    num_kv_heads rounded up to a multiple of 4 (so that copy_blocks and
+    swap_blocks can move them like blocks)."""
+    return torch.zeros(num_blocks, -(-num_kv_heads // 4) * 4, dtype=torch.float32, device=device)
+
+
+def _ready(named: dict) -> torch.device:
+    """Every tensor (None: absent) on one CUDA device and contiguous -> that device."""
+    dev = None
+    for name, t in named.items():
+        if t is None:
+            continue
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, other arguments on {dev}")
+    return dev
+
+
+def _launch(fn, what: str, dev: torch.device, stream, args: tuple) -> None:
+    """fn(*args, stream) with the tensors' device current; stream None: that
+    device's current stream."""
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _launch(fn, what, dev, stream, args)
+    rc = fn(*args, _stream(stream))
+    if rc != 0:
+        raise PkvError(rc, what)
+
+
+def _status_arg(t: Optional[torch.Tensor]):
+    if t is not None and (t.numel() < 1 or t.element_size() != 4 or t.is_floating_point()):
+        raise ValueError("device_status must be an int32 or uint32 tensor")
+    return _ptr(t)
+
+
+def _tables(block_tables: torch.Tensor, context_lens: torch.Tensor, B: int) -> int:
+    """Checks the tables and lengths of B sequences -> table entries per sequence."""
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise ValueError("block_tables and context_lens must be int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
+        raise ValueError("block_tables must be [B, MB] and context_lens [B]")
+    return int(block_tables.shape[1])
+
+
+def _q8_scale_args(k_cache: torch.Tensor, *scales: torch.Tensor) -> None:
+    NB, Hk = k_cache.shape[:2]
+    for s in scales:
+        if s.dtype != torch.float32 or tuple(s.shape) != (NB, -(-Hk // 4) * 4):
+            raise ValueError("scales must be float32 [num_blocks, num_kv_heads rounded up to a multiple of 4]")
+
+
+def _new_tokens(query_start: Optional[torch.Tensor], B: int, T: int) -> None:
+    if query_start is None:
+        if T != B:
+            raise ValueError("without query_start every sequence has one new token")
+    elif query_start.dtype != torch.int32 or tuple(query_start.shape) != (B + 1,):
+        raise ValueError("query_start must be int32 [B + 1]")
+
+
+def append_cache_q8(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    k_scales: torch.Tensor, v_scales: torch.Tensor, block_tables: torch.Tensor,
+                    context_lens: torch.Tensor, query_start: Optional[torch.Tensor] = None, *,
+                    device_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Writes each sequence's new tokens into its blocks of an 8-bit cache.
+
+    key, value: [T, Hk, D] (float16 or bfloat16); k_cache, v_cache: float8_e4m3fn
+    [NB, Hk, bs, D]; k_scales, v_scales: as q8_scales makes them, each block's
+    and kv head's power-of-two scale.  The new tokens of sequence s are rows
+    query_start[s] .. query_start[s + 1] of key and value (int32 [B + 1]; None:
+    one token per sequence) and its last ones: context_lens counts them.  A
+    block's scale grows with its rows; rows it holds are then rescaled.  Blocks
+    shared by sequences are copied first (copy_blocks on the caches and on the
+    scales)."""
+    dev = _ready(dict(key=key, value=value, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
+                      v_scales=v_scales, block_tables=block_tables, context_lens=context_lens,
+                      query_start=query_start, device_status=device_status))
+    T, Hk, D = key.shape
+    NB, Hk2, bs, D2 = k_cache.shape
+    if (Hk2, D2) != (Hk, D) or value.shape != key.shape or v_cache.shape != k_cache.shape:
+        raise ValueError("shape mismatch")
+    if key.dtype not in _DTYPE or value.dtype != key.dtype:
+        raise ValueError("key and value must share a floating dtype")
+    if k_cache.dtype != torch.float8_e4m3fn or v_cache.dtype != torch.float8_e4m3fn:
+        raise ValueError("k_cache and v_cache must be float8_e4m3fn")
+    _q8_scale_args(k_cache, k_scales, v_scales)
+    B = int(context_lens.shape[0])
+    MB = _tables(block_tables, context_lens, B)
+    _new_tokens(query_start, B, T)
+    _launch(load_library().pkv_append_cache_q8, "pkv_append_cache_q8", dev, stream, (
+        _ptr(key), _ptr(value), _DTYPE[key.dtype], _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
+        _ptr(v_scales), _ptr(block_tables), MB, _ptr(context_lens), _ptr(query_start), B, T, Hk, D, bs,
+        NB, _status_arg(device_status)))
+
+
+def summarize_blocks(k_cache: torch.Tensor, summaries: torch.Tensor, block_tables: torch.Tensor,
+                     context_lens: torch.Tensor, query_start: Optional[torch.Tensor] = None, *,
+                     num_tokens: Optional[int] = None, k_scales: Optional[torch.Tensor] = None,
+                     device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """summaries[b, h, 0 / 1] = smallest / largest key of each dimension over the
+    rows that block b holds, for the blocks that the call's new tokens touched
+    (context_lens and query_start as for append_cache_q8; num_tokens: host
+    bound of query_start[B], needed with it).
+
+    summaries: [NB, Hk, 2, D] of the cache's dtype, bfloat16 for an 8-bit cache
+    (k_cache float8_e4m3fn, with its k_scales)."""
+    dev = _ready(dict(k_cache=k_cache, summaries=summaries, block_tables=block_tables,
+                      context_lens=context_lens, query_start=query_start, k_scales=k_scales,
+                      device_status=device_status))
+    NB, Hk, bs, D = k_cache.shape
+    q8 = k_cache.dtype == torch.float8_e4m3fn
+    if not q8 and k_cache.dtype not in _DTYPE:
+        raise ValueError("k_cache must be float16, bfloat16 or float8_e4m3fn")
+    if q8 != (k_scales is not None):
+        raise ValueError("k_scales go with a float8_e4m3fn cache")
+    if q8:
+        _q8_scale_args(k_cache, k_scales)
+    if tuple(summaries.shape) != (NB, Hk, 2, D) or summaries.dtype != (torch.bfloat16 if q8 else k_cache.dtype):
+        raise ValueError("summaries must be [NB, Hk, 2, D] of the cache's dtype (bfloat16 for an 8-bit cache)")
+    B = int(context_lens.shape[0])
+    MB = _tables(block_tables, context_lens, B)
+    if num_tokens is None:
+        if query_start is not None:
+            raise ValueError("query_start needs num_tokens")
+        num_tokens = B
+    _new_tokens(query_start, B, num_tokens)
+    _launch(load_library().pkv_summarize_blocks, "pkv_summarize_blocks", dev, stream, (
+        _ptr(k_cache), PKV_E4M3 if q8 else _DTYPE[k_cache.dtype], _ptr(k_scales), _ptr(summaries),
+        _DTYPE[summaries.dtype], _ptr(block_tables), MB, _ptr(context_lens), _ptr(query_start), B,
+        int(num_tokens), Hk, D, bs, NB, _status_arg(device_status)))
+    return summaries
+
+
+def select_blocks(selected: torch.Tensor, q: torch.Tensor, summaries: torch.Tensor,
+                  block_tables: torch.Tensor, context_lens: torch.Tensor, block_size: int, *,
+                  keep_first: int = 1, keep_last: int = 1, max_context_len: Optional[int] = None,
+                  device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """selected[s, h] = the K blocks of sequence s that kv head h's query group
+    should attend to, in ascending order (-1 behind the last where the
+    sequence has fewer): the first keep_first, the last keep_last, and those
+    with the highest upper bound on the group's scores (see pkv_select_blocks).
+
+    selected: int32 [B, Hk, K]; q: [B, H, D]; summaries: [NB, Hk, 2, D], both
+    float16 or bfloat16.  max_context_len: host bound of context_lens (what the
+    table can hold if omitted)."""
+    dev = _ready(dict(selected=selected, q=q, summaries=summaries, block_tables=block_tables,
+                      context_lens=context_lens, device_status=device_status))
+    B, H, D = q.shape
+    NB, Hk, two, D2 = summaries.shape
+    if two != 2 or D2 != D or selected.dim() != 3 or tuple(selected.shape[:2]) != (B, Hk):
+        raise ValueError("shape mismatch")
+    if selected.dtype != torch.int32 or q.dtype not in _DTYPE or summaries.dtype not in _DTYPE:
+        raise ValueError("selected must be int32, q and summaries floating")
+    MB = _tables(block_tables, context_lens, B)
+    if max_context_len is None:
+        max_context_len = MB * block_size
+    _launch(load_library().pkv_select_blocks, "pkv_select_blocks", dev, stream, (
+        _ptr(selected), _ptr(q), _DTYPE[q.dtype], _ptr(summaries), _DTYPE[summaries.dtype],
+        _ptr(block_tables), MB, _ptr(context_lens), B, H, Hk, D, int(block_size), NB,
+        int(max_context_len), int(selected.shape[2]), int(keep_first), int(keep_last),
+        _status_arg(device_status)))
+    return selected
+
+
+def paged_attention_list_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                         block_size: int, max_list_blocks: int, partition_size: int = 0) -> int:
+    """Workspace bytes of paged_attention_decode_q8 (max_list_blocks: the blocks
+    of max_context_len) and paged_attention_decode_selected (the K of selected)
+    on the current device."""
+    return int(load_library().pkv_paged_attention_list_workspace_bytes(
+        num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_list_blocks, partition_size))
+
+
+def _list_workspace(workspace, dev, stream, *sizes):
+    """The caller's workspace, or one allocated here for the stream that uses it
+    -> (tensor or None, bytes)."""
+    if workspace is not None:
+        return workspace, workspace.numel() * workspace.element_size()
+    with torch.cuda.device(dev):
+        nbytes = paged_attention_list_workspace_bytes(*sizes)
+    if not nbytes:
+        return None, 0
+    workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if stream is not None:
+        # the allocator must not hand it out again before that stream is done with it
+        workspace.record_stream(stream if hasattr(stream, "cuda_stream")
+                                else torch.cuda.ExternalStream(int(stream), device=dev))
+    return workspace, nbytes
+
+
+def _decode_shapes(out, q, k_cache, v_cache) -> tuple:
+    B, H, D = q.shape
+    NB, Hk, bs, D2 = k_cache.shape
+    if D2 != D or v_cache.shape != k_cache.shape or out.shape != q.shape:
+        raise ValueError("shape mismatch")
+    if out.dtype not in _DTYPE or q.dtype not in _DTYPE:
+        raise ValueError("q and out must be floating")
+    return B, H, D, NB, Hk, bs
+
+
+def paged_attention_decode_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                              k_scales: torch.Tensor, v_scales: torch.Tensor, block_tables: torch.Tensor,
+                              context_lens: torch.Tensor, scale: float, *,
+                              max_context_len: Optional[int] = None, partition_size: int = 0,
+                              workspace: Optional[torch.Tensor] = None,
+                              device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """As paged_attention_decode, over an 8-bit cache that append_cache_q8 wrote.
+
+    q: [B, H, D], float16 or bfloat16; out: [B, H, D], any floating dtype.
+    max_context_len: host bound of context_lens (what the table can hold if
+    omitted).  workspace: paged_attention_list_workspace_bytes, allocated here
+    if needed and not given."""
+    dev = _ready(dict(out=out, q=q, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
+                      block_tables=block_tables, context_lens=context_lens, workspace=workspace,
+                      device_status=device_status))
+    B, H, D, NB, Hk, bs = _decode_shapes(out, q, k_cache, v_cache)
+    if k_cache.dtype != torch.float8_e4m3fn or v_cache.dtype != torch.float8_e4m3fn:
+        raise ValueError("k_cache and v_cache must be float8_e4m3fn")
+    _q8_scale_args(k_cache, k_scales, v_scales)
+    MB = _tables(block_tables, context_lens, B)
+    if max_context_len is None:
+        max_context_len = MB * bs
+    workspace, nbytes = _list_workspace(workspace, dev, stream, B, H, Hk, D, bs,
+                                        -(-int(max_context_len) // bs), partition_size)
+    _launch(load_library().pkv_paged_attention_decode_q8, "pkv_paged_attention_decode_q8", dev, stream, (
+        _ptr(out), _DTYPE[out.dtype], _ptr(q), _DTYPE[q.dtype], _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
+        _ptr(v_scales), _ptr(block_tables), MB, _ptr(context_lens), B, H, Hk, D, bs, NB,
+        int(max_context_len), float(scale), int(partition_size), _ptr(workspace), nbytes,
+        _status_arg(device_status)))
+    return out
+
+
+def paged_attention_decode_selected(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                                    v_cache: torch.Tensor, block_tables: torch.Tensor,
+                                    context_lens: torch.Tensor, selected: torch.Tensor, scale: float, *,
+                                    k_scales: Optional[torch.Tensor] = None,
+                                    v_scales: Optional[torch.Tensor] = None, partition_size: int = 0,
+                                    workspace: Optional[torch.Tensor] = None,
+                                    device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of each sequence over the blocks that ``selected`` (int32 [B,
+    Hk, K], as select_blocks writes it) lists for each kv head: the softmax
+    runs over their tokens alone.
+
+    q, k_cache, v_cache share float16 or bfloat16, or the caches are
+    float8_e4m3fn with their k_scales and v_scales."""
+    dev = _ready(dict(out=out, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                      context_lens=context_lens, selected=selected, k_scales=k_scales, v_scales=v_scales,
+                      workspace=workspace, device_status=device_status))
+    B, H, D, NB, Hk, bs = _decode_shapes(out, q, k_cache, v_cache)
+    q8 = k_cache.dtype == torch.float8_e4m3fn
+    if v_cache.dtype != k_cache.dtype or (not q8 and k_cache.dtype != q.dtype):
+        raise ValueError("q, k_cache and v_cache must share a dtype, or the caches be float8_e4m3fn")
+    if (k_scales is not None) != q8 or (v_scales is not None) != q8:
+        raise ValueError("k_scales and v_scales go with float8_e4m3fn caches")
+    if q8:
+        _q8_scale_args(k_cache, k_scales, v_scales)
+    if selected.dtype != torch.int32 or selected.dim() != 3 or tuple(selected.shape[:2]) != (B, Hk):
+        raise ValueError("selected must be int32 [B, Hk, K]")
+    MB = _tables(block_tables, context_lens, B)
+    K = int(selected.shape[2])
+    workspace, nbytes = _list_workspace(workspace, dev, stream, B, H, Hk, D, bs, K, partition_size)
+    _launch(load_library().pkv_paged_attention_decode_selected, "pkv_paged_attention_decode_selected", dev, stream, (
+        _ptr(out), _DTYPE[out.dtype], _ptr(q), _DTYPE[q.dtype], _ptr(k_cache), _ptr(v_cache),
+        PKV_E4M3 if q8 else _DTYPE[k_cache.dtype], _ptr(k_scales), _ptr(v_scales), _ptr(block_tables), MB,
+        _ptr(context_lens), _ptr(selected), K, B, H, Hk, D, bs, NB, MB * bs, float(scale),
+        int(partition_size), _ptr(workspace), nbytes, _status_arg(device_status)))
+    return out

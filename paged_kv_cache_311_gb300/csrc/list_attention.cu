@@ -1,0 +1,204 @@
+// list_attention.cu -- host side of paged_attention_decode_q8 and
+// paged_attention_decode_selected: checks of arguments, the cut of the list
+// into partitions, launches.
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "list_attention.cuh"
+#include "pkv_host.cuh"
+
+namespace pkv {
+namespace {
+
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// List entries per partition for `rows` (sequence, kv head) rows of at most
+// `blocks` entries: one partition when the rows alone fill the GPU, else
+// enough partitions for several CTAs per SM, of at least 64 tokens each.
+int list_part_blocks(long long rows, int blocks, int block_size, int partition_size)
+{
+    if (blocks < 1)
+        blocks = 1;
+    if (partition_size > 0)
+        return partition_size / block_size;
+    const long long want = 8LL * device_sm_count();
+    long long np = (want + rows - 1) / rows;
+    const int least = 64 / block_size;
+    long long part = (blocks + np - 1) / np;
+    part = (part + least - 1) / least * least;
+    return (int)(part < kListCap ? part : kListCap);
+}
+
+struct ListLayout {
+    size_t acc_off, total;
+};
+bool list_layout(uint64_t seqs, uint64_t heads, uint64_t np, uint64_t head_dim, ListLayout *s)
+{
+    uint64_t rows, ml, acc;
+    if (__builtin_mul_overflow(seqs, heads, &rows) || __builtin_mul_overflow(rows, np, &rows) ||
+        __builtin_mul_overflow(rows, (uint64_t)8, &ml) || __builtin_mul_overflow(rows, head_dim * 4, &acc) ||
+        ml > UINT64_MAX - 256 || ((ml + 255) & ~uint64_t(255)) > UINT64_MAX - acc)
+        return false;
+    s->acc_off = (size_t)((ml + 255) & ~uint64_t(255));
+    s->total = s->acc_off + (size_t)acc;
+    return true;
+}
+
+template <typename T, int D, int BS>
+int run_list(const ListParams &p, cudaStream_t stream)
+{
+    list_attention_kernel<T, D, BS>
+        <<<dim3((unsigned)p.np, (unsigned)p.num_kv_heads, (unsigned)p.num_seqs), kListWarps * 32, 0, stream>>>(p);
+    if (p.np > 1)
+        list_merge_kernel<D><<<(unsigned)((int64_t)p.num_seqs * p.num_kv_heads * p.group), D, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+template <typename T, int D>
+int run_list_block(const ListParams &p, int bs, cudaStream_t s)
+{
+    switch (bs) {
+    case 8: return run_list<T, D, 8>(p, s);
+    case 16: return run_list<T, D, 16>(p, s);
+    default: return run_list<T, D, 32>(p, s);
+    }
+}
+
+template <typename T>
+int run_list_type(const ListParams &p, int head_dim, int bs, cudaStream_t s)
+{
+    return head_dim == 64 ? run_list_block<T, 64>(p, bs, s) : run_list_block<T, 128>(p, bs, s);
+}
+
+int decode_list(void *out, int out_dtype, const void *q, int q_dtype, const void *k_cache, const void *v_cache,
+                int kv_dtype, const float *k_scales, const float *v_scales, const int32_t *block_tables,
+                int max_blocks_per_seq, const int32_t *context_lens, const int32_t *selected, int num_selected,
+                int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                int max_context_len, float scale, int partition_size, void *workspace, size_t workspace_bytes,
+                uint32_t *device_status, void *stream, bool select)
+{
+    if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_dim <= 0 ||
+        num_blocks <= 0 || num_blocks > INT32_MAX || max_blocks_per_seq <= 0 || block_size <= 0 ||
+        max_context_len < 0 || partition_size < 0 || !std::isfinite(scale) ||
+        (int64_t)max_context_len > (int64_t)max_blocks_per_seq * block_size || (select && num_selected <= 0))
+        return PKV_EINVAL;
+    if (out_dtype < PKV_F32 || out_dtype > PKV_BF16 || q_dtype < PKV_F32 || q_dtype > PKV_BF16 ||
+        kv_dtype < PKV_F32 || kv_dtype > PKV_E4M3 || (kv_dtype != PKV_E4M3 && kv_dtype != q_dtype))
+        return PKV_EINVAL;
+    if (q_dtype == PKV_F32 || (head_dim != 64 && head_dim != 128) ||
+        (block_size != 8 && block_size != 16 && block_size != 32) || num_heads / num_kv_heads > kListMaxGroup ||
+        num_kv_heads > 65535 || num_seqs > 65535)
+        return PKV_EUNSUPPORTED;
+    if (partition_size % 32 || partition_size % block_size)
+        return PKV_EINVAL;
+    if (num_seqs == 0)
+        return PKV_OK;
+    const bool q8 = kv_dtype == PKV_E4M3;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || (select && !selected) ||
+        q8 != (k_scales != nullptr) || q8 != (v_scales != nullptr))
+        return PKV_EINVAL;
+    if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
+        !aligned(selected, 4))
+        return PKV_EINVAL;
+
+    const int table_blocks = (max_context_len + block_size - 1) / block_size;
+    const int blocks = select ? num_selected : (table_blocks > 0 ? table_blocks : 1);
+    const int part = list_part_blocks((long long)num_seqs * num_kv_heads, blocks, block_size, partition_size);
+    const int np = (blocks + part - 1) / part;
+    if (part > kListCap && blocks > kListCap)
+        return PKV_EUNSUPPORTED;
+    ListParams p;
+    p.ws_ml = nullptr;
+    p.ws_acc = nullptr;
+    if (np > 1) {
+        ListLayout lay;
+        if (!list_layout(num_seqs, num_heads, np, head_dim, &lay))
+            return PKV_EUNSUPPORTED;
+        if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 16))
+            return PKV_EWORKSPACE;
+        p.ws_ml = static_cast<float *>(workspace);
+        p.ws_acc = reinterpret_cast<float *>(static_cast<char *>(workspace) + lay.acc_off);
+    }
+    p.out = out;
+    p.q = q;
+    p.k_cache = static_cast<const uint8_t *>(k_cache);
+    p.v_cache = static_cast<const uint8_t *>(v_cache);
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.selected = select ? selected : nullptr;
+    p.status = device_status;
+    p.num_blocks = num_blocks;
+    p.num_seqs = num_seqs;
+    p.num_kv_heads = num_kv_heads;
+    p.group = num_heads / num_kv_heads;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.max_context_len = max_context_len;
+    p.num_selected = num_selected;
+    p.scale_stride = q8_scale_stride(num_kv_heads);
+    p.part_blocks = part;
+    p.np = np;
+    p.out_dtype = out_dtype;
+    p.q_dtype = q_dtype;
+    p.qscale = scale * 1.4426950408889634f;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    switch (kv_dtype) {
+    case PKV_F16: return run_list_type<__half>(p, head_dim, block_size, s);
+    case PKV_BF16: return run_list_type<__nv_bfloat16>(p, head_dim, block_size, s);
+    default: return run_list_type<uint8_t>(p, head_dim, block_size, s);
+    }
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+size_t pkv_paged_attention_list_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                                int block_size, int max_list_blocks, int partition_size)
+{
+    if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
+        block_size > 32 || max_list_blocks <= 0 || partition_size < 0 || partition_size % block_size ||
+        (partition_size > 0 && partition_size < block_size))
+        return 0;
+    const int part = list_part_blocks((long long)num_seqs * num_kv_heads, max_list_blocks, block_size, partition_size);
+    const int np = (int)(((long long)max_list_blocks + part - 1) / part);
+    if (np <= 1)
+        return 0;
+    ListLayout lay;
+    return list_layout(num_seqs, num_heads, np, head_dim, &lay) ? lay.total : 0;
+}
+
+int pkv_paged_attention_decode_q8(void *out, int out_dtype, const void *q, int q_dtype, const void *k_cache,
+                                  const void *v_cache, const float *k_scales, const float *v_scales,
+                                  const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                                  int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                  int64_t num_blocks, int max_context_len, float scale, int partition_size,
+                                  void *workspace, size_t workspace_bytes, uint32_t *device_status, void *stream)
+{
+    return decode_list(out, out_dtype, q, q_dtype, k_cache, v_cache, PKV_E4M3, k_scales, v_scales, block_tables,
+                       max_blocks_per_seq, context_lens, nullptr, 0, num_seqs, num_heads, num_kv_heads, head_dim,
+                       block_size, num_blocks, max_context_len, scale, partition_size, workspace, workspace_bytes,
+                       device_status, stream, false);
+}
+
+int pkv_paged_attention_decode_selected(void *out, int out_dtype, const void *q, int q_dtype, const void *k_cache,
+                                        const void *v_cache, int kv_dtype, const float *k_scales,
+                                        const float *v_scales, const int32_t *block_tables, int max_blocks_per_seq,
+                                        const int32_t *context_lens, const int32_t *selected, int num_selected,
+                                        int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                        int64_t num_blocks, int max_context_len, float scale, int partition_size,
+                                        void *workspace, size_t workspace_bytes, uint32_t *device_status, void *stream)
+{
+    return decode_list(out, out_dtype, q, q_dtype, k_cache, v_cache, kv_dtype, k_scales, v_scales, block_tables,
+                       max_blocks_per_seq, context_lens, selected, num_selected, num_seqs, num_heads, num_kv_heads,
+                       head_dim, block_size, num_blocks, max_context_len, scale, partition_size, workspace,
+                       workspace_bytes, device_status, stream, true);
+}
+
+}  // extern "C"

@@ -1,0 +1,369 @@
+// q8_cache.cuh -- the 8-bit cache's writers: append_cache_q8_kernel (new
+// tokens' K and V into e4m3 blocks with one scale per block and kv head) and
+// summarize_blocks_kernel (per block and kv head, each key dimension's
+// smallest and largest value).
+//
+// The cache.  A block's rows of one kv head are e4m3 values v with one scale
+// 2^e: the row's numbers are v * 2^e.  e is the smallest exponent (>= -126)
+// with max|x| <= 448 * 2^e over the block's rows.  A power of two costs a
+// floating 8-bit type no precision (its relative step is 2^-3 of the leading
+// bit whatever the scale) and makes a later, larger scale harmless: the rows
+// already held are divided by a power of two, which is exact until a value
+// falls below 2^-6 of the new scale and loses low bits to the subnormal grid.
+//
+// Work units.  A call appends n_s tokens to each sequence s; a unit is one
+// (block touched by the call, kv head).  A token leads its unit when it is the
+// sequence's first new token or opens a block: exactly one warp then owns the
+// block's rows and scale of that head, so nothing is shared between warps,
+// there are no atomics and the result does not depend on any order.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "pkv_device.cuh"
+
+namespace pkv {
+
+// Floats between two blocks' scales: the kv heads, rounded up so that a
+// block's scales are whole 16-byte pieces (copy_blocks and swap_blocks move
+// them as they move blocks).
+inline int q8_scale_stride(int num_kv_heads) { return (num_kv_heads + 3) / 4 * 4; }
+
+struct AppendParams {
+    const void *key;
+    const void *value;
+    uint8_t *k_cache;
+    uint8_t *v_cache;
+    float *k_scales;
+    float *v_scales;
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    const int32_t *query_start;   // null: token t is sequence t's only new token
+    uint32_t *status;
+    int64_t num_blocks;
+    int num_seqs, num_tokens, num_kv_heads, max_blocks_per_seq, scale_stride;
+};
+
+struct SummarizeParams {
+    const void *k_cache;
+    const float *k_scales;        // null: 16-bit cache
+    void *summaries;              // [NB, Hk, 2, D]
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    const int32_t *query_start;
+    uint32_t *status;
+    int64_t num_blocks;
+    int num_seqs, num_tokens, num_kv_heads, max_blocks_per_seq, scale_stride;
+};
+
+// The unit that token t leads: rows [row0, row1) of physical block `block`
+// are the call's tokens t, t + 1, ...; the block holds `row1` rows after the
+// call.  ok = false: t leads nothing (padding, or not the first of its block)
+// or its sequence is refused.
+struct AppendUnit {
+    bool ok;
+    int row0, row1;
+    int64_t block;
+};
+
+// The sequence that holds token t: the largest s with query_start[s] <= t, or
+// -1.  32 probes a round, by the whole warp.
+__device__ __forceinline__ int find_seq(const int32_t *query_start, int num_seqs, int t, int lane)
+{
+    int lo = 0, hi = num_seqs;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int at = lo + lane * step;
+        const uint32_t below = __ballot_sync(0xffffffffu, at < hi && query_start[at] <= t);
+        const int n = below == 0xffffffffu ? 32 : __ffs(~below) - 1;
+        if (n == 0)
+            return -1;
+        lo += (n - 1) * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
+}
+
+template <int BS, typename P>
+__device__ __forceinline__ AppendUnit append_unit(const P &p, int t, int lane)
+{
+    AppendUnit u{false, 0, 0, 0};
+    int s = t, q0 = t, q1 = t + 1;
+    if (p.query_start) {
+        s = find_seq(p.query_start, p.num_seqs, t, lane);
+        if (s < 0)
+            return u;
+        q0 = p.query_start[s];
+        q1 = p.query_start[s + 1];
+        if (t < q0 || t >= q1)
+            return u;   // a padding token
+    }
+    const int L = p.context_lens[s];
+    const int n = q1 - q0;
+    if (!p.query_start && L == 0)
+        return u;       // a padding sequence
+    if (q0 < 0 || q1 > p.num_tokens || L < n || (int64_t)L > (int64_t)p.max_blocks_per_seq * BS) {
+        if (lane == 0)
+            report(p.status, PKV_DEV_BAD_CONTEXT_LEN);
+        return u;
+    }
+    const int pos = L - n + (t - q0);
+    u.row0 = pos % BS;
+    if (u.row0 != 0 && t != q0)
+        return u;
+    u.row1 = min(BS, u.row0 + (q1 - t));
+    const int b = p.block_tables[(int64_t)s * p.max_blocks_per_seq + pos / BS];
+    if (b < 0 || (int64_t)b >= p.num_blocks) {
+        if (lane == 0)
+            report(p.status, PKV_DEV_BAD_BLOCK);
+        return u;
+    }
+    u.block = b;
+    u.ok = true;
+    return u;
+}
+
+// |x| of a pair of 16-bit values, and packed minima / maxima.
+template <typename T> struct Pair16;
+template <> struct Pair16<__half> {
+    using V = __half2;
+};
+template <> struct Pair16<__nv_bfloat16> {
+    using V = __nv_bfloat162;
+};
+template <typename T>
+__device__ __forceinline__ typename Pair16<T>::V as_pair(uint32_t w)
+{
+    return *reinterpret_cast<typename Pair16<T>::V *>(&w);
+}
+template <typename V>
+__device__ __forceinline__ uint32_t as_word(V v)
+{
+    return *reinterpret_cast<uint32_t *>(&v);
+}
+
+// The exponent of the scale that `amax` (finite, >= 0) needs: the smallest e
+// >= -126 with amax <= 448 * 2^e, from its bits (448 = 1.75 * 2^8).
+__device__ __forceinline__ int scale_exponent(float amax)
+{
+    const uint32_t b = __float_as_uint(amax);
+    const int x = (int)(b >> 23) - 127;   // amax = m * 2^x, 1 <= m < 2 (subnormals end at -126)
+    return max(-126, x - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0));
+}
+
+// Two fp32 values -> two e4m3 bytes (nearest even; the lower byte is `lo`).
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
+{
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// Two e4m3 bytes -> two f16 values (exact).
+__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t two)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)two));
+    return d;
+}
+
+__device__ __forceinline__ float2 float2_of_e4m3(uint32_t two)
+{
+    const uint32_t w = f16x2_of_e4m3(two);
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// Eight 16-bit values -> eight e4m3 bytes of x * inv.  `odd`: the unit holds
+// an infinity; those become NaN (NaN converts to NaN by itself).
+template <typename T>
+__device__ __forceinline__ uint2 quantize8(uint4 w, float inv, bool odd)
+{
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 f = Unpack<T>::pair(in[i]);
+        f.x *= inv;
+        f.y *= inv;
+        if (odd) {
+            f.x = isinf(f.x) ? NAN : f.x;
+            f.y = isinf(f.y) ? NAN : f.y;
+        }
+        o[i] = e4m3x2(f.x, f.y);
+    }
+    return make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
+}
+
+// One warp per (token, kv head, K or V); see the head of the file.
+template <typename T, int D, int BS>
+__global__ void __launch_bounds__(256)
+append_cache_q8_kernel(const __grid_constant__ AppendParams p)
+{
+    constexpr int LPR = D / 8;        // lanes per row (16 bytes of input each)
+    constexpr int RPL = 32 / LPR;     // rows a warp holds per load
+    constexpr int NL = BS / RPL;      // loads of a full block
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x;
+    const int unit = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (unit >= 2 * p.num_kv_heads)
+        return;
+    const int h = unit >> 1;
+    const bool is_v = unit & 1;
+    const AppendUnit u = append_unit<BS>(p, t, lane);
+    if (!u.ok)
+        return;
+    const uint4 *src = reinterpret_cast<const uint4 *>(is_v ? p.value : p.key);
+    uint8_t *blk = (is_v ? p.v_cache : p.k_cache) + (u.block * p.num_kv_heads + h) * (int64_t)(BS * D);
+    float *scale = (is_v ? p.v_scales : p.k_scales) + u.block * p.scale_stride + h;
+    const int r = lane / LPR, c = lane % LPR;
+    const int n = u.row1 - u.row0;
+
+    uint4 x[NL];
+    uint32_t m = 0;   // the largest magnitude, as an ordered pattern of |x| in fp32
+    bool odd = false;
+    typename Pair16<T>::V mx = as_pair<T>(0u);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const int row = i * RPL + r;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (row < n)
+            x[i] = src[((int64_t)(t + row) * p.num_kv_heads + h) * LPR + c];
+    }
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        // |x| by clearing the sign bits; a NaN operand loses to a number
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            mx = __hmax2(mx, as_pair<T>(w[k] & 0x7fff7fffu));
+    }
+    {
+        const float2 f = Unpack<T>::pair(as_word(mx));
+        m = __float_as_uint(fmaxf(f.x, f.y));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (m >= 0x7f800000u) {
+        // an infinity: the finite values set the scale
+        odd = true;
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 f = Unpack<T>::pair(w[k] & 0x7fff7fffu);
+                a = f.x < INFINITY ? fmaxf(a, f.x) : a;
+                a = f.y < INFINITY ? fmaxf(a, f.y) : a;
+            }
+        }
+        m = __reduce_max_sync(0xffffffffu, __float_as_uint(a));
+    }
+    int e = scale_exponent(__uint_as_float(m));
+    if (u.row0 > 0) {
+        // rows already held: the scale never shrinks; when it grows they are
+        // written again, divided by the power of two
+        const int old = (int)((__float_as_uint(*scale) >> 23) & 0xffu) - 127;
+        if (old >= e) {
+            e = old;
+        } else {
+            const float down = __uint_as_float((uint32_t)max(old - e + 127, 0) << 23);
+            uint2 *rows = reinterpret_cast<uint2 *>(blk);
+            for (int i = lane; i < u.row0 * LPR; i += 32) {
+                const uint2 v = rows[i];
+                const float2 a = float2_of_e4m3(v.x & 0xffffu), b = float2_of_e4m3(v.x >> 16);
+                const float2 f = float2_of_e4m3(v.y & 0xffffu), g = float2_of_e4m3(v.y >> 16);
+                rows[i] = make_uint2(e4m3x2(a.x * down, a.y * down) | e4m3x2(b.x * down, b.y * down) << 16,
+                                     e4m3x2(f.x * down, f.y * down) | e4m3x2(g.x * down, g.y * down) << 16);
+            }
+        }
+    }
+    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const int row = i * RPL + r;
+        if (row < n)
+            *reinterpret_cast<uint2 *>(blk + (u.row0 + row) * D + c * 8) = quantize8<T>(x[i], inv, odd);
+    }
+    __syncwarp();
+    if (lane == 0)
+        *scale = __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// One warp per (token, kv head): the token that leads a block reads all the
+// rows the block now holds and writes their minima and maxima.  T: the
+// cache's 16-bit type, or for an e4m3 cache (Q8) the summaries' type.
+template <typename T, int D, int BS, bool Q8>
+__global__ void __launch_bounds__(256)
+summarize_blocks_kernel(const __grid_constant__ SummarizeParams p)
+{
+    using V = typename Pair16<typename std::conditional<Q8, __half, T>::type>::V;
+    using E = typename std::conditional<Q8, __half, T>::type;
+    constexpr int EPL = Q8 ? 16 : 8;      // values of a lane's 16 bytes
+    constexpr int LPR = D / EPL;          // lanes per row
+    constexpr int RPL = 32 / LPR;
+    constexpr int NL = (BS + RPL - 1) / RPL;
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x;
+    const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (h >= p.num_kv_heads)
+        return;
+    const AppendUnit u = append_unit<BS>(p, t, lane);
+    if (!u.ok)
+        return;
+    const uint4 *blk = reinterpret_cast<const uint4 *>(p.k_cache) +
+                       (u.block * p.num_kv_heads + h) * (int64_t)(BS * LPR);
+    const int r = lane / LPR, c = lane % LPR;
+    uint4 x[NL];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        // lanes without a row of their own repeat row 0
+        const int row = i * RPL + r;
+        x[i] = blk[(row < u.row1 ? row : 0) * LPR + c];
+    }
+    V lo[EPL / 2], hi[EPL / 2];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int k = 0; k < EPL / 2; ++k) {
+            V v;
+            if constexpr (Q8)
+                v = as_pair<E>(f16x2_of_e4m3((k & 1) ? w[k >> 1] >> 16 : w[k >> 1] & 0xffffu));
+            else
+                v = as_pair<E>(w[k]);
+            // NaN stays: a block with a NaN key says so
+            lo[k] = i ? __hmin2_nan(lo[k], v) : v;
+            hi[k] = i ? __hmax2_nan(hi[k], v) : v;
+        }
+    }
+#pragma unroll
+    for (int off = LPR; off < 32; off <<= 1) {
+#pragma unroll
+        for (int k = 0; k < EPL / 2; ++k) {
+            lo[k] = __hmin2_nan(lo[k], as_pair<E>(__shfl_xor_sync(0xffffffffu, as_word(lo[k]), off)));
+            hi[k] = __hmax2_nan(hi[k], as_pair<E>(__shfl_xor_sync(0xffffffffu, as_word(hi[k]), off)));
+        }
+    }
+    if (r >= 2)
+        return;
+    // row group 0 writes the minima, row group 1 the maxima
+    uint32_t o[EPL / 2];
+#pragma unroll
+    for (int k = 0; k < EPL / 2; ++k)
+        o[k] = as_word(r ? hi[k] : lo[k]);
+    if constexpr (Q8) {
+        const float s = p.k_scales[u.block * p.scale_stride + h];
+#pragma unroll
+        for (int k = 0; k < EPL / 2; ++k) {
+            const float2 f = __half22float2(as_pair<__half>(o[k]));
+            o[k] = Mma<T>::pack(f.x * s, f.y * s);
+        }
+    }
+    uint4 *dst = reinterpret_cast<uint4 *>(p.summaries) +
+                 ((u.block * p.num_kv_heads + h) * 2 + r) * (int64_t)(D / 8) + c * (EPL / 8);
+#pragma unroll
+    for (int k = 0; k < EPL / 8; ++k)
+        dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+}
+
+}  // namespace pkv
