@@ -450,7 +450,7 @@ int pkv_append_cache_q8(const void *key, const void *value, int dtype, void *k_c
  *   max_context_len  host bound of context_lens (at most max_blocks_per_seq *
  *              block_size)
  *   partition_size  0 = automatic; else tokens per partition of the context,
- *              a multiple of 32 and of block_size (1024 blocks at most, unless
+ *              a multiple of 32 and of block_size (512 blocks at most, unless
  *              the whole context is shorter: PKV_EUNSUPPORTED)
  *   workspace  at least pkv_paged_attention_list_workspace_bytes(num_seqs,
  *              num_heads, num_kv_heads, head_dim, block_size,

@@ -48,10 +48,33 @@ bool list_layout(uint64_t seqs, uint64_t heads, uint64_t np, uint64_t head_dim, 
 template <typename T, int D, int BS>
 int run_list(const ListParams &p, cudaStream_t stream)
 {
-    list_attention_kernel<T, D, BS>
-        <<<dim3((unsigned)p.np, (unsigned)p.num_kv_heads, (unsigned)p.num_seqs), kListWarps * 32, 0, stream>>>(p);
-    if (p.np > 1)
-        list_merge_kernel<D><<<(unsigned)((int64_t)p.num_seqs * p.num_kv_heads * p.group), D, 0, stream>>>(p);
+    using C = ListCfg<T, D, BS>;
+    constexpr int E = ListElem<T>::bytes;
+    alignas(64) CUtensorMap tmk;
+    alignas(64) CUtensorMap tmv;
+    // rows of 64 bytes are read in pairs: lines of 128 bytes, half as many
+    for (int i = 0; i < 2; ++i) {
+        const int rc = encode_kv_map(i ? &tmv : &tmk, i ? p.v_cache : p.k_cache, ListElem<T>::tma, E, D * C::TPL, BS / C::TPL,
+                                     p.num_kv_heads, p.num_blocks, C::BOX_LINES);
+        if (rc)
+            return rc;
+    }
+    static unsigned long long done = 0;
+    auto kern = list_attention_kernel<T, D, BS>;
+    int rc = ensure_smem_attr(reinterpret_cast<const void *>(kern), C::SMEM_BYTES, &done);
+    if (rc)
+        return rc;
+    kern<<<dim3((unsigned)p.np, (unsigned)p.num_kv_heads, (unsigned)p.num_seqs), kListThreads, C::SMEM_BYTES, stream>>>(p, tmk, tmv);
+    if (p.np > 1) {
+        static unsigned long long merge_done = 0;
+        rc = ensure_smem_attr(reinterpret_cast<const void *>(list_merge_kernel<D>), 0, &merge_done);
+        if (rc)
+            return rc;
+        rc = launch_pdl(list_merge_kernel<D>, dim3((unsigned)((int64_t)p.num_seqs * p.num_kv_heads * p.group)),
+                        dim3(kMergeWarps * 32), 0, stream, p);
+        if (rc)
+            return rc;
+    }
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 

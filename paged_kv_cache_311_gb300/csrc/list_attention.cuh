@@ -7,9 +7,28 @@
 // 16-bit cache).
 //
 // One CTA per (partition of the list, kv head, sequence); it owns the kv
-// head's G query heads, so each K/V byte is read once.  With more than one
-// partition the CTAs write (max, sum, unnormalised sum of values) and
-// list_merge_kernel combines them.
+// head's G <= 8 query heads, so each K/V byte is read from HBM once.  With more
+// than one partition the CTAs write (max, sum, unnormalised sum of values)
+// and list_merge_kernel combines them.
+//
+// Each of the CTA's four warps streams tiles of 16 tokens through a ring of
+// TMA loads of its own (128-byte swizzled boxes, one per block) and runs the
+// online softmax over them with warp-level MMAs (m16n8k16): the tile's tokens
+// are M of S^T = K q^T, its dimensions M of O^T += V^T P^T, the query heads N.
+//
+// An e4m3 tile is multiplied in f16, which holds every e4m3 value exactly; the
+// conversion is one instruction per two values, on fragments as ldmatrix
+// leaves them:
+//   K: a thread gets four neighbouring dimensions of a row where a 16-bit
+//      tile gives two.  A dot product may take its dimensions in any order, so
+//      the low pair plays dimensions 2c, 2c + 1 of the MMA's k axis and the
+//      high pair 2c + 8, 2c + 9; q is laid out to match.
+//   V: transposed ldmatrix moves byte pairs (dimensions 2g, 2g + 1) of tokens
+//      2c, 2c + 1; one byte permute pairs them by dimension.  Row g of the
+//      MMA's M axis is then dimension 2g and row g + 8 dimension 2g + 1.
+// The K scale multiplies the scores (exactly: a power of two); the V scale
+// multiplies the tile's product as it joins the accumulators, so no weight
+// has to fit a 16-bit range together with it.
 #pragma once
 
 #include "pa_decode.cuh"
@@ -40,14 +59,64 @@ struct ListParams {
 };
 
 constexpr int kListWarps = 4;
+constexpr int kListThreads = kListWarps * 32;
 constexpr int kListMaxGroup = 8;
-constexpr int kListCap = 1024;   // list entries one CTA stages
+constexpr int kListCap = 512;    // list entries one CTA stages
 
-// The list entries of one CTA, staged in shared memory.
-struct ListStage {
-    int32_t phys[kListCap];
-    float ks[kListCap];
-    float vs[kListCap];
+// The element an MMA works on, and the cache's bytes per element.
+template <typename T> struct ListElem {
+    using M = T;
+    static constexpr int bytes = 2;
+    static constexpr CUtensorMapDataType tma = Elem<T>::tma;
+};
+template <> struct ListElem<uint8_t> {
+    using M = __half;
+    static constexpr int bytes = 1;
+    static constexpr CUtensorMapDataType tma = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+};
+
+// Ring bytes of a CTA: three CTAs fit an SM.
+#ifndef PKV_LIST_RING
+#define PKV_LIST_RING 65536
+#endif
+
+template <typename T, int D, int BS>
+struct ListCfg {
+    static constexpr bool Q8 = ListElem<T>::bytes == 1;
+    static constexpr int TILE = 16;
+    static constexpr int ROW = D * ListElem<T>::bytes;         // bytes of a token's row
+    // a box's lines are 128 bytes: a row's chunk, or two rows of 64 bytes
+    static constexpr int TPL = ROW < 128 ? 128 / ROW : 1;      // tokens per line
+    static constexpr int CHUNKS = ROW < 128 ? 1 : ROW / 128;
+    static constexpr int PPT = (ROW < 128 ? ROW : 128) / 16;   // 16-byte pieces of a token in a line
+    static constexpr int BOX_TOK = BS < TILE ? BS : TILE;
+    static constexpr int BOXES = TILE / BOX_TOK;
+    static constexpr int BOX_LINES = BOX_TOK / TPL;
+    static constexpr int BOX_BYTES = BOX_TOK * ROW;
+    static constexpr int BOX_STRIDE = BOX_BYTES < 1024 ? 1024 : BOX_BYTES;   // swizzle atoms are 1024 bytes
+    static constexpr int TILE_BYTES = BOXES * BOX_STRIDE;      // K (or V) of a tile
+    static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+    static constexpr int S = PKV_LIST_RING / (kListWarps * STAGE_BYTES);
+    static constexpr int KS = D / 16;                          // k-steps of QK, m-tiles of PV
+    static constexpr int AWS = D + 4;                          // row stride of the merge scratch, in floats
+
+    static constexpr int OFF_PHYS = kListWarps * S * STAGE_BYTES;
+    static constexpr int OFF_KS = OFF_PHYS + kListCap * 4;
+    static constexpr int OFF_VS = OFF_KS + (Q8 ? kListCap * 4 : 0);
+    static constexpr int OFF_BAR = OFF_VS + (Q8 ? kListCap * 4 : 0);
+    static constexpr int OFF_FLAG = OFF_BAR + kListWarps * S * 8;
+    static constexpr int SMEM_BYTES = OFF_FLAG + 16 + 1024;    // slack for the alignment to 1024
+
+    static_assert(BOX_BYTES % 512 == 0 && BOX_STRIDE % 1024 == 0 && S >= 2, "ring");
+    static_assert(kListWarps * kListMaxGroup * (AWS + 2) * 4 <= OFF_PHYS, "merge scratch fits in the ring");
+
+    // Shared-memory offset of 16-byte piece q of token t of a tile.
+    __device__ __forceinline__ static uint32_t addr(int t, int q)
+    {
+        const int bx = t / BOX_TOK, r = t % BOX_TOK;
+        const int line = r / TPL, pc = (r % TPL) * PPT + q % PPT;
+        return bx * BOX_STRIDE + ((q / PPT) * BOX_LINES + line) * 128 + ((pc ^ (line & 7)) << 4);
+    }
 };
 
 // Stages entries [e0, e0 + part_blocks) of a (sequence, kv head) row's list:
@@ -59,7 +128,8 @@ struct ListStage {
 // sequence's blocks, with -1 only behind its last entry: so no block counts
 // twice and only the last entry can be partial.
 template <int BS>
-__device__ __forceinline__ int stage_list(const ListParams &p, ListStage *st, int seq, int kvh, int part, int L)
+__device__ __forceinline__ int stage_list(const ListParams &p, int32_t *phys, float *ks, float *vs, int seq, int kvh,
+                                          int part, int L)
 {
     const int nblk = (L + BS - 1) / BS;
     const int total = p.selected ? p.num_selected : nblk;
@@ -67,7 +137,7 @@ __device__ __forceinline__ int stage_list(const ListParams &p, ListStage *st, in
     const int32_t *sel = p.selected ? p.selected + ((int64_t)seq * p.num_kv_heads + kvh) * p.num_selected : nullptr;
     const int32_t *table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
     int bad = 0, tokens = 0;
-    for (int e = e0 + (int)threadIdx.x; e < e1; e += kListWarps * 32) {
+    for (int e = e0 + (int)threadIdx.x; e < e1; e += kListThreads) {
         int j = e;
         if (sel) {
             const int before = e > 0 ? sel[e - 1] : -1;
@@ -86,10 +156,10 @@ __device__ __forceinline__ int stage_list(const ListParams &p, ListStage *st, in
             bad = 1;
             b = 0;
         }
-        st->phys[e - e0] = b;
+        phys[e - e0] = b;
         if (p.k_scales) {
-            st->ks[e - e0] = p.k_scales[(int64_t)b * p.scale_stride + kvh];
-            st->vs[e - e0] = p.v_scales[(int64_t)b * p.scale_stride + kvh];
+            ks[e - e0] = p.k_scales[(int64_t)b * p.scale_stride + kvh];
+            vs[e - e0] = p.v_scales[(int64_t)b * p.scale_stride + kvh];
         }
         tokens = max(tokens, (e - e0) * BS + min(BS, L - j * BS));
     }
@@ -113,7 +183,7 @@ __device__ __forceinline__ int stage_list(const ListParams &p, ListStage *st, in
 template <int D>
 __device__ __forceinline__ void write_empty(const ListParams &p, int seq, int kvh, int part, bool refused)
 {
-    for (int i = threadIdx.x; i < p.group * D; i += kListWarps * 32) {
+    for (int i = threadIdx.x; i < p.group * D; i += kListThreads) {
         const int64_t sh = ((int64_t)seq * p.num_kv_heads + kvh) * p.group + i / D;
         if (p.np == 1) {
             store_out(p.out, p.out_dtype, sh * D + i % D, 0.f);
@@ -125,47 +195,292 @@ __device__ __forceinline__ void write_empty(const ListParams &p, int seq, int kv
     }
 }
 
-__device__ __forceinline__ float load_q(const ListParams &p, int64_t i)
-{
-    return p.q_dtype == PKV_F16 ? to_float(static_cast<const __half *>(p.q)[i])
-                                : to_float(static_cast<const __nv_bfloat16 *>(p.q)[i]);
-}
+// One warp's state: its rows of q, running maxima, sums and accumulators.
+// Lane (g, c) = (lane / 4, lane % 4).
+template <typename T, int D, int BS>
+struct ListEngine {
+    using C = ListCfg<T, D, BS>;
+    using M = typename ListElem<T>::M;
+    static constexpr int KS = C::KS;
 
-// D / 32 consecutive values of one row, from the cache's type to fp32.
-template <typename T, int N>
-__device__ __forceinline__ void load_row(const uint8_t *row, int lane, float (&x)[N])
-{
-    if constexpr (std::is_same<T, uint8_t>::value) {
+    uint32_t qf[KS][2];      // q^T B-fragments of head g
+    float o[KS][4];          // O^T C-fragments
+    float m[2], lsum[2];     // heads 2c, 2c + 1
+    float qs[2];             // score factors of heads 2c, 2c + 1
+    uint32_t koff[4], voff[4];   // this lane's ldmatrix offsets in a tile, 64 bytes of a row
+    int g, c;
+    bool lo;                 // weights in two 16-bit parts
+
+    __device__ __forceinline__ void init(const ListParams &p, int seq, int kvh, int lane)
+    {
+        g = lane >> 2;
+        c = lane & 3;
+        // A weight in f16 is off by 2^-12 of itself at most, less than the
+        // output's rounding to bfloat16; bfloat16 weights, and the other
+        // outputs, take a second part.
+        lo = !std::is_same<M, __half>::value || p.out_dtype != PKV_BF16;
+        const int tk = (lane & 7) + ((lane >> 3) & 1) * 8, dk = lane >> 4;
+        const int tv = C::Q8 ? tk : (lane & 7) + (lane >> 4) * 8, dv = C::Q8 ? dk : (lane >> 3) & 1;
 #pragma unroll
-        for (int k = 0; k < N; k += 2) {
-            const float2 f = float2_of_e4m3(*reinterpret_cast<const uint16_t *>(row + lane * N + k));
-            x[k] = f.x;
-            x[k + 1] = f.y;
+        for (int k = 0; k < 4; ++k) {
+            koff[k] = C::addr(tk, (2 * k + dk) % (C::CHUNKS * C::PPT));
+            voff[k] = C::addr(tv, (2 * k + dv) % (C::CHUNKS * C::PPT));
         }
-    } else {
+        const bool live = g < p.group;
+        const int64_t row = ((int64_t)seq * p.num_kv_heads + kvh) * p.group + (live ? g : 0);
+        const uint32_t *qp = reinterpret_cast<const uint32_t *>(p.q) + row * (D / 2);
+        float factor = p.qscale;
+        if constexpr (C::Q8) {
 #pragma unroll
-        for (int k = 0; k < N; k += 2) {
-            const float2 f = Unpack<T>::pair(reinterpret_cast<const uint32_t *>(row)[(lane * N + k) / 2]);
-            x[k] = f.x;
-            x[k + 1] = f.y;
+            for (int ks = 0; ks < KS; ++ks) {
+                const uint2 w = live ? *reinterpret_cast<const uint2 *>(qp + 8 * ks + 2 * c) : make_uint2(0u, 0u);
+                qf[ks][0] = w.x;
+                qf[ks][1] = w.y;
+            }
+            if (p.q_dtype == PKV_BF16) {
+                // bfloat16 to f16: the row's largest magnitude is brought to
+                // [2^14, 2^15) by a power of two, so that what f16 cannot
+                // hold is below 2^-38 of it
+                __nv_bfloat162 mx = as_pair<__nv_bfloat16>(0u);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    mx = __hmax2(mx, as_pair<__nv_bfloat16>(qf[ks][0] & 0x7fff7fffu));
+                    mx = __hmax2(mx, as_pair<__nv_bfloat16>(qf[ks][1] & 0x7fff7fffu));
+                }
+                const float2 f = Unpack<__nv_bfloat16>::pair(as_word(mx));
+                float a = fmaxf(f.x, f.y);
+                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+                int x = (int)(__float_as_uint(a) >> 23) - 127 - 14;
+                x = a < INFINITY ? max(x, -100) : 0;
+                const float down = __uint_as_float((uint32_t)(127 - x) << 23);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 v = Unpack<__nv_bfloat16>::pair(qf[ks][i]);
+                        qf[ks][i] = Mma<__half>::pack(v.x * down, v.y * down);
+                    }
+                }
+                factor *= __uint_as_float((uint32_t)(127 + x) << 23);
+            }
+        } else {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                qf[ks][0] = live ? qp[8 * ks + c] : 0u;
+                qf[ks][1] = live ? qp[8 * ks + c + 4] : 0u;
+            }
+        }
+        // head h's factor sits in lanes 4 h ..
+        qs[0] = __shfl_sync(0xffffffffu, factor, 8 * c);
+        qs[1] = __shfl_sync(0xffffffffu, factor, 8 * c + 4);
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt)
+            o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        lsum[0] = lsum[1] = 0.f;
+    }
+
+    // Byte offset of the chunk that holds 32 bytes group k of a row.
+    __device__ __forceinline__ static uint32_t chunk_off(int k) { return (uint32_t)((k >> 2) * C::BOX_LINES * 128); }
+
+    // A tile's tokens: rows 0..7 with scales ks0, vs0, rows 8..15 with ks1,
+    // vs1 (the same unless a block holds 8 tokens); nvalid of them count.
+    __device__ __forceinline__ void tile(uint32_t kbase, uint32_t vbase, int nvalid, int lane, float ks0, float ks1,
+                                         float vs0, float vs1)
+    {
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (C::Q8) {
+#pragma unroll
+            for (int j = 0; j < KS / 2; ++j) {
+                uint32_t w[4];
+                ldsm_x4(kbase + chunk_off(j) + koff[j & 3], w);
+                const uint32_t a0[4] = {f16x2_of_e4m3(w[0] & 0xffffu), f16x2_of_e4m3(w[1] & 0xffffu),
+                                        f16x2_of_e4m3(w[0] >> 16), f16x2_of_e4m3(w[1] >> 16)};
+                const uint32_t a1[4] = {f16x2_of_e4m3(w[2] & 0xffffu), f16x2_of_e4m3(w[3] & 0xffffu),
+                                        f16x2_of_e4m3(w[2] >> 16), f16x2_of_e4m3(w[3] >> 16)};
+                Mma<M>::run(s, a0, qf[2 * j][0], qf[2 * j][1]);
+                Mma<M>::run(s2, a1, qf[2 * j + 1][0], qf[2 * j + 1][1]);
+            }
+        } else {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t a[4];
+                ldsm_x4(kbase + chunk_off(ks) + koff[ks & 3], a);
+                Mma<M>::run(ks & 1 ? s2 : s, a, qf[ks][0], qf[ks][1]);
+            }
+        }
+
+        // Online softmax in the log2 domain; this lane holds tokens g, g + 8
+        // of heads 2c, 2c + 1.  While every score stays within kSlack of its
+        // head's reference m, the weights 2^(x - m) <= 2^kSlack are taken
+        // against it unchanged: no maximum across lanes, no rescaling.
+        constexpr float kSlack = 8.f;
+        const bool ok0 = g < nvalid, ok1 = g + 8 < nvalid;
+        float x0[2], x1[2], p0[2], p1[2];
+        bool over = false;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            x0[j] = ok0 ? (s[j] + s2[j]) * (qs[j] * ks0) : -INFINITY;
+            x1[j] = ok1 ? (s[2 + j] + s2[2 + j]) * (qs[j] * ks1) : -INFINITY;
+            over |= fmaxf(x0[j], x1[j]) > m[j] + kSlack;
+        }
+        if (__any_sync(0xffffffffu, over)) {
+            float alpha[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float tm = fmaxf(x0[j], x1[j]);
+                tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 4));
+                tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 8));
+                tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
+                const float mn = fmaxf(m[j], tm);
+                // no number yet: the sums are zero (or NaN), whatever alpha is
+                alpha[j] = ex2_fast(m[j] - fmaxf(mn, -1e30f));
+                lsum[j] *= alpha[j];
+                m[j] = mn;
+            }
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt) {
+                o[mt][0] *= alpha[0];
+                o[mt][1] *= alpha[1];
+                o[mt][2] *= alpha[0];
+                o[mt][3] *= alpha[1];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            // the finite stand-in keeps 2^(-inf - m) at 0; a NaN score stays NaN
+            const float mr = fmaxf(m[j], -1e30f);
+            p0[j] = ex2_fast(x0[j] - mr);
+            p1[j] = ex2_fast(x1[j] - mr);
+            lsum[j] += p0[j] + p1[j];
+        }
+
+        // Rows of V past the valid tokens may hold anything; zero them so that
+        // a weight of 0 leaves 0.
+        if (nvalid < C::TILE) {
+            constexpr int NPC = C::CHUNKS * C::PPT;
+            for (int i = lane; i < (C::TILE - nvalid) * NPC; i += 32)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vbase + C::addr(nvalid + i / NPC, i % NPC)),
+                             "r"(0u)
+                             : "memory");
+            __syncwarp();
+        }
+
+        const uint32_t h0 = Mma<M>::pack(p0[0], p0[1]), h1 = Mma<M>::pack(p1[0], p1[1]);
+        const uint32_t bh0 = movmatrix_trans(h0), bh1 = movmatrix_trans(h1);
+        uint32_t bl0 = 0u, bl1 = 0u;
+        if (lo) {
+            const float2 f0 = Mma<M>::unpack(h0), f1 = Mma<M>::unpack(h1);
+            bl0 = movmatrix_trans(Mma<M>::pack(p0[0] - f0.x, p0[1] - f0.y));
+            bl1 = movmatrix_trans(Mma<M>::pack(p1[0] - f1.x, p1[1] - f1.y));
+        }
+        if constexpr (C::Q8) {
+#pragma unroll
+            for (int j = 0; j < KS / 2; ++j) {
+                uint32_t w[4];
+                ldsm_x4_trans(vbase + chunk_off(j) + voff[j & 3], w);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t u = __byte_perm(w[2 * i], 0, 0x3120), v = __byte_perm(w[2 * i + 1], 0, 0x3120);
+                    const uint32_t a[4] = {f16x2_of_e4m3(u & 0xffffu), f16x2_of_e4m3(u >> 16),
+                                           f16x2_of_e4m3(v & 0xffffu), f16x2_of_e4m3(v >> 16)};
+                    float t[4] = {0.f, 0.f, 0.f, 0.f};
+                    float *acc = o[2 * j + i];
+                    if constexpr (BS == 8) {
+                        mma_k8(t, a[0], a[1], bh0);
+                        if (lo)
+                            mma_k8(t, a[0], a[1], bl0);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            acc[k] = fmaf(vs0, t[k], acc[k]);
+                            t[k] = 0.f;
+                        }
+                        mma_k8(t, a[2], a[3], bh1);
+                        if (lo)
+                            mma_k8(t, a[2], a[3], bl1);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            acc[k] = fmaf(vs1, t[k], acc[k]);
+                    } else {
+                        Mma<M>::run(t, a, bh0, bh1);
+                        if (lo)
+                            Mma<M>::run(t, a, bl0, bl1);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            acc[k] = fmaf(vs0, t[k], acc[k]);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt) {
+                uint32_t a[4];
+                ldsm_x4_trans(vbase + chunk_off(mt) + voff[mt & 3], a);
+                Mma<M>::run(o[mt], a, bh0, bh1);
+                if (lo)
+                    Mma<M>::run(o[mt], a, bl0, bl1);
+            }
         }
     }
-}
 
-// T: __half, __nv_bfloat16, or uint8_t for an e4m3 cache.  One warp takes a
-// token at a time, a lane D / 32 of its dimensions.
+    // D = A * B + D, m16n8k8, f16.
+    __device__ __forceinline__ static void mma_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b)
+    {
+        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(b));
+    }
+
+    // This warp's (max, sum, sums of values) of the heads below `group` into
+    // the merge scratch.
+    __device__ __forceinline__ void finish(float *mw, float *lw, float *aw, int warp, int group)
+    {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float l = lsum[j];
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            const int row = 2 * c + j;
+            if (row < group) {
+                if (g == 0) {
+                    mw[warp * kListMaxGroup + row] = m[j];
+                    lw[warp * kListMaxGroup + row] = l;
+                }
+                float *dst = aw + (warp * kListMaxGroup + row) * C::AWS;
+#pragma unroll
+                for (int mt = 0; mt < KS; ++mt) {
+                    if constexpr (C::Q8) {
+                        *reinterpret_cast<float2 *>(dst + 16 * mt + 2 * g) = make_float2(o[mt][j], o[mt][2 + j]);
+                    } else {
+                        dst[16 * mt + g] = o[mt][j];
+                        dst[16 * mt + g + 8] = o[mt][2 + j];
+                    }
+                }
+            }
+        }
+    }
+};
+
+// T: __half, __nv_bfloat16, or uint8_t for an e4m3 cache.  Grid (partition,
+// kv head, sequence).
 template <typename T, int D, int BS>
-__global__ void __launch_bounds__(kListWarps * 32)
-list_attention_kernel(const __grid_constant__ ListParams p)
+__global__ void __launch_bounds__(kListThreads, 3)
+list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv)
 {
-    constexpr bool Q8 = std::is_same<T, uint8_t>::value;
-    constexpr int N = D / 32;
-    constexpr int MG = kListMaxGroup;
-    __shared__ ListStage st;
-    __shared__ float s_m[kListWarps][MG], s_l[kListWarps][MG];
-    __shared__ float s_acc[kListWarps][MG][D];
+    using C = ListCfg<T, D, BS>;
+    constexpr int S = C::S, TILE = C::TILE, NW = kListWarps;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = aligned_smem(smem_raw);
+    int32_t *phys = reinterpret_cast<int32_t *>(smem + C::OFF_PHYS);
+    float *ks_s = reinterpret_cast<float *>(smem + C::OFF_KS);
+    float *vs_s = reinterpret_cast<float *>(smem + C::OFF_VS);
     const int part = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + warp * S;
+    uint32_t *flag = reinterpret_cast<uint32_t *>(smem + C::OFF_FLAG);
     const int L = p.context_lens[seq];
     if (L < 0 || L > p.max_context_len) {
         if (part == 0 && kvh == 0 && threadIdx.x == 0)
@@ -173,118 +488,217 @@ list_attention_kernel(const __grid_constant__ ListParams p)
         write_empty<D>(p, seq, kvh, part, true);
         return;
     }
-    const int tokens = stage_list<BS>(p, &st, seq, kvh, part, L);
+    if (lane == 0) {
+        for (int s = 0; s < S; ++s)
+            mbar_init(&bars[s], 1);
+        fence_mbar_init();
+    }
+    if (threadIdx.x == 0) {
+        *flag = 0;
+        prefetch_tensormap(&tmk);
+        prefetch_tensormap(&tmv);
+    }
+    const int tokens = stage_list<BS>(p, phys, ks_s, vs_s, seq, kvh, part, L);
     if (tokens <= 0) {
         write_empty<D>(p, seq, kvh, part, tokens < 0);
         return;
     }
-    const int64_t head0 = ((int64_t)seq * p.num_kv_heads + kvh) * p.group;
-    float q[MG][N], acc[MG][N], m[MG], l[MG];
-#pragma unroll
-    for (int g = 0; g < MG; ++g) {
-        m[g] = -INFINITY;
-        l[g] = 0.f;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            q[g][k] = g < p.group ? load_q(p, (head0 + g) * D + lane * N + k) * p.qscale : 0.f;
-            acc[g][k] = 0.f;
+
+    // ---- this warp's tiles: warp, warp + NW, ...
+    const int ntiles = (tokens + TILE - 1) / TILE;
+    const int my_n = warp < ntiles ? (ntiles - 1 - warp) / NW + 1 : 0;
+    uint8_t *stages = smem + warp * S * C::STAGE_BYTES;
+    auto issue = [&](int i, int st) {
+        const int t0 = (warp + i * NW) * TILE;
+        uint8_t *kd = stages + st * C::STAGE_BYTES, *vd = kd + C::TILE_BYTES;
+        const int nbox = min(C::BOXES, (tokens - t0 + C::BOX_TOK - 1) / C::BOX_TOK);
+        mbar_arrive_expect_tx(&bars[st], (uint32_t)(nbox * 2 * C::BOX_BYTES));
+        for (int b = 0; b < nbox; ++b) {
+            const int tok = t0 + b * C::BOX_TOK;
+            const int blk = phys[tok / BS], line = (tok % BS) / C::TPL;
+            tma_load_5d(kd + b * C::BOX_STRIDE, &tmk, &bars[st], 0, line, 0, kvh, blk);
+            tma_load_5d(vd + b * C::BOX_STRIDE, &tmv, &bars[st], 0, line, 0, kvh, blk);
         }
+    };
+    if (lane == 0) {
+        for (int i = 0; i < min(my_n, S); ++i)
+            issue(i, i);
     }
-    constexpr int ROW = D * (Q8 ? 1 : 2);
-    for (int t = warp; t < tokens; t += kListWarps) {
-        const int64_t row = ((int64_t)st.phys[t / BS] * p.num_kv_heads + kvh) * BS + t % BS;
-        float k[N], v[N];
-        load_row<T, N>(p.k_cache + row * ROW, lane, k);
-        load_row<T, N>(p.v_cache + row * ROW, lane, v);
-        const float ks = Q8 ? st.ks[t / BS] : 1.f, vs = Q8 ? st.vs[t / BS] : 1.f;
-#pragma unroll
-        for (int g = 0; g < MG; ++g) {
-            if (g < p.group) {
-                float s = 0.f;
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    s = fmaf(q[g][i], k[i], s);
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1)
-                    s += __shfl_xor_sync(0xffffffffu, s, off);
-                s *= ks;
-                const float mn = fmaxf(m[g], s);
-                const float a = mn == -INFINITY ? 1.f : exp2f(m[g] - mn);
-                // a NaN score stays one, also before any number has come
-                const float e = s == -INFINITY ? 0.f : exp2f(s - (mn == -INFINITY ? 0.f : mn));
-                m[g] = mn;
-                l[g] = l[g] * a + e;
-                const float ev = e * vs;
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    acc[g][i] = acc[g][i] * a + ev * v[i];
+    ListEngine<T, D, BS> eng;
+    eng.init(p, seq, kvh, lane);
+
+    int failed_at = -1;
+    for (int i = 0; i < my_n; ++i) {
+        const int st = i % S;
+        if (!mbar_wait_bounded(&bars[st], (uint32_t)((i / S) & 1))) {
+            failed_at = i;
+            break;
+        }
+        const int t0 = (warp + i * NW) * TILE;
+        const int nvalid = min(TILE, tokens - t0);
+        const uint32_t kbase = smem_u32(stages + st * C::STAGE_BYTES);
+        float ks0 = 1.f, ks1 = 1.f, vs0 = 1.f, vs1 = 1.f;
+        if constexpr (C::Q8) {
+            const int e = t0 / BS;
+            ks0 = ks1 = ks_s[e];
+            vs0 = vs1 = vs_s[e];
+            if constexpr (BS == 8) {
+                // a second block that is not there weighs nothing
+                ks1 = nvalid > 8 ? ks_s[e + 1] : 0.f;
+                vs1 = nvalid > 8 ? vs_s[e + 1] : 0.f;
             }
         }
+        eng.tile(kbase, kbase + C::TILE_BYTES, nvalid, lane, ks0, ks1, vs0, vs1);
+        __syncwarp();
+        if (lane == 0 && i + S < my_n) {
+            fence_proxy_async_smem();
+            issue(i + S, st);
+        }
     }
-#pragma unroll
-    for (int g = 0; g < MG; ++g) {
+    if (failed_at >= 0) {
+        // no CTA leaves with loads in flight
+        for (int i = failed_at; i < min(my_n, failed_at + S); ++i)
+            drain_wait(&bars[i % S], (uint32_t)((i / S) & 1), p.status);
         if (lane == 0) {
-            s_m[warp][g] = m[g];
-            s_l[warp][g] = l[g];
+            report(p.status, PKV_DEV_TIMEOUT);
+            atomicOr(flag, 1u);
         }
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            s_acc[warp][g][lane * N + i] = acc[g][i];
     }
+
+    // ---- the warps' parts, through the rings' memory
     __syncthreads();
-    for (int i = threadIdx.x; i < p.group * D; i += kListWarps * 32) {
-        const int g = i / D, d = i % D;
-        float M = -INFINITY, num = 0.f, den = 0.f;
+    const bool failed = *reinterpret_cast<volatile uint32_t *>(flag) != 0;
+    float *mw = reinterpret_cast<float *>(smem);
+    float *lw = mw + NW * kListMaxGroup;
+    float *aw = lw + NW * kListMaxGroup;
+    eng.finish(mw, lw, aw, warp, p.group);
+    __syncthreads();
+    const int64_t head0 = ((int64_t)seq * p.num_kv_heads + kvh) * p.group;
+    for (int i = threadIdx.x; i < p.group * D; i += kListThreads) {
+        const int r = i / D, d = i % D;
+        float Mx = -INFINITY, num = 0.f, den = 0.f;
 #pragma unroll
-        for (int w = 0; w < kListWarps; ++w)
-            M = fmaxf(M, s_m[w][g]);
+        for (int w = 0; w < NW; ++w)
+            Mx = fmaxf(Mx, mw[w * kListMaxGroup + r]);
+        const float ref = fmaxf(Mx, -1e30f);
 #pragma unroll
-        for (int w = 0; w < kListWarps; ++w) {
-            if (s_m[w][g] != -INFINITY || s_l[w][g] != 0.f) {
-                const float f = exp2f(s_m[w][g] - M);
-                num += f * s_acc[w][g][d];
-                den += f * s_l[w][g];
-            }
+        for (int w = 0; w < NW; ++w) {
+            const float f = exp2f(mw[w * kListMaxGroup + r] - ref);   // 0 for a warp without tokens; NaN sums stay
+            num += f * aw[(w * kListMaxGroup + r) * C::AWS + d];
+            den += f * lw[w * kListMaxGroup + r];
         }
         if (p.np == 1) {
-            store_out(p.out, p.out_dtype, (head0 + g) * D + d, den == 0.f ? 0.f : num / den);
+            store_out(p.out, p.out_dtype, (head0 + r) * D + d, failed || den == 0.f ? 0.f : num / den);
         } else {
-            const int64_t slot = (head0 + g) * p.np + part;
+            const int64_t slot = (head0 + r) * p.np + part;
             p.ws_acc[slot * D + d] = num;
             if (d == 0) {
-                p.ws_ml[slot * 2 + 0] = M;
-                p.ws_ml[slot * 2 + 1] = den;
+                p.ws_ml[slot * 2 + 0] = Mx;
+                p.ws_ml[slot * 2 + 1] = failed ? -1.f : den;
             }
         }
     }
+    if (p.np > 1)
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// One CTA per (sequence, head), a thread per dimension: the log-sum-exp merge
-// of the np partials.  A sum of -1 marks a refused partition: the row is zero.
+// One CTA per (sequence, head): the log-sum-exp merge of the np partials,
+// launched as a programmatic dependent of the partitions' kernel.  Warp w
+// takes partials w, w + 8, ...; a lane holds D / 32 dimensions.  A sum of -1
+// marks a refused partition: the row is zero.
+constexpr int kMergeWarps = 8;
+
 template <int D>
-__global__ void __launch_bounds__(D)
+__global__ void __launch_bounds__(kMergeWarps * 32)
 list_merge_kernel(const __grid_constant__ ListParams p)
 {
+    constexpr int N = D / 32, U = 4;
+    using V = typename std::conditional<N == 4, float4, float2>::type;
+    __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
+    __shared__ int s_bad[kMergeWarps];
+    __shared__ float s_acc[kMergeWarps][D];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t sh = blockIdx.x;
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml) + sh * p.np;
-    const float *acc = p.ws_acc + sh * p.np * D + threadIdx.x;
-    float M = -INFINITY;
-    bool refused = false;
-    for (int k = 0; k < p.np; ++k) {
-        const float2 t = ml[k];
-        M = fmaxf(M, t.x);
-        refused |= t.y < 0.f;
-    }
-    float num = 0.f, den = 0.f;
-    for (int k = 0; k < p.np; ++k) {
-        const float2 t = ml[k];
-        if (t.y != 0.f) {
-            const float f = exp2f(t.x - M);
-            num += f * acc[(int64_t)k * D];
-            den += f * t.y;
+    const float *acc = p.ws_acc + sh * p.np * D + lane * N;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float mx = -INFINITY, den = 0.f, num[N];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        num[i] = 0.f;
+    for (int k0 = warp; k0 < p.np; k0 += kMergeWarps * U) {
+        float2 t[U];
+        float a[U][N];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = k0 + u * kMergeWarps;
+            t[u] = k < p.np ? __ldcg(ml + k) : make_float2(-INFINITY, 0.f);
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = k0 + u * kMergeWarps;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                a[u][i] = 0.f;
+            if (t[u].y != 0.f && !(t[u].y < 0.f)) {   // a partial of sum 0 was not written
+                const V v = __ldcg(reinterpret_cast<const V *>(acc + k * D));
+                a[u][0] = v.x;
+                a[u][1] = v.y;
+                if constexpr (N == 4) {
+                    a[u][2] = v.z;
+                    a[u][3] = v.w;
+                }
+            }
+        }
+        float mn = mx;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            mn = fmaxf(mn, t[u].x);
+            bad |= t[u].y < 0.f;
+        }
+        const float ref = fmaxf(mn, -1e30f);
+        const float f0 = exp2f(mx - ref);
+        den *= f0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            num[i] *= f0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float f = exp2f(t[u].x - ref);
+            den += f * t[u].y;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                num[i] += f * a[u][i];
+        }
+        mx = mn;
     }
-    store_out(p.out, p.out_dtype, sh * D + threadIdx.x, refused || den == 0.f ? 0.f : num / den);
+    if (lane == 0) {
+        s_m[warp] = mx;
+        s_l[warp] = den;
+        s_bad[warp] = bad;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        s_acc[warp][lane * N + i] = num[i];
+    __syncthreads();
+    if (threadIdx.x < D) {
+        float M = -INFINITY, n = 0.f, d = 0.f;
+        bool zero = false;
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) {
+            M = fmaxf(M, s_m[w]);
+            zero |= s_bad[w] != 0;
+        }
+        const float ref = fmaxf(M, -1e30f);
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) {
+            const float f = exp2f(s_m[w] - ref);
+            n += f * s_acc[w][threadIdx.x];
+            d += f * s_l[w];
+        }
+        store_out(p.out, p.out_dtype, sh * D + threadIdx.x, zero || d == 0.f ? 0.f : n / d);
+    }
 }
 
 }  // namespace pkv
