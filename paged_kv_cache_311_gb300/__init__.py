@@ -577,51 +577,67 @@ def q8_scales(num_blocks: int, num_kv_heads: int, device=None) -> torch.Tensor:
     return torch.zeros(num_blocks, -(-num_kv_heads // 4) * 4, dtype=torch.float32, device=device)
 
 
-def _ready(named: dict) -> torch.device:
-    """Every tensor (None: absent) on one CUDA device and contiguous -> that device."""
-    dev = None
-    for name, t in named.items():
-        if t is None:
-            continue
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, other arguments on {dev}")
-    return dev
+# The current device and a device's current stream as plain numbers: the calls
+# below are made once per layer and step, and torch.cuda.current_stream() alone
+# costs more than a small kernel's launch.
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _launch(fn, what: str, dev: torch.device, stream, args: tuple) -> None:
+def _ready(names: str, *tensors: Optional[torch.Tensor]) -> int:
+    """Every tensor (None: absent) contiguous and on one CUDA device -> its
+    index.  names: the tensors' names, for the error."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or not t.is_contiguous() or t.get_device() != index):
+            name = names.split()[next(i for i, x in enumerate(tensors) if x is t)]
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous CUDA tensor")
+            raise ValueError(f"{name} is on {t.device}, other arguments on {tensors[0].device}")
+    return index
+
+
+def _launch(fn, what: str, index: int, stream, *args) -> None:
     """fn(*args, stream) with the tensors' device current; stream None: that
     device's current stream."""
-    if torch.cuda.current_device() != dev.index:
-        with torch.cuda.device(dev):
-            return _launch(fn, what, dev, stream, args)
-    rc = fn(*args, _stream(stream))
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return _launch(fn, what, index, stream, *args)
+    if stream is None:
+        stream = _current_raw_stream(index)
+    else:
+        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    rc = fn(*args, stream)
     if rc != 0:
         raise PkvError(rc, what)
 
 
+def _address(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
 def _status_arg(t: Optional[torch.Tensor]):
-    if t is not None and (t.numel() < 1 or t.element_size() != 4 or t.is_floating_point()):
+    if t is None:
+        return None
+    if t.numel() < 1 or t.element_size() != 4 or t.is_floating_point():
         raise ValueError("device_status must be an int32 or uint32 tensor")
-    return _ptr(t)
+    return t.data_ptr()
 
 
 def _tables(block_tables: torch.Tensor, context_lens: torch.Tensor, B: int) -> int:
     """Checks the tables and lengths of B sequences -> table entries per sequence."""
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
         raise ValueError("block_tables and context_lens must be int32")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
+    shape = block_tables.shape
+    if len(shape) != 2 or shape[0] != B or context_lens.shape != (B,):
         raise ValueError("block_tables must be [B, MB] and context_lens [B]")
-    return int(block_tables.shape[1])
+    return shape[1]
 
 
-def _q8_scale_args(k_cache: torch.Tensor, *scales: torch.Tensor) -> None:
-    NB, Hk = k_cache.shape[:2]
+def _q8_scale_args(NB: int, Hk: int, *scales: torch.Tensor) -> None:
     for s in scales:
-        if s.dtype != torch.float32 or tuple(s.shape) != (NB, -(-Hk // 4) * 4):
+        if s.dtype != torch.float32 or s.shape != (NB, (Hk + 3) // 4 * 4):
             raise ValueError("scales must be float32 [num_blocks, num_kv_heads rounded up to a multiple of 4]")
 
 
@@ -629,7 +645,7 @@ def _new_tokens(query_start: Optional[torch.Tensor], B: int, T: int) -> None:
     if query_start is None:
         if T != B:
             raise ValueError("without query_start every sequence has one new token")
-    elif query_start.dtype != torch.int32 or tuple(query_start.shape) != (B + 1,):
+    elif query_start.dtype != torch.int32 or query_start.shape != (B + 1,):
         raise ValueError("query_start must be int32 [B + 1]")
 
 
@@ -647,25 +663,26 @@ def append_cache_q8(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tenso
     block's scale grows with its rows; rows it holds are then rescaled.  Blocks
     shared by sequences are copied first (copy_blocks on the caches and on the
     scales)."""
-    dev = _ready(dict(key=key, value=value, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
-                      v_scales=v_scales, block_tables=block_tables, context_lens=context_lens,
-                      query_start=query_start, device_status=device_status))
-    T, Hk, D = key.shape
-    NB, Hk2, bs, D2 = k_cache.shape
-    if (Hk2, D2) != (Hk, D) or value.shape != key.shape or v_cache.shape != k_cache.shape:
+    index = _ready("key value k_cache v_cache k_scales v_scales block_tables context_lens query_start device_status",
+                   key, value, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, query_start,
+                   device_status)
+    T, Hk, D = shape = key.shape
+    NB, Hk2, bs, D2 = cache_shape = k_cache.shape
+    if Hk2 != Hk or D2 != D or value.shape != shape or v_cache.shape != cache_shape:
         raise ValueError("shape mismatch")
-    if key.dtype not in _DTYPE or value.dtype != key.dtype:
+    dtype = _DTYPE.get(key.dtype)
+    if dtype is None or value.dtype != key.dtype:
         raise ValueError("key and value must share a floating dtype")
     if k_cache.dtype != torch.float8_e4m3fn or v_cache.dtype != torch.float8_e4m3fn:
         raise ValueError("k_cache and v_cache must be float8_e4m3fn")
-    _q8_scale_args(k_cache, k_scales, v_scales)
-    B = int(context_lens.shape[0])
+    _q8_scale_args(NB, Hk, k_scales, v_scales)
+    B = context_lens.numel()
     MB = _tables(block_tables, context_lens, B)
     _new_tokens(query_start, B, T)
-    _launch(load_library().pkv_append_cache_q8, "pkv_append_cache_q8", dev, stream, (
-        _ptr(key), _ptr(value), _DTYPE[key.dtype], _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
-        _ptr(v_scales), _ptr(block_tables), MB, _ptr(context_lens), _ptr(query_start), B, T, Hk, D, bs,
-        NB, _status_arg(device_status)))
+    _launch((_lib or load_library()).pkv_append_cache_q8, "pkv_append_cache_q8", index, stream,
+            key.data_ptr(), value.data_ptr(), dtype, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
+            v_scales.data_ptr(), block_tables.data_ptr(), MB, context_lens.data_ptr(), _address(query_start), B, T,
+            Hk, D, bs, NB, _status_arg(device_status))
 
 
 def summarize_blocks(k_cache: torch.Tensor, summaries: torch.Tensor, block_tables: torch.Tensor,
@@ -679,30 +696,30 @@ def summarize_blocks(k_cache: torch.Tensor, summaries: torch.Tensor, block_table
 
     summaries: [NB, Hk, 2, D] of the cache's dtype, bfloat16 for an 8-bit cache
     (k_cache float8_e4m3fn, with its k_scales)."""
-    dev = _ready(dict(k_cache=k_cache, summaries=summaries, block_tables=block_tables,
-                      context_lens=context_lens, query_start=query_start, k_scales=k_scales,
-                      device_status=device_status))
+    index = _ready("k_cache summaries block_tables context_lens query_start k_scales device_status", k_cache, summaries,
+                   block_tables, context_lens, query_start, k_scales, device_status)
     NB, Hk, bs, D = k_cache.shape
     q8 = k_cache.dtype == torch.float8_e4m3fn
-    if not q8 and k_cache.dtype not in _DTYPE:
+    dtype = PKV_E4M3 if q8 else _DTYPE.get(k_cache.dtype)
+    if dtype is None:
         raise ValueError("k_cache must be float16, bfloat16 or float8_e4m3fn")
     if q8 != (k_scales is not None):
         raise ValueError("k_scales go with a float8_e4m3fn cache")
     if q8:
-        _q8_scale_args(k_cache, k_scales)
-    if tuple(summaries.shape) != (NB, Hk, 2, D) or summaries.dtype != (torch.bfloat16 if q8 else k_cache.dtype):
+        _q8_scale_args(NB, Hk, k_scales)
+    if summaries.shape != (NB, Hk, 2, D) or summaries.dtype != (torch.bfloat16 if q8 else k_cache.dtype):
         raise ValueError("summaries must be [NB, Hk, 2, D] of the cache's dtype (bfloat16 for an 8-bit cache)")
-    B = int(context_lens.shape[0])
+    B = context_lens.numel()
     MB = _tables(block_tables, context_lens, B)
     if num_tokens is None:
         if query_start is not None:
             raise ValueError("query_start needs num_tokens")
         num_tokens = B
     _new_tokens(query_start, B, num_tokens)
-    _launch(load_library().pkv_summarize_blocks, "pkv_summarize_blocks", dev, stream, (
-        _ptr(k_cache), PKV_E4M3 if q8 else _DTYPE[k_cache.dtype], _ptr(k_scales), _ptr(summaries),
-        _DTYPE[summaries.dtype], _ptr(block_tables), MB, _ptr(context_lens), _ptr(query_start), B,
-        int(num_tokens), Hk, D, bs, NB, _status_arg(device_status)))
+    _launch((_lib or load_library()).pkv_summarize_blocks, "pkv_summarize_blocks", index, stream,
+            k_cache.data_ptr(), dtype, _address(k_scales), summaries.data_ptr(), PKV_BF16 if q8 else dtype,
+            block_tables.data_ptr(), MB, context_lens.data_ptr(), _address(query_start), B, int(num_tokens), Hk, D, bs,
+            NB, _status_arg(device_status))
     return summaries
 
 
@@ -718,22 +735,23 @@ def select_blocks(selected: torch.Tensor, q: torch.Tensor, summaries: torch.Tens
     selected: int32 [B, Hk, K]; q: [B, H, D]; summaries: [NB, Hk, 2, D], both
     float16 or bfloat16.  max_context_len: host bound of context_lens (what the
     table can hold if omitted)."""
-    dev = _ready(dict(selected=selected, q=q, summaries=summaries, block_tables=block_tables,
-                      context_lens=context_lens, device_status=device_status))
+    index = _ready("selected q summaries block_tables context_lens device_status", selected, q, summaries, block_tables,
+                   context_lens, device_status)
     B, H, D = q.shape
     NB, Hk, two, D2 = summaries.shape
-    if two != 2 or D2 != D or selected.dim() != 3 or tuple(selected.shape[:2]) != (B, Hk):
+    out_shape = selected.shape
+    if two != 2 or D2 != D or len(out_shape) != 3 or out_shape[:2] != (B, Hk):
         raise ValueError("shape mismatch")
-    if selected.dtype != torch.int32 or q.dtype not in _DTYPE or summaries.dtype not in _DTYPE:
+    q_dtype, s_dtype = _DTYPE.get(q.dtype), _DTYPE.get(summaries.dtype)
+    if selected.dtype != torch.int32 or q_dtype is None or s_dtype is None:
         raise ValueError("selected must be int32, q and summaries floating")
     MB = _tables(block_tables, context_lens, B)
     if max_context_len is None:
         max_context_len = MB * block_size
-    _launch(load_library().pkv_select_blocks, "pkv_select_blocks", dev, stream, (
-        _ptr(selected), _ptr(q), _DTYPE[q.dtype], _ptr(summaries), _DTYPE[summaries.dtype],
-        _ptr(block_tables), MB, _ptr(context_lens), B, H, Hk, D, int(block_size), NB,
-        int(max_context_len), int(selected.shape[2]), int(keep_first), int(keep_last),
-        _status_arg(device_status)))
+    _launch((_lib or load_library()).pkv_select_blocks, "pkv_select_blocks", index, stream,
+            selected.data_ptr(), q.data_ptr(), q_dtype, summaries.data_ptr(), s_dtype, block_tables.data_ptr(), MB,
+            context_lens.data_ptr(), B, H, Hk, D, int(block_size), NB, int(max_context_len), out_shape[2],
+            int(keep_first), int(keep_last), _status_arg(device_status))
     return selected
 
 
@@ -746,31 +764,33 @@ def paged_attention_list_workspace_bytes(num_seqs: int, num_heads: int, num_kv_h
         num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_list_blocks, partition_size))
 
 
-def _list_workspace(workspace, dev, stream, *sizes):
+def _list_workspace(workspace, index: int, stream, *sizes):
     """The caller's workspace, or one allocated here for the stream that uses it
-    -> (tensor or None, bytes)."""
+    -> (tensor or None, address, bytes)."""
     if workspace is not None:
-        return workspace, workspace.numel() * workspace.element_size()
-    with torch.cuda.device(dev):
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    with torch.cuda.device(index):
         nbytes = paged_attention_list_workspace_bytes(*sizes)
     if not nbytes:
-        return None, 0
-    workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return None, None, 0
+    device = torch.device("cuda", index)
+    workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
     if stream is not None:
         # the allocator must not hand it out again before that stream is done with it
         workspace.record_stream(stream if hasattr(stream, "cuda_stream")
-                                else torch.cuda.ExternalStream(int(stream), device=dev))
-    return workspace, nbytes
+                                else torch.cuda.ExternalStream(int(stream), device=device))
+    return workspace, workspace.data_ptr(), nbytes
 
 
 def _decode_shapes(out, q, k_cache, v_cache) -> tuple:
-    B, H, D = q.shape
-    NB, Hk, bs, D2 = k_cache.shape
-    if D2 != D or v_cache.shape != k_cache.shape or out.shape != q.shape:
+    B, H, D = shape = q.shape
+    NB, Hk, bs, D2 = cache_shape = k_cache.shape
+    if D2 != D or v_cache.shape != cache_shape or out.shape != shape:
         raise ValueError("shape mismatch")
-    if out.dtype not in _DTYPE or q.dtype not in _DTYPE:
+    out_dtype, q_dtype = _DTYPE.get(out.dtype), _DTYPE.get(q.dtype)
+    if out_dtype is None or q_dtype is None:
         raise ValueError("q and out must be floating")
-    return B, H, D, NB, Hk, bs
+    return B, H, D, NB, Hk, bs, out_dtype, q_dtype
 
 
 def paged_attention_decode_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -785,23 +805,20 @@ def paged_attention_decode_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torch
     max_context_len: host bound of context_lens (what the table can hold if
     omitted).  workspace: paged_attention_list_workspace_bytes, allocated here
     if needed and not given."""
-    dev = _ready(dict(out=out, q=q, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
-                      block_tables=block_tables, context_lens=context_lens, workspace=workspace,
-                      device_status=device_status))
-    B, H, D, NB, Hk, bs = _decode_shapes(out, q, k_cache, v_cache)
+    index = _ready("out q k_cache v_cache k_scales v_scales block_tables context_lens workspace device_status", out, q,
+                   k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, workspace, device_status)
+    B, H, D, NB, Hk, bs, out_dtype, q_dtype = _decode_shapes(out, q, k_cache, v_cache)
     if k_cache.dtype != torch.float8_e4m3fn or v_cache.dtype != torch.float8_e4m3fn:
         raise ValueError("k_cache and v_cache must be float8_e4m3fn")
-    _q8_scale_args(k_cache, k_scales, v_scales)
+    _q8_scale_args(NB, Hk, k_scales, v_scales)
     MB = _tables(block_tables, context_lens, B)
-    if max_context_len is None:
-        max_context_len = MB * bs
-    workspace, nbytes = _list_workspace(workspace, dev, stream, B, H, Hk, D, bs,
-                                        -(-int(max_context_len) // bs), partition_size)
-    _launch(load_library().pkv_paged_attention_decode_q8, "pkv_paged_attention_decode_q8", dev, stream, (
-        _ptr(out), _DTYPE[out.dtype], _ptr(q), _DTYPE[q.dtype], _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
-        _ptr(v_scales), _ptr(block_tables), MB, _ptr(context_lens), B, H, Hk, D, bs, NB,
-        int(max_context_len), float(scale), int(partition_size), _ptr(workspace), nbytes,
-        _status_arg(device_status)))
+    max_context_len = MB * bs if max_context_len is None else int(max_context_len)
+    workspace, ws, nbytes = _list_workspace(workspace, index, stream, B, H, Hk, D, bs, (max_context_len + bs - 1) // bs,
+                                            partition_size)
+    _launch((_lib or load_library()).pkv_paged_attention_decode_q8, "pkv_paged_attention_decode_q8", index, stream,
+            out.data_ptr(), out_dtype, q.data_ptr(), q_dtype, k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), MB, context_lens.data_ptr(), B, H, Hk, D,
+            bs, NB, max_context_len, scale, partition_size, ws, nbytes, _status_arg(device_status))
     return out
 
 
@@ -818,25 +835,26 @@ def paged_attention_decode_selected(out: torch.Tensor, q: torch.Tensor, k_cache:
 
     q, k_cache, v_cache share float16 or bfloat16, or the caches are
     float8_e4m3fn with their k_scales and v_scales."""
-    dev = _ready(dict(out=out, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                      context_lens=context_lens, selected=selected, k_scales=k_scales, v_scales=v_scales,
-                      workspace=workspace, device_status=device_status))
-    B, H, D, NB, Hk, bs = _decode_shapes(out, q, k_cache, v_cache)
+    index = _ready("out q k_cache v_cache block_tables context_lens selected k_scales v_scales workspace device_status",
+                   out, q, k_cache, v_cache, block_tables, context_lens, selected, k_scales, v_scales, workspace,
+                   device_status)
+    B, H, D, NB, Hk, bs, out_dtype, q_dtype = _decode_shapes(out, q, k_cache, v_cache)
     q8 = k_cache.dtype == torch.float8_e4m3fn
     if v_cache.dtype != k_cache.dtype or (not q8 and k_cache.dtype != q.dtype):
         raise ValueError("q, k_cache and v_cache must share a dtype, or the caches be float8_e4m3fn")
     if (k_scales is not None) != q8 or (v_scales is not None) != q8:
         raise ValueError("k_scales and v_scales go with float8_e4m3fn caches")
     if q8:
-        _q8_scale_args(k_cache, k_scales, v_scales)
-    if selected.dtype != torch.int32 or selected.dim() != 3 or tuple(selected.shape[:2]) != (B, Hk):
+        _q8_scale_args(NB, Hk, k_scales, v_scales)
+    list_shape = selected.shape
+    if selected.dtype != torch.int32 or len(list_shape) != 3 or list_shape[:2] != (B, Hk):
         raise ValueError("selected must be int32 [B, Hk, K]")
+    K = list_shape[2]
     MB = _tables(block_tables, context_lens, B)
-    K = int(selected.shape[2])
-    workspace, nbytes = _list_workspace(workspace, dev, stream, B, H, Hk, D, bs, K, partition_size)
-    _launch(load_library().pkv_paged_attention_decode_selected, "pkv_paged_attention_decode_selected", dev, stream, (
-        _ptr(out), _DTYPE[out.dtype], _ptr(q), _DTYPE[q.dtype], _ptr(k_cache), _ptr(v_cache),
-        PKV_E4M3 if q8 else _DTYPE[k_cache.dtype], _ptr(k_scales), _ptr(v_scales), _ptr(block_tables), MB,
-        _ptr(context_lens), _ptr(selected), K, B, H, Hk, D, bs, NB, MB * bs, float(scale),
-        int(partition_size), _ptr(workspace), nbytes, _status_arg(device_status)))
+    workspace, ws, nbytes = _list_workspace(workspace, index, stream, B, H, Hk, D, bs, K, partition_size)
+    _launch((_lib or load_library()).pkv_paged_attention_decode_selected, "pkv_paged_attention_decode_selected", index,
+            stream, out.data_ptr(), out_dtype, q.data_ptr(), q_dtype, k_cache.data_ptr(), v_cache.data_ptr(),
+            PKV_E4M3 if q8 else q_dtype, _address(k_scales), _address(v_scales), block_tables.data_ptr(), MB,
+            context_lens.data_ptr(), selected.data_ptr(), K, B, H, Hk, D, bs, NB, MB * bs, scale, partition_size, ws,
+            nbytes, _status_arg(device_status))
     return out
