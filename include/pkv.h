@@ -520,7 +520,7 @@ int pkv_summarize_blocks(const void *k_cache, int cache_dtype, const float *k_sc
  *   summaries    as pkv_summarize_blocks leaves them
  *   keep_first, keep_last  >= 0, together at most num_selected
  * q_dtype and summary_dtype: PKV_F16 or PKV_BF16 (PKV_F32: PKV_EUNSUPPORTED).
- * Shapes as for pkv_paged_attention_decode_q8; contexts of at most 131,072
+ * Shapes as for pkv_paged_attention_decode_q8; contexts of at most 40,960
  * blocks.  A length outside [0, max_context_len] (PKV_DEV_BAD_CONTEXT_LEN) or
  * a block id outside the pool (PKV_DEV_BAD_BLOCK) selects nothing: all -1.
  */

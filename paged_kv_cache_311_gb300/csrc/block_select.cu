@@ -7,12 +7,11 @@
 namespace pkv {
 namespace {
 
-constexpr int kSelectMaxCluster = 8;
-constexpr int kSelectMaxChunk = 16384;
+constexpr int kSelectMaxBlocks = 40960;   // their scores fit CTA 0's shared memory
 
-size_t select_smem(int chunk, int head_dim)
+size_t select_smem(int chunk, int most, int head_dim)
 {
-    return sizeof(SelectShared) + (size_t)chunk * 12 + (size_t)head_dim * 8;
+    return sizeof(SelectShared) + (size_t)head_dim * 8 + (size_t)chunk * 4 + (size_t)most * 4 + (size_t)(most + 31) / 32 * 8;
 }
 
 template <typename T, int D>
@@ -20,13 +19,13 @@ int launch_select(const SelectParams &p, int ctas, cudaStream_t stream)
 {
     static unsigned long long done = 0;
     auto kern = select_blocks_kernel<T, D>;
-    const int rc = ensure_smem_attr(reinterpret_cast<const void *>(kern), (int)select_smem(kSelectMaxChunk, D), &done);
+    const int rc = ensure_smem_attr(reinterpret_cast<const void *>(kern), (int)select_smem(kSelectMaxBlocks / kSelectCluster, kSelectMaxBlocks, D), &done);
     if (rc)
         return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas, (unsigned)p.num_kv_heads, (unsigned)p.num_seqs);
     cfg.blockDim = dim3(kSelectThreads);
-    cfg.dynamicSmemBytes = select_smem(p.chunk, D);
+    cfg.dynamicSmemBytes = select_smem(p.chunk, p.most, D);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -65,7 +64,7 @@ extern "C" int pkv_select_blocks(int32_t *selected, const void *q, int q_dtype, 
         num_kv_heads > 65535 || num_seqs > 65535)
         return PKV_EUNSUPPORTED;
     const int most = (max_context_len + block_size - 1) / block_size;
-    if (most > kSelectMaxCluster * kSelectMaxChunk)
+    if (most > kSelectMaxBlocks)
         return PKV_EUNSUPPORTED;
     if (num_seqs == 0)
         return PKV_OK;
@@ -75,8 +74,9 @@ extern "C" int pkv_select_blocks(int32_t *selected, const void *q, int q_dtype, 
         !aligned(context_lens, 4))
         return PKV_EINVAL;
 
+    // CTAs per row: as many as leave each 64 blocks (a load of eight per warp)
     int ctas = 1;
-    while (ctas < kSelectMaxCluster && most > ctas * 256)
+    while (ctas < kSelectCluster && most > ctas * 64)
         ctas *= 2;
     SelectParams p;
     p.selected = selected;
@@ -95,6 +95,7 @@ extern "C" int pkv_select_blocks(int32_t *selected, const void *q, int q_dtype, 
     p.num_selected = num_selected;
     p.keep_first = keep_first;
     p.keep_last = keep_last;
+    p.most = most;
     p.chunk = most > 0 ? (most + ctas - 1) / ctas : 1;
     p.q_dtype = q_dtype;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -7,23 +7,24 @@
 // Q+ = sum_g max(q_g, 0) and Q- = sum_g max(-q_g, 0) it is one product of
 // length 2 D:  score = Q+ . hi - Q- . lo.
 //
-// One cluster of C CTAs serves a (sequence, kv head): CTA c scores the
-// consecutive blocks [c * chunk, (c + 1) * chunk) into its shared memory, and
-// the selection runs over the cluster's shared memories, so scores never
-// touch HBM and one launch does it all.
+// One cluster of C CTAs serves a (sequence, kv head).  CTA c scores the
+// consecutive blocks [c * chunk, (c + 1) * chunk), a warp eight at a time, and
+// stores the scores into the shared memory of CTA 0, which selects: scores
+// never touch HBM, and one launch does it all.
 //
 // Exactness.  Which blocks are selected is a set of whole numbers, so it must
 // not depend on how a sum was rounded.  The fp32 scores carry an error bound
-// eps = 2^-18 * S, S = sum_d (Q+ + Q-)_d * max|summary|_d over the CTA's
-// blocks (see kScoreErr).  A radix selection finds the m-th largest fp32
-// score T; scores above T + 2 eps are in, those below T - 2 eps are out, and
-// only if what lies between does not fit are those blocks scored again in
-// fp64 and selected by (score, then lowest block).
+// eps = 2^-18 * S, S >= sum_d (Q+ + Q-)_d * max|summary|_d (see kScoreErr).
+// CTA 0 finds the m-th largest fp32 score T; scores above T + 2 eps are in,
+// those below T - 2 eps are out, and only if what lies between does not fit
+// are those blocks scored again in fp64 and selected by (score, then lowest
+// block).
 #pragma once
 
 #include <cooperative_groups.h>
 
 #include "pkv_device.cuh"
+#include "q8_cache.cuh"
 
 namespace pkv {
 
@@ -38,6 +39,7 @@ struct SelectParams {
     int num_seqs, num_kv_heads, group, max_blocks_per_seq, max_context_len, block_size;
     int num_selected, keep_first, keep_last;
     int chunk;                    // blocks per CTA
+    int most;                     // blocks of max_context_len
     int q_dtype;
 };
 
@@ -71,15 +73,18 @@ __device__ __forceinline__ unsigned long long order_key64(double x)
     return b >> 63 ? ~b : b | 1ull << 63;
 }
 
-// Shared memory of one CTA, before its `chunk` entries of each array.
+constexpr int kSelectBins = 2048;
+constexpr int kSelectCluster = 8;   // CTAs per cluster, at most
+constexpr int kSelectList = 256;
+
+// CTA 0's shared memory before its arrays.
 struct SelectShared {
-    uint32_t hist[2][256];   // read by the whole cluster, alternating rounds
+    uint32_t hist[kSelectBins];
+    uint32_t list[kSelectList];
     uint32_t scan[kSelectThreads / 32];
-    uint32_t scan2[kSelectThreads / 32];
-    float bound;             // this CTA's eps
-    uint32_t count[4];       // this CTA's counts, read by the whole cluster
-    uint32_t pick[2];        // the round's bin and what is left in it
-    int bad;
+    uint32_t pick[4];
+    float bound[kSelectCluster];   // written by the cluster's CTAs
+    int bad[kSelectCluster];
 };
 
 // Exclusive sum of v over the CTA's threads; *total receives the sum.
@@ -108,66 +113,125 @@ __device__ __forceinline__ uint32_t cta_exclusive(uint32_t v, uint32_t *warp_sum
     return before + x - v;
 }
 
-// The m-th largest (m >= 1) of the cluster's keys: key(i) of the entries i in
-// [0, n) of each CTA for which live(i).  Four rounds of eight bits; *left =
-// how many of the entries equal to the result are among the m largest.
-template <typename Key, typename Live>
-__device__ uint32_t cluster_kth(SelectShared *sh, int n, uint32_t m, Key key, Live live, int *round,
-                                uint32_t *left)
+// The m-th largest (1 <= m <= number of live entries) of key[i], i in [0, n),
+// live(i); *left = how many of the entries equal to it are among the m
+// largest.  Each round spreads what is left over 2048 bins between its
+// smallest and largest key -- scores of one row share their leading bits, and
+// bins of fixed bits would put them all into a few, whose atomics then queue
+// -- and keeps the bin of the m-th; once at most 256 keys are left, each is
+// ranked against all.
+template <typename Live>
+__device__ uint32_t kth_largest(SelectShared *sh, const uint32_t *key, int n, uint32_t m, Live live, uint32_t *left)
 {
-    namespace cg = cooperative_groups;
-    cg::cluster_group cluster = cg::this_cluster();
-    const int tid = threadIdx.x, C = (int)cluster.num_blocks();
-    uint32_t prefix = 0, mask = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        uint32_t *hist = sh->hist[*round & 1];
-        ++*round;
-        hist[tid] = 0;
+    const int tid = threadIdx.x;
+    uint32_t lo = 0xffffffffu, hi = 0;
+    for (int i = tid; i < n; i += kSelectThreads) {
+        if (live(i)) {
+            lo = min(lo, key[i]);
+            hi = max(hi, key[i]);
+        }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    __syncthreads();
+    if (tid == 0) {
+        sh->pick[0] = 0xffffffffu;
+        sh->pick[1] = 0;
+    }
+    __syncthreads();
+    if ((tid & 31) == 0) {
+        atomicMin(&sh->pick[0], lo);
+        atomicMax(&sh->pick[1], hi);
+    }
+    __syncthreads();
+    lo = sh->pick[0];
+    hi = sh->pick[1];
+    for (;;) {
+        // keys in [lo, hi] hold the m-th largest of themselves
+        if (lo == hi) {
+            *left = m;
+            return lo;
+        }
+        const uint32_t span = hi - lo;
+        const int shift = max(0, 32 - __clz(span) - 11);   // span >> shift < 2048
+#pragma unroll
+        for (int k = 0; k < kSelectBins / kSelectThreads; ++k)
+            sh->hist[k * kSelectThreads + tid] = 0;
         __syncthreads();
         for (int i = tid; i < n; i += kSelectThreads) {
             if (live(i)) {
-                const uint32_t k = key(i);
-                if ((k & mask) == prefix)
-                    atomicAdd(&hist[k >> shift & 255u], 1u);
+                const uint32_t k = key[i];
+                if (k >= lo && k <= hi)
+                    atomicAdd(&sh->hist[(k - lo) >> shift], 1u);
             }
         }
-        cluster.sync();
-        // bins from the highest: thread t looks at bin 255 - t
-        const int bin = 255 - tid;
-        uint32_t v = 0;
-        for (int c = 0; c < C; ++c)
-            v += cluster.map_shared_rank(hist, c)[bin];
-        uint32_t total;
-        const uint32_t above = cta_exclusive(v, sh->scan, &total);
-        if (above < m && m <= above + v) {
-            sh->pick[0] = (uint32_t)bin;
-            sh->pick[1] = m - above;
+        __syncthreads();
+        // thread t adds up bins [first, first + 8), from the highest down
+        constexpr int BPT = kSelectBins / kSelectThreads;
+        const int first = kSelectBins - BPT * (tid + 1);
+        uint32_t h[BPT], sum = 0, total;
+#pragma unroll
+        for (int k = 0; k < BPT; ++k) {
+            h[k] = sh->hist[first + k];
+            sum += h[k];
+        }
+        uint32_t above = cta_exclusive(sum, sh->scan, &total);
+        if (above < m && m <= above + sum) {
+#pragma unroll
+            for (int k = BPT - 1; k >= 0; --k) {
+                if (above < m && m <= above + h[k]) {
+                    sh->pick[0] = (uint32_t)(first + k);
+                    sh->pick[1] = m - above;
+                    sh->pick[2] = h[k];
+                }
+                above += h[k];
+            }
+            sh->pick[3] = 0;
         }
         __syncthreads();
-        prefix |= sh->pick[0] << shift;
-        mask |= 255u << shift;
+        const uint32_t bin = sh->pick[0], inside = sh->pick[2];
         m = sh->pick[1];
+        const uint32_t base = lo + (bin << shift);
+        hi = base + min(hi - base, (1u << shift) - 1u);
+        lo = base;
+        if (shift == 0) {
+            *left = m;
+            return lo;
+        }
+        if (inside > kSelectList) {
+            __syncthreads();   // pick is read
+            continue;
+        }
+        for (int i = tid; i < n; i += kSelectThreads) {
+            if (live(i)) {
+                const uint32_t k = key[i];
+                if (k >= lo && k <= hi)
+                    sh->list[atomicAdd(&sh->pick[3], 1u)] = k;   // equal keys are alike: their order does not matter
+            }
+        }
         __syncthreads();
+        if (tid < (int)inside) {
+            const uint32_t k = sh->list[tid];
+            uint32_t more = 0, same = 0;
+            for (uint32_t j = 0; j < inside; ++j) {
+                more += sh->list[j] > k;
+                same += sh->list[j] == k;
+            }
+            if (more < m && m <= more + same) {
+                sh->pick[0] = k;
+                sh->pick[1] = m - more;
+            }
+        }
+        __syncthreads();
+        *left = sh->pick[1];
+        return sh->pick[0];
     }
-    *left = m;
-    return prefix;
 }
 
-// The sum over the cluster's CTAs of count[slot] (all may call), and the sum
-// over the CTAs before this one.
-__device__ __forceinline__ uint32_t cluster_sum(SelectShared *sh, int slot, uint32_t *before)
+__device__ __forceinline__ float select_q(const SelectParams &p, int64_t i)
 {
-    namespace cg = cooperative_groups;
-    cg::cluster_group cluster = cg::this_cluster();
-    const int C = (int)cluster.num_blocks(), me = (int)cluster.block_rank();
-    uint32_t all = 0, b = 0;
-    for (int c = 0; c < C; ++c) {
-        const uint32_t v = cluster.map_shared_rank(&sh->count[slot], c)[0];
-        all += v;
-        b += c < me ? v : 0u;
-    }
-    *before = b;
-    return all;
+    return p.q_dtype == PKV_F16 ? to_float(static_cast<const __half *>(p.q)[i])
+                                : to_float(static_cast<const __nv_bfloat16 *>(p.q)[i]);
 }
 
 template <typename T, int D>
@@ -176,256 +240,274 @@ select_blocks_kernel(const __grid_constant__ SelectParams p)
 {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
-    constexpr int HALF = D / 8;              // lanes that hold one of the two rows
+    constexpr int HALF = D / 8;              // lanes that hold one of a summary's two rows
     constexpr int LPB = 2 * HALF;            // lanes per block
-    constexpr int BPW = 32 / LPB;            // blocks a warp scores side by side
+    constexpr int BPW = 32 / LPB;            // blocks of one load
+    constexpr int U = 8;                     // loads in flight
     constexpr int NW = kSelectThreads / 32;
-    extern __shared__ uint8_t smem[];
+    extern __shared__ __align__(16) uint8_t smem[];
     SelectShared *sh = reinterpret_cast<SelectShared *>(smem);
-    uint32_t *key = reinterpret_cast<uint32_t *>(smem + sizeof(SelectShared));
-    uint32_t *key_lo = key + p.chunk;
-    int32_t *phys = reinterpret_cast<int32_t *>(key_lo + p.chunk);
-    float *qsum = reinterpret_cast<float *>(phys + p.chunk);   // Q+ [D], Q- [D]
+    float *qsum = reinterpret_cast<float *>(smem + sizeof(SelectShared));   // Q+ [D], Q- [D]
+    int32_t *phys = reinterpret_cast<int32_t *>(qsum + 2 * D);              // [chunk]
+    uint32_t *key = reinterpret_cast<uint32_t *>(phys + p.chunk);           // [most], CTA 0's in use
+    uint32_t *in = key + p.most;                                            // bit i: block i is selected
+    uint32_t *pend = in + (p.most + 31) / 32;                               // bit i: block i is in doubt
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int me = (int)cluster.block_rank();
+    const int me = (int)cluster.block_rank(), C = (int)cluster.num_blocks();
     const int kvh = blockIdx.y, seq = blockIdx.z;
-    int32_t *out = p.selected + ((int64_t)seq * p.num_kv_heads + kvh) * p.num_selected;
-    const int K = p.num_selected;
+    cluster.barrier_arrive();   // CTA 0 has started once this completes: its memory may be written
     const int L = p.context_lens[seq];
     const bool bad_len = L < 0 || L > p.max_context_len;
     if (bad_len && kvh == 0 && me == 0 && tid == 0)
         report(p.status, PKV_DEV_BAD_CONTEXT_LEN);
     const int n = bad_len ? 0 : (L + p.block_size - 1) / p.block_size;
+    const int K = p.num_selected;
     const int b0 = min(me * p.chunk, n);
     const int mine = min(p.chunk, n - b0);
-    const int32_t *table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq + b0;
+    const int32_t *table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
+    const int64_t q0 = ((int64_t)seq * p.num_kv_heads + kvh) * p.group * D;
 
-    // ---- block ids; every CTA of the cluster learns whether one is bad
     int bad = 0;
     for (int i = tid; i < mine; i += kSelectThreads) {
-        int b = table[i];
+        int b = table[b0 + i];
         if (b < 0 || (int64_t)b >= p.num_blocks) {
             bad = 1;
             b = 0;
         }
         phys[i] = b;
     }
-    for (int d = tid; d < D; d += kSelectThreads) {
+    if (n > K && tid < D) {
         float up = 0.f, down = 0.f;
         for (int g = 0; g < p.group; ++g) {
-            const int64_t at = ((int64_t)seq * p.num_kv_heads * p.group + kvh * p.group + g) * D + d;
-            const float x = p.q_dtype == PKV_F16 ? to_float(static_cast<const __half *>(p.q)[at])
-                                                 : to_float(static_cast<const __nv_bfloat16 *>(p.q)[at]);
+            const float x = select_q(p, q0 + (int64_t)g * D + tid);
             // NaN goes into both sums
             up += x < 0.f ? 0.f : x;
             down += x > 0.f ? 0.f : -x;
         }
-        qsum[d] = up;
-        qsum[D + d] = down;
+        qsum[tid] = up;
+        qsum[D + tid] = down;
     }
     bad = __syncthreads_or(bad);
-    if (tid == 0) {
-        sh->bad = bad;
-        sh->bound = 0.f;
-    }
-    cluster.sync();
-    for (int c = 0; c < (int)cluster.num_blocks(); ++c)
-        bad |= *cluster.map_shared_rank(&sh->bad, c);
-    if (bad || n <= K) {
-        // a refused row selects nothing; a short one selects everything
-        if (bad && me == 0 && tid == 0)
-            report(p.status, PKV_DEV_BAD_BLOCK);
-        const int have = bad ? 0 : n;
-        for (int i = me * kSelectThreads + tid; i < K; i += (int)cluster.num_blocks() * kSelectThreads)
-            out[i] = i < have ? i : -1;
-        cluster.sync();   // no CTA leaves while another reads its shared memory
-        return;
-    }
+    cluster.barrier_wait();
 
-    // ---- scores
-    const bool is_lo = (lane % LPB) < HALF;
-    const int c8 = (lane % HALF) * 8;
-    float w[8];   // this lane's weights: -Q- on the minima, Q+ on the maxima
-    float biggest[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        w[k] = is_lo ? -qsum[D + c8 + k] : qsum[c8 + k];
-        biggest[k] = 0.f;
-    }
-    const uint4 *sums = reinterpret_cast<const uint4 *>(p.summaries);
-    for (int i0 = warp * BPW; i0 < mine; i0 += NW * BPW) {
-        const int i = i0 + lane / LPB;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (i < mine)
-            x = sums[((int64_t)phys[i] * p.num_kv_heads + kvh) * LPB + lane % LPB];
-        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-        float s = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 f = Unpack<T>::pair(in[k]);
-            s = fmaf(w[2 * k], f.x, s);
-            s = fmaf(w[2 * k + 1], f.y, s);
-            biggest[2 * k] = fmaxf(biggest[2 * k], fabsf(f.x));
-            biggest[2 * k + 1] = fmaxf(biggest[2 * k + 1], fabsf(f.y));
-        }
-#pragma unroll
-        for (int off = 1; off < LPB; off <<= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, off);
-        if (i < mine && lane % LPB == 0)
-            key[i] = order_key(s);
-    }
-    {
-        float S = 0.f;
+    // ---- scores, into CTA 0's shared memory
+    float S = 0.f;
+    if (n > K && !bad) {
+        uint32_t *keys = cluster.map_shared_rank(key, 0) + b0;
+        const bool is_lo = (lane % LPB) < HALF;
+        const int c8 = (lane % HALF) * 8;
+        float w[8];   // this lane's weights: -Q- on the minima, Q+ on the maxima
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            S += fabsf(w[k]) * biggest[k];
+            w[k] = is_lo ? -qsum[D + c8 + k] : qsum[c8 + k];
+        using V = typename Pair16<T>::V;
+        V biggest[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            biggest[k] = as_pair<T>(0u);
+        const uint4 *sums = reinterpret_cast<const uint4 *>(p.summaries) + kvh * LPB + lane % LPB;
+        const int64_t stride = (int64_t)p.num_kv_heads * LPB;
+        for (int i0 = warp * U * BPW; i0 < mine; i0 += NW * U * BPW) {
+            uint4 x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * BPW + lane / LPB;
+                x[u] = make_uint4(0, 0, 0, 0);
+                if (i < mine)
+                    x[u] = __ldg(sums + phys[i] * stride);
+            }
+            float s[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t word[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                s[u] = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = Unpack<T>::pair(word[k]);
+                    s[u] = fmaf(w[2 * k], f.x, s[u]);
+                    s[u] = fmaf(w[2 * k + 1], f.y, s[u]);
+                    biggest[k] = __hmax2(biggest[k], as_pair<T>(word[k] & 0x7fff7fffu));
+                }
+            }
+            // sums over a block's lanes: the halves of the lanes take halves
+            // of the blocks until each lane has one, then add up the rest
+            int u0 = 0;
+#pragma unroll
+            for (int k = U / 2, off = LPB / 2; k >= 1; k >>= 1, off >>= 1) {
+                const bool up = lane & off;
+#pragma unroll
+                for (int u = 0; u < k; ++u) {
+                    const float give = up ? s[u] : s[u + k];
+                    const float keep = up ? s[u + k] : s[u];
+                    s[u] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+                }
+                u0 += up ? k : 0;
+            }
+#pragma unroll
+            for (int off = LPB / 2 / U; off >= 1; off >>= 1)
+                s[0] += __shfl_xor_sync(0xffffffffu, s[0], off);
+            const int i = i0 + u0 * BPW + lane / LPB;
+            if (i < mine && lane % (LPB / U) == 0)
+                keys[i] = order_key(s[0]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = Unpack<T>::pair(as_word(biggest[k]));
+            S += fabsf(w[2 * k]) * f.x;
+            S += fabsf(w[2 * k + 1]) * f.y;
+        }
 #pragma unroll
         for (int off = 1; off < LPB; off <<= 1)
             S += __shfl_xor_sync(0xffffffffu, S, off);
-        if (lane % LPB == 0)   // NaN and infinite bounds order above every number
-            atomicMax(reinterpret_cast<uint32_t *>(&sh->bound), __float_as_uint(S) & 0x7fffffffu);
+        // NaN and infinity order above every number
+        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(S) & 0x7fffffffu);
+        if (lane == 0)
+            sh->scan[warp] = most;
+        __syncthreads();
+        uint32_t all = 0;
+#pragma unroll
+        for (int k = 0; k < NW; ++k)
+            all = max(all, sh->scan[k]);
+        S = __uint_as_float(all);
+    }
+    if (tid == 0) {
+        SelectShared *to = cluster.map_shared_rank(sh, 0);
+        to->bound[me] = S;
+        to->bad[me] = bad;
     }
     cluster.sync();
-    float S = 0.f;
-    for (int c = 0; c < (int)cluster.num_blocks(); ++c) {
-        const float x = *cluster.map_shared_rank(&sh->bound, c);
-        S = !(x <= 3.0e38f) ? INFINITY : fmaxf(S, x);
-    }
-    const float eps = S * kScoreErr;
+    if (me != 0)
+        return;
 
-    // ---- the m-th largest score of the blocks that are not always selected
+    // ---- CTA 0 selects
+    S = 0.f;
+    for (int c = 0; c < C; ++c) {
+        S = !(sh->bound[c] <= 3.0e38f) ? INFINITY : fmaxf(S, sh->bound[c]);
+        bad |= sh->bad[c];
+    }
+    int32_t *out = p.selected + ((int64_t)seq * p.num_kv_heads + kvh) * K;
+    if (bad || n <= K) {
+        // a refused row selects nothing; a short one selects everything
+        if (bad && tid == 0)
+            report(p.status, PKV_DEV_BAD_BLOCK);
+        const int have = bad ? 0 : n;
+        for (int i = tid; i < K; i += kSelectThreads)
+            out[i] = i < have ? i : -1;
+        return;
+    }
     const int first = min(p.keep_first, n), last = max(first, n - p.keep_last);
-    const uint32_t m = (uint32_t)(K - (first + n - last));
-    auto open = [&](int i) { const int j = b0 + i; return j >= first && j < last; };
-    int round = 0;
-    uint32_t left = 0;
-    uint32_t tie_hi = 0, tie_lo = 0, ties = 0;   // which of the doubtful blocks are in
-    float hi_edge = 0.f, lo_edge = 0.f;
-    bool resolve = false;
+    const uint32_t m = (uint32_t)(K - (first + n - last));   // places for blocks [first, last)
+    const int words = (n + 31) / 32;
+    uint32_t ties = 0;   // of the blocks in doubt, the lowest `ties` are in
+    float hi_edge = INFINITY, lo_edge = INFINITY;
     if (m > 0) {
-        const uint32_t kth = cluster_kth(sh, mine, m, [&](int i) { return key[i]; }, open, &round, &left);
-        const float t = key_value(kth);
-        hi_edge = t + 2.f * eps;
-        lo_edge = t - 2.f * eps;
-        // an infinite bound or threshold decides nothing: all are doubtful
-        if (!(fabsf(t) < INFINITY && eps < INFINITY)) {
-            hi_edge = INFINITY;
-            lo_edge = -INFINITY;
+        const float eps = S * kScoreErr;
+        uint32_t left;
+        const float t = key_value(kth_largest(sh, key, n, m, [&](int i) { return i >= first && i < last; }, &left));
+        const bool finite = fabsf(t) < INFINITY && eps < INFINITY;   // else all are in doubt
+        hi_edge = finite ? t + 2.f * eps : INFINITY;
+        lo_edge = finite ? t - 2.f * eps : -INFINITY;
+    }
+    uint32_t sure = 0, doubt = 0;
+    for (int i = tid; i < words * 32; i += kSelectThreads) {   // a warp's 32 blocks are one word
+        bool a = i < n, b = false;
+        if (i >= first && i < last) {
+            const float s = key_value(key[i]);
+            a = m > 0 && s > hi_edge;
+            b = m > 0 && !a && !(s < lo_edge);
+            sure += a;
+            doubt += b;
+        }
+        const uint32_t wa = __ballot_sync(0xffffffffu, a), wb = __ballot_sync(0xffffffffu, b);
+        if (lane == 0) {
+            in[i / 32] = wa;
+            pend[i / 32] = wb;
         }
     }
-    // sure: above every doubt; doubtful: between the edges
-    auto sure = [&](int i) { return m > 0 && key_value(key[i]) > hi_edge; };
-    auto doubt = [&](int i) { return m > 0 && !(key_value(key[i]) > hi_edge) && !(key_value(key[i]) < lo_edge); };
-    uint32_t doubt_total = 0, sure_total = 0, before;
-    {
-        uint32_t a = 0, b = 0, ta, tb;
-        for (int i = tid; i < mine; i += kSelectThreads) {
-            if (open(i)) {
-                a += sure(i);
-                b += doubt(i);
-            }
-        }
-        cta_exclusive(a, sh->scan, &ta);
-        cta_exclusive(b, sh->scan2, &tb);
-        if (tid == 0) {
-            sh->count[0] = ta;
-            sh->count[1] = tb;
-        }
-        cluster.sync();
-        sure_total = cluster_sum(sh, 0, &before);
-        doubt_total = cluster_sum(sh, 1, &before);
-    }
-    resolve = m > 0 && sure_total + doubt_total > m;
-    // what a block is: 0 out, 1 in, 2 in if its place among the ties allows
-    auto state = [&](int i) -> int {
-        const int j = b0 + i;
-        if (j < first || j >= last)
-            return 1;
-        if (m == 0)
-            return 0;
-        if (!resolve)
-            return sure(i) || doubt(i) ? 1 : 0;
-        return (int)(key_lo[i]);
-    };
-    if (resolve) {
-        // fp64 scores of the doubtful blocks; key / key_lo become their
-        // high and low words, and then what each block is
-        const uint32_t want = m - sure_total;
-        for (int i = tid; i < mine; i += kSelectThreads)
-            key_lo[i] = open(i) ? (sure(i) ? 1u : doubt(i) ? 2u : 0u) : 1u;
-        __syncthreads();
-        for (int i = warp; i < mine; i += NW) {
-            if (key_lo[i] != 2u)
-                continue;
-            double s = 0.0;
-            for (int k = lane; k < 2 * D; k += 32) {
-                const int d = k % D;
-                double wgt = 0.0;
-                for (int g = 0; g < p.group; ++g) {
-                    const int64_t at = ((int64_t)seq * p.num_kv_heads * p.group + kvh * p.group + g) * D + d;
-                    const float x = p.q_dtype == PKV_F16 ? to_float(static_cast<const __half *>(p.q)[at])
-                                                         : to_float(static_cast<const __nv_bfloat16 *>(p.q)[at]);
-                    wgt += k < D ? (x > 0.f ? 0.f : x) : (x < 0.f ? 0.f : x);
+    uint32_t sure_total, doubt_total;
+    (void)cta_exclusive(sure, sh->scan, &sure_total);
+    (void)cta_exclusive(doubt, sh->scan, &doubt_total);
+    ties = m - sure_total;
+    if (doubt_total > ties && S > 0.f) {
+        // fp64 scores of the blocks in doubt, selected by their high words
+        // and then, among equals, by their low words
+        for (int half = 0; half < 2; ++half) {
+            for (int i = warp; i < n; i += NW) {
+                if (!(pend[i / 32] >> (i % 32) & 1u))
+                    continue;
+                double s = 0.0;
+                const int64_t at = ((int64_t)table[i] * p.num_kv_heads + kvh) * 2 * D;
+                for (int k = lane; k < 2 * D; k += 32) {
+                    double wgt = 0.0;
+                    for (int g = 0; g < p.group; ++g) {
+                        const float x = select_q(p, q0 + (int64_t)g * D + k % D);
+                        wgt += k < D ? (x > 0.f ? 0.f : x) : (x < 0.f ? 0.f : x);
+                    }
+                    s += wgt * (double)to_float(static_cast<const T *>(p.summaries)[at + k]);
                 }
-                const T v = static_cast<const T *>(p.summaries)[((int64_t)phys[i] * p.num_kv_heads + kvh) * 2 * D + k];
-                s += wgt * (double)to_float(v);
-            }
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1)
-                s += __shfl_xor_sync(0xffffffffu, s, off);
-            const unsigned long long kk = order_key64(s);
-            if (lane == 0) {
-                key[i] = (uint32_t)(kk >> 32);
-                phys[i] = (int32_t)(uint32_t)kk;   // the id is not needed again
+                for (int off = 16; off > 0; off >>= 1)
+                    s += __shfl_xor_sync(0xffffffffu, s, off);
+                const unsigned long long kk = order_key64(s);
+                if (lane == 0)
+                    key[i] = half ? (uint32_t)kk : (uint32_t)(kk >> 32);
             }
-        }
-        __syncthreads();
-        auto doubtful = [&](int i) { return key_lo[i] == 2u; };
-        uint32_t left_hi;
-        tie_hi = cluster_kth(sh, mine, want, [&](int i) { return key[i]; }, doubtful, &round, &left_hi);
-        tie_lo = cluster_kth(sh, mine, left_hi, [&](int i) { return (uint32_t)phys[i]; },
-                             [&](int i) { return key_lo[i] == 2u && key[i] == tie_hi; }, &round, &ties);
-        __syncthreads();
-        for (int i = tid; i < mine; i += kSelectThreads) {
-            if (key_lo[i] == 2u) {
-                const uint32_t a = key[i], b = (uint32_t)phys[i];
-                key_lo[i] = a > tie_hi || (a == tie_hi && b > tie_lo) ? 1u : a == tie_hi && b == tie_lo ? 2u : 0u;
+            __syncthreads();
+            uint32_t left;
+            const uint32_t t = kth_largest(sh, key, n, ties, [&](int i) { return (pend[i / 32] >> (i % 32) & 1u) != 0; }, &left);
+            __syncthreads();
+            uint32_t still = 0;
+            for (int i = tid; i < words * 32; i += kSelectThreads) {
+                const uint32_t old = pend[i / 32];
+                const bool is = i < n && (old >> lane & 1u);
+                const uint32_t k = is ? key[i] : 0u;
+                const uint32_t wa = __ballot_sync(0xffffffffu, is && k > t);
+                const uint32_t wb = __ballot_sync(0xffffffffu, is && k == t);
+                if (lane == 0) {
+                    in[i / 32] |= wa;
+                    pend[i / 32] = wb;
+                }
+                still += is && k == t;
             }
+            ties = left;
+            uint32_t total;
+            (void)cta_exclusive(still, sh->scan, &total);
+            if (total == ties)
+                break;
         }
     }
     __syncthreads();
 
-    // ---- emission in ascending order: each thread owns a run of blocks
-    const int per = (mine + kSelectThreads - 1) / kSelectThreads;
-    const int i0 = min(tid * per, mine), i1 = min(i0 + per, mine);
-    uint32_t ins = 0, maybe = 0, total_in, total_maybe, in_before, maybe_before;
-    for (int i = i0; i < i1; ++i) {
-        const int s = state(i);
-        ins += s == 1;
-        maybe += s == 2;
+    // ---- emission in ascending order: thread t owns words [w0, w1)
+    const int per = (words + kSelectThreads - 1) / kSelectThreads;
+    const int w0 = min(tid * per, words), w1 = min(w0 + per, words);
+    uint32_t c = 0, total;
+    for (int k = w0; k < w1; ++k)
+        c += __popc(pend[k]);
+    uint32_t seen = cta_exclusive(c, sh->scan, &total);
+    c = 0;
+    for (int k = w0; k < w1; ++k) {
+        // the lowest `ties` blocks in doubt are in
+        uint32_t w = pend[k], kept = 0;
+        const uint32_t here = (uint32_t)__popc(w);
+        if (seen + here <= ties) {
+            kept = w;
+        } else {
+            for (uint32_t left = seen < ties ? ties - seen : 0u; left > 0; --left) {
+                kept |= w & (0u - w);
+                w &= w - 1;
+            }
+        }
+        seen += here;
+        in[k] |= kept;
+        c += __popc(in[k]);
     }
-    uint32_t in_at = cta_exclusive(ins, sh->scan, &total_in);
-    uint32_t maybe_at = cta_exclusive(maybe, sh->scan2, &total_maybe);
-    if (tid == 0) {
-        sh->count[2] = total_in;
-        sh->count[3] = total_maybe;
+    uint32_t at = cta_exclusive(c, sh->scan, &total);
+    for (int k = w0; k < w1; ++k) {
+        for (uint32_t w = in[k]; w; w &= w - 1)
+            out[at++] = k * 32 + __ffs(w) - 1;
     }
-    cluster.sync();
-    (void)cluster_sum(sh, 2, &in_before);
-    (void)cluster_sum(sh, 3, &maybe_before);
-    in_at += in_before;
-    maybe_at += maybe_before;
-    for (int i = i0; i < i1; ++i) {
-        const int s = state(i);
-        // the lowest `ties` of the equal scores are in
-        const bool in = s == 1 || (s == 2 && maybe_at < ties);
-        if (in)
-            out[in_at + min(maybe_at, ties)] = b0 + i;
-        in_at += s == 1;
-        maybe_at += s == 2;
-    }
-    cluster.sync();   // no CTA leaves while another reads its shared memory
 }
 
 }  // namespace pkv

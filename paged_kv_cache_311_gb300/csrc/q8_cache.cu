@@ -25,10 +25,19 @@ int check_sizes(int num_seqs, int num_tokens, int num_kv_heads, int head_dim, in
     return PKV_OK;
 }
 
+// Tokens per CTA: one while that keeps the grid below eight CTAs per SM (a
+// decode step's tokens all lead a block: their heads then spread over
+// blockIdx.y), else as many as keep it there, up to kUnitTokens.
 template <typename K, typename P>
-int launch(K kern, const P &p, int units, cudaStream_t stream)
+int launch(K kern, P p, int units, cudaStream_t stream)
 {
-    kern<<<dim3((unsigned)p.num_tokens, (unsigned)((units + 7) / 8)), 256, 0, stream>>>(p);
+    const int most = p.num_tokens / (8 * device_sm_count());
+    p.tokens_per_cta = 1;
+    while (p.tokens_per_cta * 2 <= most && p.tokens_per_cta < kUnitTokens)
+        p.tokens_per_cta *= 2;
+    const unsigned x = (unsigned)(((int64_t)p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta);
+    const unsigned y = p.tokens_per_cta == 1 ? (unsigned)((units + kUnitWarps - 1) / kUnitWarps) : 1u;
+    kern<<<dim3(x, y), kUnitThreads, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 

@@ -14,8 +14,12 @@
 // Work units.  A call appends n_s tokens to each sequence s; a unit is one
 // (block touched by the call, kv head).  A token leads its unit when it is the
 // sequence's first new token or opens a block: exactly one warp then owns the
-// block's rows and scale of that head, so nothing is shared between warps,
-// there are no atomics and the result does not depend on any order.
+// block's rows and scale of that head, so nothing is shared between warps and
+// the result does not depend on any order.  A CTA looks at a run of tokens, a
+// thread each, lists the leaders in shared memory and deals (leader, head) to
+// its warps: in a prompt only one token in block_size leads, and a warp for
+// every token spent its time finding that out (216 us for 12.8K tokens of 40
+// heads, 12.8K x 80 warps, where the bytes need 57).
 #pragma once
 
 #include <cuda_fp8.h>
@@ -42,6 +46,7 @@ struct AppendParams {
     uint32_t *status;
     int64_t num_blocks;
     int num_seqs, num_tokens, num_kv_heads, max_blocks_per_seq, scale_stride;
+    int tokens_per_cta;           // at most kUnitTokens
 };
 
 struct SummarizeParams {
@@ -54,73 +59,76 @@ struct SummarizeParams {
     uint32_t *status;
     int64_t num_blocks;
     int num_seqs, num_tokens, num_kv_heads, max_blocks_per_seq, scale_stride;
+    int tokens_per_cta;           // at most kUnitTokens
 };
 
-// The unit that token t leads: rows [row0, row1) of physical block `block`
-// are the call's tokens t, t + 1, ...; the block holds `row1` rows after the
-// call.  ok = false: t leads nothing (padding, or not the first of its block)
-// or its sequence is refused.
+// A unit's rows: rows [row0, row1) of physical block `block` are the call's
+// tokens t, t + 1, ...; the block holds `row1` rows after the call.
 struct AppendUnit {
-    bool ok;
-    int row0, row1;
-    int64_t block;
+    int t, row0, row1, block;
 };
 
-// The sequence that holds token t: the largest s with query_start[s] <= t, or
-// -1.  32 probes a round, by the whole warp.
-__device__ __forceinline__ int find_seq(const int32_t *query_start, int num_seqs, int t, int lane)
-{
-    int lo = 0, hi = num_seqs;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32;
-        const int at = lo + lane * step;
-        const uint32_t below = __ballot_sync(0xffffffffu, at < hi && query_start[at] <= t);
-        const int n = below == 0xffffffffu ? 32 : __ffs(~below) - 1;
-        if (n == 0)
-            return -1;
-        lo += (n - 1) * step;
-        hi = min(hi, lo + step);
-    }
-    return lo;
-}
+constexpr int kUnitWarps = 8;
+constexpr int kUnitThreads = kUnitWarps * 32;
+constexpr int kUnitTokens = 64;   // tokens a CTA looks at, at most
 
+// Whether token t leads a unit (false also for padding and for what is refused).
 template <int BS, typename P>
-__device__ __forceinline__ AppendUnit append_unit(const P &p, int t, int lane)
+__device__ __forceinline__ bool append_unit(const P &p, int t, AppendUnit &u)
 {
-    AppendUnit u{false, 0, 0, 0};
     int s = t, q0 = t, q1 = t + 1;
     if (p.query_start) {
-        s = find_seq(p.query_start, p.num_seqs, t, lane);
-        if (s < 0)
-            return u;
+        // the largest s with query_start[s] <= t
+        int lo = 0, hi = p.num_seqs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (p.query_start[mid] <= t)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        s = lo;
         q0 = p.query_start[s];
         q1 = p.query_start[s + 1];
         if (t < q0 || t >= q1)
-            return u;   // a padding token
+            return false;   // a padding token
     }
     const int L = p.context_lens[s];
     const int n = q1 - q0;
     if (!p.query_start && L == 0)
-        return u;       // a padding sequence
+        return false;       // a padding sequence
     if (q0 < 0 || q1 > p.num_tokens || L < n || (int64_t)L > (int64_t)p.max_blocks_per_seq * BS) {
-        if (lane == 0)
-            report(p.status, PKV_DEV_BAD_CONTEXT_LEN);
-        return u;
+        report(p.status, PKV_DEV_BAD_CONTEXT_LEN);
+        return false;
     }
     const int pos = L - n + (t - q0);
+    u.t = t;
     u.row0 = pos % BS;
     if (u.row0 != 0 && t != q0)
-        return u;
+        return false;
     u.row1 = min(BS, u.row0 + (q1 - t));
-    const int b = p.block_tables[(int64_t)s * p.max_blocks_per_seq + pos / BS];
-    if (b < 0 || (int64_t)b >= p.num_blocks) {
-        if (lane == 0)
-            report(p.status, PKV_DEV_BAD_BLOCK);
-        return u;
+    u.block = p.block_tables[(int64_t)s * p.max_blocks_per_seq + pos / BS];
+    if (u.block < 0 || (int64_t)u.block >= p.num_blocks) {
+        report(p.status, PKV_DEV_BAD_BLOCK);
+        return false;
     }
-    u.block = b;
-    u.ok = true;
-    return u;
+    return true;
+}
+
+// Lists the units that this CTA's tokens lead (blockIdx.x * tokens ..) in
+// shared memory and returns their number.  All threads call it.
+template <int BS, typename P>
+__device__ __forceinline__ int list_units(const P &p, AppendUnit *list, int *count)
+{
+    if (threadIdx.x == 0)
+        *count = 0;
+    __syncthreads();
+    const int64_t t = (int64_t)blockIdx.x * p.tokens_per_cta + threadIdx.x;
+    AppendUnit u;
+    if ((int)threadIdx.x < p.tokens_per_cta && t < p.num_tokens && append_unit<BS>(p, (int)t, u))
+        list[atomicAdd(count, 1)] = u;   // the order decides which warp works, not what it writes
+    __syncthreads();
+    return *count;
 }
 
 // |x| of a pair of 16-bit values, and packed minima / maxima.
@@ -194,27 +202,16 @@ __device__ __forceinline__ uint2 quantize8(uint4 w, float inv, bool odd)
     return make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
 }
 
-// One warp per (token, kv head, K or V); see the head of the file.
+// One unit's rows of one kv head, K or V, by one warp.
 template <typename T, int D, int BS>
-__global__ void __launch_bounds__(256)
-append_cache_q8_kernel(const __grid_constant__ AppendParams p)
+__device__ __forceinline__ void append_rows(const AppendParams &p, const AppendUnit &u, int h, bool is_v, int lane)
 {
     constexpr int LPR = D / 8;        // lanes per row (16 bytes of input each)
     constexpr int RPL = 32 / LPR;     // rows a warp holds per load
     constexpr int NL = BS / RPL;      // loads of a full block
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x;
-    const int unit = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (unit >= 2 * p.num_kv_heads)
-        return;
-    const int h = unit >> 1;
-    const bool is_v = unit & 1;
-    const AppendUnit u = append_unit<BS>(p, t, lane);
-    if (!u.ok)
-        return;
     const uint4 *src = reinterpret_cast<const uint4 *>(is_v ? p.value : p.key);
-    uint8_t *blk = (is_v ? p.v_cache : p.k_cache) + (u.block * p.num_kv_heads + h) * (int64_t)(BS * D);
-    float *scale = (is_v ? p.v_scales : p.k_scales) + u.block * p.scale_stride + h;
+    uint8_t *blk = (is_v ? p.v_cache : p.k_cache) + ((int64_t)u.block * p.num_kv_heads + h) * (BS * D);
+    float *scale = (is_v ? p.v_scales : p.k_scales) + (int64_t)u.block * p.scale_stride + h;
     const int r = lane / LPR, c = lane % LPR;
     const int n = u.row1 - u.row0;
 
@@ -227,7 +224,7 @@ append_cache_q8_kernel(const __grid_constant__ AppendParams p)
         const int row = i * RPL + r;
         x[i] = make_uint4(0, 0, 0, 0);
         if (row < n)
-            x[i] = src[((int64_t)(t + row) * p.num_kv_heads + h) * LPR + c];
+            x[i] = src[((int64_t)(u.t + row) * p.num_kv_heads + h) * LPR + c];
     }
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
@@ -289,12 +286,23 @@ append_cache_q8_kernel(const __grid_constant__ AppendParams p)
         *scale = __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// One warp per (token, kv head): the token that leads a block reads all the
-// rows the block now holds and writes their minima and maxima.  T: the
-// cache's 16-bit type, or for an e4m3 cache (Q8) the summaries' type.
+template <typename T, int D, int BS>
+__global__ void __launch_bounds__(kUnitThreads)
+append_cache_q8_kernel(const __grid_constant__ AppendParams p)
+{
+    __shared__ AppendUnit list[kUnitTokens];
+    __shared__ int count;
+    const int units = 2 * p.num_kv_heads;
+    const int items = list_units<BS>(p, list, &count) * units;
+    for (int i = blockIdx.y * kUnitWarps + (threadIdx.x >> 5); i < items; i += gridDim.y * kUnitWarps)
+        append_rows<T, D, BS>(p, list[i / units], (i % units) >> 1, i & 1, threadIdx.x & 31);
+}
+
+// All rows that a unit's block holds, of one kv head, by one warp: their
+// minima and maxima.  T: the cache's 16-bit type, or for an e4m3 cache (Q8)
+// the summaries' type.
 template <typename T, int D, int BS, bool Q8>
-__global__ void __launch_bounds__(256)
-summarize_blocks_kernel(const __grid_constant__ SummarizeParams p)
+__device__ __forceinline__ void summarize_rows(const SummarizeParams &p, const AppendUnit &u, int h, int lane)
 {
     using V = typename Pair16<typename std::conditional<Q8, __half, T>::type>::V;
     using E = typename std::conditional<Q8, __half, T>::type;
@@ -302,16 +310,8 @@ summarize_blocks_kernel(const __grid_constant__ SummarizeParams p)
     constexpr int LPR = D / EPL;          // lanes per row
     constexpr int RPL = 32 / LPR;
     constexpr int NL = (BS + RPL - 1) / RPL;
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x;
-    const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (h >= p.num_kv_heads)
-        return;
-    const AppendUnit u = append_unit<BS>(p, t, lane);
-    if (!u.ok)
-        return;
     const uint4 *blk = reinterpret_cast<const uint4 *>(p.k_cache) +
-                       (u.block * p.num_kv_heads + h) * (int64_t)(BS * LPR);
+                       ((int64_t)u.block * p.num_kv_heads + h) * (BS * LPR);
     const int r = lane / LPR, c = lane % LPR;
     uint4 x[NL];
 #pragma unroll
@@ -352,7 +352,7 @@ summarize_blocks_kernel(const __grid_constant__ SummarizeParams p)
     for (int k = 0; k < EPL / 2; ++k)
         o[k] = as_word(r ? hi[k] : lo[k]);
     if constexpr (Q8) {
-        const float s = p.k_scales[u.block * p.scale_stride + h];
+        const float s = p.k_scales[(int64_t)u.block * p.scale_stride + h];
 #pragma unroll
         for (int k = 0; k < EPL / 2; ++k) {
             const float2 f = __half22float2(as_pair<__half>(o[k]));
@@ -360,10 +360,21 @@ summarize_blocks_kernel(const __grid_constant__ SummarizeParams p)
         }
     }
     uint4 *dst = reinterpret_cast<uint4 *>(p.summaries) +
-                 ((u.block * p.num_kv_heads + h) * 2 + r) * (int64_t)(D / 8) + c * (EPL / 8);
+                 (((int64_t)u.block * p.num_kv_heads + h) * 2 + r) * (D / 8) + c * (EPL / 8);
 #pragma unroll
     for (int k = 0; k < EPL / 8; ++k)
         dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+}
+
+template <typename T, int D, int BS, bool Q8>
+__global__ void __launch_bounds__(kUnitThreads)
+summarize_blocks_kernel(const __grid_constant__ SummarizeParams p)
+{
+    __shared__ AppendUnit list[kUnitTokens];
+    __shared__ int count;
+    const int items = list_units<BS>(p, list, &count) * p.num_kv_heads;
+    for (int i = blockIdx.y * kUnitWarps + (threadIdx.x >> 5); i < items; i += gridDim.y * kUnitWarps)
+        summarize_rows<T, D, BS, Q8>(p, list[i / p.num_kv_heads], i % p.num_kv_heads, threadIdx.x & 31);
 }
 
 }  // namespace pkv

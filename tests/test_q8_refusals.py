@@ -70,7 +70,7 @@ def select(lib, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(H=7), EINVAL), (dict(H=18), EUNSUPPORTED), (dict(maxL=1025), EINVAL), (dict(K=0), EINVAL), (dict(K=2), EINVAL),
     (dict(first=-1), EINVAL), (dict(last=2147483647), EINVAL), (dict(qdt=0), EUNSUPPORTED), (dict(sdt=0), EUNSUPPORTED),
-    (dict(qdt=3), EINVAL), (dict(D=32), EUNSUPPORTED), (dict(mb=1 << 20, maxL=131073 * 16), EUNSUPPORTED),
+    (dict(qdt=3), EINVAL), (dict(D=32), EUNSUPPORTED), (dict(mb=1 << 20, maxL=40961 * 16), EUNSUPPORTED),
     (dict(sel=0), EINVAL), (dict(q=A + 4), EINVAL), (dict(B=65536), EUNSUPPORTED), (dict(B=0, sel=0), 0),
 ])
 def test_select_host_checks(lib, kw, code):
