@@ -75,8 +75,10 @@ extern "C" int pkv_select_blocks(int32_t *selected, const void *q, int q_dtype, 
         return PKV_EINVAL;
 
     // CTAs per row: as many as leave each 64 blocks (a load of eight per warp)
+    // and as are resident together, four to an SM
+    const long long rows = (long long)num_seqs * num_kv_heads;
     int ctas = 1;
-    while (ctas < kSelectCluster && most > ctas * 64)
+    while (ctas < kSelectCluster && most > ctas * 64 && rows * ctas * 2 <= 4LL * device_sm_count())
         ctas *= 2;
     SelectParams p;
     p.selected = selected;

@@ -14,7 +14,7 @@
 //
 // Exactness.  Which blocks are selected is a set of whole numbers, so it must
 // not depend on how a sum was rounded.  The fp32 scores carry an error bound
-// eps = 2^-18 * S, S >= sum_d (Q+ + Q-)_d * max|summary|_d (see kScoreErr).
+// eps = 14 2^-24 S, S >= sum_d (Q+ + Q-)_d * max|summary|_d (see kScoreErr).
 // CTA 0 finds the m-th largest fp32 score T; scores above T + 2 eps are in,
 // those below T - 2 eps are out, and only if what lies between does not fit
 // are those blocks scored again in fp64 and selected by (score, then lowest
@@ -45,11 +45,11 @@ struct SelectParams {
 
 constexpr int kSelectThreads = 256;
 
-// Error of an fp32 score relative to S: each Q+- carries (G - 1) <= 7
-// roundings, a product one, a lane's sum of 8 products 8, the sum over lanes
-// 5: at most 21 roundings of 2^-24 each, so 2^-19 S bounds it; doubled for
-// the rounding of S itself.
-constexpr float kScoreErr = 1.0f / (1 << 18);
+// Error of an fp32 score relative to S, in roundings of 2^-24: each Q+- sums
+// its G <= 8 terms in a tree (3), a lane adds 8 products in two chains (4 + 1),
+// the sum over lanes takes at most 5: 13; one more covers the rounding of S
+// and of the edges T +- 2 eps.
+constexpr float kScoreErr = 14.0f / (1 << 24);
 
 // A float's bits as an unsigned number of the same order; NaN counts as +inf.
 __device__ __forceinline__ uint32_t order_key(float x)
@@ -278,15 +278,24 @@ select_blocks_kernel(const __grid_constant__ SelectParams p)
         phys[i] = b;
     }
     if (n > K && tid < D) {
-        float up = 0.f, down = 0.f;
-        for (int g = 0; g < p.group; ++g) {
-            const float x = select_q(p, q0 + (int64_t)g * D + tid);
+        float up[8], down[8];
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+            const float x = g < p.group ? select_q(p, q0 + (int64_t)g * D + tid) : 0.f;
             // NaN goes into both sums
-            up += x < 0.f ? 0.f : x;
-            down += x > 0.f ? 0.f : -x;
+            up[g] = x < 0.f ? 0.f : x;
+            down[g] = x > 0.f ? 0.f : -x;
         }
-        qsum[tid] = up;
-        qsum[D + tid] = down;
+#pragma unroll
+        for (int k = 4; k >= 1; k >>= 1) {
+#pragma unroll
+            for (int g = 0; g < k; ++g) {
+                up[g] += up[g + k];
+                down[g] += down[g + k];
+            }
+        }
+        qsum[tid] = up[0];
+        qsum[D + tid] = down[0];
     }
     bad = __syncthreads_or(bad);
     cluster.barrier_wait();
@@ -321,14 +330,13 @@ select_blocks_kernel(const __grid_constant__ SelectParams p)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const uint32_t word[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-                s[u] = 0.f;
+                float2 two = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float2 f = Unpack<T>::pair(word[k]);
-                    s[u] = fmaf(w[2 * k], f.x, s[u]);
-                    s[u] = fmaf(w[2 * k + 1], f.y, s[u]);
+                    two = ffma2(make_float2(w[2 * k], w[2 * k + 1]), Unpack<T>::pair(word[k]), two);
                     biggest[k] = __hmax2(biggest[k], as_pair<T>(word[k] & 0x7fff7fffu));
                 }
+                s[u] = two.x + two.y;
             }
             // sums over a block's lanes: the halves of the lanes take halves
             // of the blocks until each lane has one, then add up the rest
@@ -430,26 +438,69 @@ select_blocks_kernel(const __grid_constant__ SelectParams p)
     (void)cta_exclusive(doubt, sh->scan, &doubt_total);
     ties = m - sure_total;
     if (doubt_total > ties && S > 0.f) {
-        // fp64 scores of the blocks in doubt, selected by their high words
-        // and then, among equals, by their low words
+        // The blocks in doubt by their fp64 scores.
+        auto exact = [&](int i) -> unsigned long long {   // by a warp
+            double s = 0.0;
+            const int64_t at = ((int64_t)table[i] * p.num_kv_heads + kvh) * 2 * D;
+            double wgt[2 * D / 32], v[2 * D / 32];
+#pragma unroll
+            for (int k = 0; k < 2 * D / 32; ++k) {
+                v[k] = (double)to_float(static_cast<const T *>(p.summaries)[at + k * 32 + lane]);
+                wgt[k] = 0.0;
+            }
+            for (int g = 0; g < p.group; ++g) {
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                    const float x = select_q(p, q0 + (int64_t)g * D + k * 32 + lane);
+                    wgt[k] += x > 0.f ? 0.f : x;
+                    wgt[k + D / 32] += x < 0.f ? 0.f : x;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 2 * D / 32; ++k)
+                s += wgt[k] * v[k];
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                s += __shfl_xor_sync(0xffffffffu, s, off);
+            return order_key64(s);
+        };
+        if (doubt_total <= kSelectList) {
+            // a few (two, mostly): listed in ascending order, ranked against each other
+            const int per = (words + kSelectThreads - 1) / kSelectThreads;
+            const int w0 = min(tid * per, words), w1 = min(w0 + per, words);
+            uint32_t c = 0, total;
+            for (int k = w0; k < w1; ++k)
+                c += __popc(pend[k]);
+            c = cta_exclusive(c, sh->scan, &total);
+            for (int k = w0; k < w1; ++k)
+                for (uint32_t w = pend[k]; w; w &= w - 1)
+                    sh->list[c++] = k * 32 + __ffs(w) - 1;
+            __syncthreads();
+            unsigned long long *score = reinterpret_cast<unsigned long long *>(sh->hist);
+            for (uint32_t e = warp; e < doubt_total; e += NW) {
+                const unsigned long long kk = exact((int)sh->list[e]);
+                if (lane == 0)
+                    score[e] = kk;
+            }
+            for (int k = tid; k < words; k += kSelectThreads)
+                pend[k] = 0;
+            __syncthreads();
+            if (tid < (int)doubt_total) {
+                const unsigned long long mine64 = score[tid];
+                uint32_t rank = 0;
+                for (uint32_t e = 0; e < doubt_total; ++e)
+                    rank += score[e] > mine64 || (score[e] == mine64 && e < (uint32_t)tid);
+                if (rank < ties)
+                    atomicOr(&in[sh->list[tid] / 32], 1u << (sh->list[tid] % 32));
+            }
+            ties = 0;
+        } else
+        // many: by their high words and then, among equals, by their low words
         for (int half = 0; half < 2; ++half) {
             for (int i = warp; i < n; i += NW) {
                 if (!(pend[i / 32] >> (i % 32) & 1u))
                     continue;
-                double s = 0.0;
-                const int64_t at = ((int64_t)table[i] * p.num_kv_heads + kvh) * 2 * D;
-                for (int k = lane; k < 2 * D; k += 32) {
-                    double wgt = 0.0;
-                    for (int g = 0; g < p.group; ++g) {
-                        const float x = select_q(p, q0 + (int64_t)g * D + k % D);
-                        wgt += k < D ? (x > 0.f ? 0.f : x) : (x < 0.f ? 0.f : x);
-                    }
-                    s += wgt * (double)to_float(static_cast<const T *>(p.summaries)[at + k]);
-                }
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1)
-                    s += __shfl_xor_sync(0xffffffffu, s, off);
-                const unsigned long long kk = order_key64(s);
+                const unsigned long long kk = exact(i);
                 if (lane == 0)
                     key[i] = half ? (uint32_t)kk : (uint32_t)(kk >> 32);
             }
