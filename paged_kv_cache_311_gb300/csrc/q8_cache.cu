@@ -31,7 +31,7 @@ int check_sizes(int num_seqs, int num_tokens, int num_kv_heads, int head_dim, in
 template <typename K, typename P>
 int launch(K kern, P p, int units, cudaStream_t stream)
 {
-    const int most = p.num_tokens / (8 * device_sm_count());
+    const int most = p.num_tokens / (PKV_UNIT_CTAS * device_sm_count());
     p.tokens_per_cta = 1;
     while (p.tokens_per_cta * 2 <= most && p.tokens_per_cta < kUnitTokens)
         p.tokens_per_cta *= 2;

@@ -70,7 +70,13 @@ struct AppendUnit {
 
 constexpr int kUnitWarps = 8;
 constexpr int kUnitThreads = kUnitWarps * 32;
-constexpr int kUnitTokens = 64;   // tokens a CTA looks at, at most
+#ifndef PKV_UNIT_TOKENS
+#define PKV_UNIT_TOKENS 64
+#endif
+#ifndef PKV_UNIT_CTAS
+#define PKV_UNIT_CTAS 8
+#endif
+constexpr int kUnitTokens = PKV_UNIT_TOKENS;   // tokens a CTA looks at, at most
 
 // Whether token t leads a unit (false also for padding and for what is refused).
 template <int BS, typename P>
@@ -298,83 +304,120 @@ append_cache_q8_kernel(const __grid_constant__ AppendParams p)
         append_rows<T, D, BS>(p, list[i / units], (i % units) >> 1, i & 1, threadIdx.x & 31);
 }
 
-// All rows that a unit's block holds, of one kv head, by one warp: their
-// minima and maxima.  T: the cache's 16-bit type, or for an e4m3 cache (Q8)
-// the summaries' type.
+// One block's rows of one kv head by one warp: load() issues the loads,
+// finish() writes the minima and maxima.  A lane keeps to its own 4 or 8
+// bytes of every row, so that rows meet in registers: with 16 bytes per lane
+// and several rows to a load, the shuffles that joined the rows cost more
+// than the comparisons.  T: the cache's 16-bit type, or for an e4m3 cache
+// (Q8) the summaries' type.
 template <typename T, int D, int BS, bool Q8>
-__device__ __forceinline__ void summarize_rows(const SummarizeParams &p, const AppendUnit &u, int h, int lane)
-{
-    using V = typename Pair16<typename std::conditional<Q8, __half, T>::type>::V;
+struct BlockRange {
     using E = typename std::conditional<Q8, __half, T>::type;
-    constexpr int EPL = Q8 ? 16 : 8;      // values of a lane's 16 bytes
-    constexpr int LPR = D / EPL;          // lanes per row
-    constexpr int RPL = 32 / LPR;
-    constexpr int NL = (BS + RPL - 1) / RPL;
-    const uint4 *blk = reinterpret_cast<const uint4 *>(p.k_cache) +
-                       ((int64_t)u.block * p.num_kv_heads + h) * (BS * LPR);
-    const int r = lane / LPR, c = lane % LPR;
-    uint4 x[NL];
+    using V = typename Pair16<E>::V;
+    static constexpr int ROW = D * (Q8 ? 1 : 2);            // bytes of a row
+    static constexpr int LW = ROW == 256 ? 2 : 1;           // words a lane holds of a row
+    static constexpr int LPR = ROW / (4 * LW);              // lanes per row
+    static constexpr int RPL = 32 / LPR;                    // rows per load
+    static constexpr int NL = BS / RPL;
+    static constexpr int NP = LW * (Q8 ? 2 : 1);            // pairs of values a lane holds of a row
+    static constexpr int U = NL * LW <= 8 ? 4 : NL * LW <= 16 ? 2 : 1;   // blocks a warp has in flight
+    uint32_t x[NL][LW];
+    float scale;
+
+    __device__ __forceinline__ void load(const SummarizeParams &p, const AppendUnit &u, int h, int lane)
+    {
+        const uint32_t *blk = reinterpret_cast<const uint32_t *>(p.k_cache) +
+                              ((int64_t)u.block * p.num_kv_heads + h) * (BS * ROW / 4) + (lane % LPR) * LW;
+        const int r = lane / LPR;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-        // lanes without a row of their own repeat row 0
-        const int row = i * RPL + r;
-        x[i] = blk[(row < u.row1 ? row : 0) * LPR + c];
+        for (int i = 0; i < NL; ++i) {
+            // lanes without a row of their own repeat row 0
+            const int row = i * RPL + r;
+            const uint32_t *src = blk + (row < u.row1 ? row : 0) * (ROW / 4);
+            if constexpr (LW == 2) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(src);
+                x[i][0] = v.x;
+                x[i][1] = v.y;
+            } else {
+                x[i][0] = *src;
+            }
+        }
+        if constexpr (Q8)
+            scale = p.k_scales[(int64_t)u.block * p.scale_stride + h];
     }
-    V lo[EPL / 2], hi[EPL / 2];
+
+    __device__ __forceinline__ void finish(const SummarizeParams &p, const AppendUnit &u, int h, int lane) const
+    {
+        V lo[NP], hi[NP];
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        for (int i = 0; i < NL; ++i) {
 #pragma unroll
-        for (int k = 0; k < EPL / 2; ++k) {
-            V v;
-            if constexpr (Q8)
-                v = as_pair<E>(f16x2_of_e4m3((k & 1) ? w[k >> 1] >> 16 : w[k >> 1] & 0xffffu));
-            else
-                v = as_pair<E>(w[k]);
-            // NaN stays: a block with a NaN key says so
-            lo[k] = i ? __hmin2_nan(lo[k], v) : v;
-            hi[k] = i ? __hmax2_nan(hi[k], v) : v;
+            for (int k = 0; k < NP; ++k) {
+                V v;
+                if constexpr (Q8)
+                    v = as_pair<E>(f16x2_of_e4m3((k & 1) ? x[i][k >> 1] >> 16 : x[i][k >> 1] & 0xffffu));
+                else
+                    v = as_pair<E>(x[i][k]);
+                // NaN stays: a block with a NaN key says so
+                lo[k] = i ? __hmin2_nan(lo[k], v) : v;
+                hi[k] = i ? __hmax2_nan(hi[k], v) : v;
+            }
+        }
+        if constexpr (RPL == 2) {
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                lo[k] = __hmin2_nan(lo[k], as_pair<E>(__shfl_xor_sync(0xffffffffu, as_word(lo[k]), LPR)));
+                hi[k] = __hmax2_nan(hi[k], as_pair<E>(__shfl_xor_sync(0xffffffffu, as_word(hi[k]), LPR)));
+            }
+        }
+        uint32_t *dst = reinterpret_cast<uint32_t *>(p.summaries) +
+                        ((int64_t)u.block * p.num_kv_heads + h) * D + (lane % LPR) * NP;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            uint32_t o[NP];
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                o[k] = as_word(r ? hi[k] : lo[k]);
+                if constexpr (Q8) {
+                    const float2 f = __half22float2(as_pair<__half>(o[k]));
+                    o[k] = Mma<T>::pack(f.x * scale, f.y * scale);
+                }
+            }
+            if (lane < LPR) {
+                if constexpr (NP == 2)
+                    *reinterpret_cast<uint2 *>(dst + r * (D / 2)) = make_uint2(o[0], o[1]);
+                else
+                    dst[r * (D / 2)] = o[0];
+            }
         }
     }
-#pragma unroll
-    for (int off = LPR; off < 32; off <<= 1) {
-#pragma unroll
-        for (int k = 0; k < EPL / 2; ++k) {
-            lo[k] = __hmin2_nan(lo[k], as_pair<E>(__shfl_xor_sync(0xffffffffu, as_word(lo[k]), off)));
-            hi[k] = __hmax2_nan(hi[k], as_pair<E>(__shfl_xor_sync(0xffffffffu, as_word(hi[k]), off)));
-        }
-    }
-    if (r >= 2)
-        return;
-    // row group 0 writes the minima, row group 1 the maxima
-    uint32_t o[EPL / 2];
-#pragma unroll
-    for (int k = 0; k < EPL / 2; ++k)
-        o[k] = as_word(r ? hi[k] : lo[k]);
-    if constexpr (Q8) {
-        const float s = p.k_scales[(int64_t)u.block * p.scale_stride + h];
-#pragma unroll
-        for (int k = 0; k < EPL / 2; ++k) {
-            const float2 f = __half22float2(as_pair<__half>(o[k]));
-            o[k] = Mma<T>::pack(f.x * s, f.y * s);
-        }
-    }
-    uint4 *dst = reinterpret_cast<uint4 *>(p.summaries) +
-                 (((int64_t)u.block * p.num_kv_heads + h) * 2 + r) * (D / 8) + c * (EPL / 8);
-#pragma unroll
-    for (int k = 0; k < EPL / 8; ++k)
-        dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-}
+};
 
 template <typename T, int D, int BS, bool Q8>
 __global__ void __launch_bounds__(kUnitThreads)
 summarize_blocks_kernel(const __grid_constant__ SummarizeParams p)
 {
+    using R = BlockRange<T, D, BS, Q8>;
     __shared__ AppendUnit list[kUnitTokens];
     __shared__ int count;
-    const int items = list_units<BS>(p, list, &count) * p.num_kv_heads;
-    for (int i = blockIdx.y * kUnitWarps + (threadIdx.x >> 5); i < items; i += gridDim.y * kUnitWarps)
-        summarize_rows<T, D, BS, Q8>(p, list[i / p.num_kv_heads], i % p.num_kv_heads, threadIdx.x & 31);
+    const int lane = threadIdx.x & 31, Hk = p.num_kv_heads;
+    const int items = list_units<BS>(p, list, &count) * Hk;
+    const int step = gridDim.y * kUnitWarps;
+    for (int i0 = blockIdx.y * kUnitWarps + (threadIdx.x >> 5); i0 < items; i0 += step * R::U) {
+        R b[R::U];
+#pragma unroll
+        for (int k = 0; k < R::U; ++k) {
+            const int i = i0 + k * step;
+            if (i < items)
+                b[k].load(p, list[i / Hk], i % Hk, lane);
+        }
+#pragma unroll
+        for (int k = 0; k < R::U; ++k) {
+            const int i = i0 + k * step;
+            if (i < items)
+                b[k].finish(p, list[i / Hk], i % Hk, lane);
+        }
+    }
 }
 
 }  // namespace pkv
