@@ -14,16 +14,21 @@ namespace {
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // List entries per partition for `rows` (sequence, kv head) rows of at most
-// `blocks` entries: one partition when the rows alone fill the GPU, else
-// enough partitions for several CTAs per SM, of at least 64 tokens each.
+// `blocks` entries.
 int list_part_blocks(long long rows, int blocks, int block_size, int partition_size)
 {
     if (blocks < 1)
         blocks = 1;
     if (partition_size > 0)
         return partition_size / block_size;
-    const long long want = 8LL * device_sm_count();
-    long long np = (want + rows - 1) / rows;
+    // rows that fill the SMs stay whole up to 4096 tokens; else enough
+    // partitions for four CTAs per SM, of 64 to 2048 tokens
+    const long long want = 4LL * device_sm_count();
+    const bool fills = rows >= device_sm_count();
+    const long long most = (fills ? 4096 : 2048) / block_size;
+    long long np = fills ? 1 : (want + rows - 1) / rows;
+    if ((blocks + np - 1) / np > most)
+        np = (blocks + (2048 / block_size) - 1) / (2048 / block_size);
     const int least = 64 / block_size;
     long long part = (blocks + np - 1) / np;
     part = (part + least - 1) / least * least;
@@ -70,8 +75,13 @@ int run_list(const ListParams &p, cudaStream_t stream)
         rc = ensure_smem_attr(reinterpret_cast<const void *>(list_merge_kernel<D>), 0, &merge_done);
         if (rc)
             return rc;
-        rc = launch_pdl(list_merge_kernel<D>, dim3((unsigned)((int64_t)p.num_seqs * p.num_kv_heads * p.group)),
-                        dim3(kMergeWarps * 32), 0, stream, p);
+        // a warp for each head where the heads fill the GPU, else several
+        const int64_t heads = (int64_t)p.num_seqs * p.num_kv_heads * p.group;
+        int per_head = 1;
+        while (per_head < kMergeWarps && per_head * 8 < p.np && heads * per_head * 2 <= 32LL * device_sm_count())
+            per_head *= 2;
+        rc = launch_pdl(list_merge_kernel<D>, dim3((unsigned)((heads * per_head + kMergeWarps - 1) / kMergeWarps)),
+                        dim3(kMergeWarps * 32), 0, stream, p, per_head);
         if (rc)
             return rc;
     }

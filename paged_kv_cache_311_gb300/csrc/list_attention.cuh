@@ -75,9 +75,12 @@ template <> struct ListElem<uint8_t> {
     static constexpr CUtensorMapDataType tma = CU_TENSOR_MAP_DATA_TYPE_UINT8;
 };
 
-// Ring bytes of a CTA: three CTAs fit an SM.
+// Ring bytes of a CTA (at least two stages a warp), and CTAs per SM.
 #ifndef PKV_LIST_RING
-#define PKV_LIST_RING 65536
+#define PKV_LIST_RING 49152
+#endif
+#ifndef PKV_LIST_CTAS
+#define PKV_LIST_CTAS 4
 #endif
 
 template <typename T, int D, int BS>
@@ -96,7 +99,8 @@ struct ListCfg {
     static constexpr int BOX_STRIDE = BOX_BYTES < 1024 ? 1024 : BOX_BYTES;   // swizzle atoms are 1024 bytes
     static constexpr int TILE_BYTES = BOXES * BOX_STRIDE;      // K (or V) of a tile
     static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
-    static constexpr int S = PKV_LIST_RING / (kListWarps * STAGE_BYTES);
+    static constexpr int S0 = PKV_LIST_RING / (kListWarps * STAGE_BYTES);
+    static constexpr int S = S0 < 2 ? 2 : S0;
     static constexpr int KS = D / 16;                          // k-steps of QK, m-tiles of PV
     static constexpr int AWS = D + 4;                          // row stride of the merge scratch, in floats
 
@@ -105,7 +109,7 @@ struct ListCfg {
     static constexpr int OFF_VS = OFF_KS + (Q8 ? kListCap * 4 : 0);
     static constexpr int OFF_BAR = OFF_VS + (Q8 ? kListCap * 4 : 0);
     static constexpr int OFF_FLAG = OFF_BAR + kListWarps * S * 8;
-    static constexpr int SMEM_BYTES = OFF_FLAG + 16 + 1024;    // slack for the alignment to 1024
+    static constexpr int SMEM_BYTES = OFF_FLAG + 32 + 1024;    // slack for the alignment to 1024
 
     static_assert(BOX_BYTES % 512 == 0 && BOX_STRIDE % 1024 == 0 && S >= 2, "ring");
     static_assert(kListWarps * kListMaxGroup * (AWS + 2) * 4 <= OFF_PHYS, "merge scratch fits in the ring");
@@ -119,64 +123,86 @@ struct ListCfg {
     }
 };
 
-// Stages entries [e0, e0 + part_blocks) of a (sequence, kv head) row's list:
-// physical block ids and scales.  Returns the number of tokens they hold (the
-// sequence's last block, always the list's last entry, may be partial), or -1
-// if the row is refused.  All threads of the CTA call it; ends with a barrier.
+// The list entries of a CTA's partition, in registers: thread t holds entries
+// t, t + 128, ... of it.  Two steps, so that every load that can leave at once
+// does: load() needs nothing but the arguments, resolve() the row's length.
 //
 // A selected list is refused unless it is strictly ascending and inside the
 // sequence's blocks, with -1 only behind its last entry: so no block counts
 // twice and only the last entry can be partial.
 template <int BS>
-__device__ __forceinline__ int stage_list(const ListParams &p, int32_t *phys, float *ks, float *vs, int seq, int kvh,
-                                          int part, int L)
-{
-    const int nblk = (L + BS - 1) / BS;
-    const int total = p.selected ? p.num_selected : nblk;
-    const int e0 = part * p.part_blocks, e1 = min(e0 + p.part_blocks, total);
-    const int32_t *sel = p.selected ? p.selected + ((int64_t)seq * p.num_kv_heads + kvh) * p.num_selected : nullptr;
-    const int32_t *table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
-    int bad = 0, tokens = 0;
-    for (int e = e0 + (int)threadIdx.x; e < e1; e += kListThreads) {
-        int j = e;
-        if (sel) {
-            const int before = e > 0 ? sel[e - 1] : -1;
-            j = sel[e];
-            if (j < 0 && j != -1)
-                bad = 1;
-            if (j < 0)
-                continue;
-            if (j >= nblk || (e > 0 && (before < 0 || before >= j))) {
-                bad = 1;
-                continue;
+struct ListEntries {
+    static constexpr int N = kListCap / kListThreads;
+    int id[N];       // load(): table entry, or logical block of a selected list
+    int before[N];   // the list's entry in front (selected lists)
+
+    __device__ __forceinline__ void load(const ListParams &p, int seq, int kvh, int e0)
+    {
+        const int have = min(p.part_blocks, (p.selected ? p.num_selected : p.max_blocks_per_seq) - e0);
+        const int32_t *src = p.selected ? p.selected + ((int64_t)seq * p.num_kv_heads + kvh) * p.num_selected + e0
+                                        : p.block_tables + (int64_t)seq * p.max_blocks_per_seq + e0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int k = i * kListThreads + (int)threadIdx.x;
+            id[i] = before[i] = -1;
+            if (k < have) {
+                id[i] = src[k];
+                if (p.selected && e0 + k > 0)
+                    before[i] = src[k - 1];
             }
         }
-        int b = table[j];
-        if (b < 0 || (int64_t)b >= p.num_blocks) {
-            bad = 1;
-            b = 0;
-        }
-        phys[e - e0] = b;
-        if (p.k_scales) {
-            ks[e - e0] = p.k_scales[(int64_t)b * p.scale_stride + kvh];
-            vs[e - e0] = p.v_scales[(int64_t)b * p.scale_stride + kvh];
-        }
-        tokens = max(tokens, (e - e0) * BS + min(BS, L - j * BS));
     }
-    __shared__ int most[kListWarps];
-    tokens = __reduce_max_sync(0xffffffffu, tokens);
-    if ((threadIdx.x & 31) == 0)
-        most[threadIdx.x >> 5] = tokens;
-    if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0)
-            report(p.status, PKV_DEV_BAD_BLOCK);
-        return -1;
-    }
+
+    // Physical block ids into phys; returns the tokens of this thread's
+    // entries counted from the partition's start, or -1 for a refused entry.
+    __device__ __forceinline__ int resolve(const ListParams &p, int32_t *phys, int seq, int e0, int L)
+    {
+        const int nblk = (L + BS - 1) / BS;
+        const int have = min(p.part_blocks, (p.selected ? p.num_selected : nblk) - e0);
+        int tokens = 0;
+        bool bad = false;
+        if (p.selected) {
+            const int32_t *table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
 #pragma unroll
-    for (int w = 0; w < kListWarps; ++w)
-        tokens = max(tokens, most[w]);
-    return tokens;
-}
+            for (int i = 0; i < N; ++i) {
+                const int k = i * kListThreads + (int)threadIdx.x, j = id[i];
+                if (k < have && j >= 0 && j < nblk && (e0 + k == 0 || (before[i] >= 0 && before[i] < j))) {
+                    id[i] = table[j];
+                    before[i] = k * BS + min(BS, L - j * BS);
+                } else {
+                    bad |= k < have && j != -1;
+                    before[i] = 0;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int k = i * kListThreads + (int)threadIdx.x;
+            const int here = p.selected ? before[i] : k < have ? min(k * BS + BS, L - e0 * BS) : 0;
+            if (here > 0) {
+                bad |= id[i] < 0 || (int64_t)id[i] >= p.num_blocks;
+                phys[k] = id[i];
+                tokens = max(tokens, here);
+            } else {
+                id[i] = -1;
+            }
+        }
+        return bad ? -1 : tokens;
+    }
+
+    __device__ __forceinline__ void scales(const ListParams &p, float *ks, float *vs, int kvh) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int k = i * kListThreads + (int)threadIdx.x;
+            if (id[i] >= 0) {
+                const int64_t at = (int64_t)id[i] * p.scale_stride + kvh;
+                ks[k] = p.k_scales[at];
+                vs[k] = p.v_scales[at];
+            }
+        }
+    }
+};
 
 // A row that has no result: zeros, or a partial that says so (sum -1) or that
 // holds nothing (sum 0).
@@ -211,10 +237,30 @@ struct ListEngine {
     int g, c;
     bool lo;                 // weights in two 16-bit parts
 
-    __device__ __forceinline__ void init(const ListParams &p, int seq, int kvh, int lane)
+    // Issues the loads of q.
+    __device__ __forceinline__ void load(const ListParams &p, int seq, int kvh, int lane)
     {
         g = lane >> 2;
         c = lane & 3;
+        const bool live = g < p.group;
+        const int64_t row = ((int64_t)seq * p.num_kv_heads + kvh) * p.group + (live ? g : 0);
+        const uint32_t *qp = reinterpret_cast<const uint32_t *>(p.q) + row * (D / 2);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            if constexpr (C::Q8) {
+                const uint2 w = live ? *reinterpret_cast<const uint2 *>(qp + 8 * ks + 2 * c) : make_uint2(0u, 0u);
+                qf[ks][0] = w.x;
+                qf[ks][1] = w.y;
+            } else {
+                qf[ks][0] = live ? qp[8 * ks + c] : 0u;
+                qf[ks][1] = live ? qp[8 * ks + c + 4] : 0u;
+            }
+        }
+    }
+
+    __device__ __forceinline__ void init(const ListParams &p)
+    {
+        const int lane = threadIdx.x & 31;
         // A weight in f16 is off by 2^-12 of itself at most, less than the
         // output's rounding to bfloat16; bfloat16 weights, and the other
         // outputs, take a second part.
@@ -226,17 +272,8 @@ struct ListEngine {
             koff[k] = C::addr(tk, (2 * k + dk) % (C::CHUNKS * C::PPT));
             voff[k] = C::addr(tv, (2 * k + dv) % (C::CHUNKS * C::PPT));
         }
-        const bool live = g < p.group;
-        const int64_t row = ((int64_t)seq * p.num_kv_heads + kvh) * p.group + (live ? g : 0);
-        const uint32_t *qp = reinterpret_cast<const uint32_t *>(p.q) + row * (D / 2);
         float factor = p.qscale;
         if constexpr (C::Q8) {
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const uint2 w = live ? *reinterpret_cast<const uint2 *>(qp + 8 * ks + 2 * c) : make_uint2(0u, 0u);
-                qf[ks][0] = w.x;
-                qf[ks][1] = w.y;
-            }
             if (p.q_dtype == PKV_BF16) {
                 // bfloat16 to f16: the row's largest magnitude is brought to
                 // [2^14, 2^15) by a power of two, so that what f16 cannot
@@ -263,12 +300,6 @@ struct ListEngine {
                     }
                 }
                 factor *= __uint_as_float((uint32_t)(127 + x) << 23);
-            }
-        } else {
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                qf[ks][0] = live ? qp[8 * ks + c] : 0u;
-                qf[ks][1] = live ? qp[8 * ks + c + 4] : 0u;
             }
         }
         // head h's factor sits in lanes 4 h ..
@@ -364,6 +395,9 @@ struct ListEngine {
                 asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vbase + C::addr(nvalid + i / NPC, i % NPC)),
                              "r"(0u)
                              : "memory");
+            // a later load into the stage must not overtake these stores: each
+            // lane orders its own before it
+            fence_proxy_async_smem();
             __syncwarp();
         }
 
@@ -466,7 +500,7 @@ struct ListEngine {
 // T: __half, __nv_bfloat16, or uint8_t for an e4m3 cache.  Grid (partition,
 // kv head, sequence).
 template <typename T, int D, int BS>
-__global__ void __launch_bounds__(kListThreads, 3)
+__global__ void __launch_bounds__(kListThreads, PKV_LIST_CTAS)
 list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv)
 {
@@ -481,13 +515,15 @@ list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constan
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + warp * S;
     uint32_t *flag = reinterpret_cast<uint32_t *>(smem + C::OFF_FLAG);
+    int *warp_tokens = reinterpret_cast<int *>(smem + C::OFF_FLAG + 16);
+    // what needs nothing but the arguments leaves first: the length, the
+    // list's entries and q
     const int L = p.context_lens[seq];
-    if (L < 0 || L > p.max_context_len) {
-        if (part == 0 && kvh == 0 && threadIdx.x == 0)
-            report(p.status, PKV_DEV_BAD_CONTEXT_LEN);
-        write_empty<D>(p, seq, kvh, part, true);
-        return;
-    }
+    const int e0 = part * p.part_blocks;
+    ListEntries<BS> entries;
+    entries.load(p, seq, kvh, e0);
+    ListEngine<T, D, BS> eng;
+    eng.load(p, seq, kvh, lane);
     if (lane == 0) {
         for (int s = 0; s < S; ++s)
             mbar_init(&bars[s], 1);
@@ -498,7 +534,28 @@ list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constan
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
     }
-    const int tokens = stage_list<BS>(p, phys, ks_s, vs_s, seq, kvh, part, L);
+    if (L < 0 || L > p.max_context_len) {
+        if (part == 0 && kvh == 0 && threadIdx.x == 0)
+            report(p.status, PKV_DEV_BAD_CONTEXT_LEN);
+        write_empty<D>(p, seq, kvh, part, true);
+        return;
+    }
+    int tokens = 0;
+    if (p.selected || e0 * BS < L) {
+        tokens = entries.resolve(p, phys, seq, e0, L);
+        const int most = __reduce_max_sync(0xffffffffu, tokens);
+        if (lane == 0)
+            warp_tokens[warp] = most;
+        if (__syncthreads_or(tokens < 0)) {
+            if (threadIdx.x == 0)
+                report(p.status, PKV_DEV_BAD_BLOCK);
+            tokens = -1;
+        } else {
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+                tokens = max(tokens, warp_tokens[w]);
+        }
+    }
     if (tokens <= 0) {
         write_empty<D>(p, seq, kvh, part, tokens < 0);
         return;
@@ -524,8 +581,11 @@ list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constan
         for (int i = 0; i < min(my_n, S); ++i)
             issue(i, i);
     }
-    ListEngine<T, D, BS> eng;
-    eng.init(p, seq, kvh, lane);
+    if constexpr (C::Q8)
+        entries.scales(p, ks_s, vs_s, kvh);
+    eng.init(p);
+    if constexpr (C::Q8)
+        __syncthreads();   // every thread's scales
 
     int failed_at = -1;
     for (int i = 0; i < my_n; ++i) {
@@ -602,53 +662,48 @@ list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constan
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// One CTA per (sequence, head): the log-sum-exp merge of the np partials,
-// launched as a programmatic dependent of the partitions' kernel.  Warp w
-// takes partials w, w + 8, ...; a lane holds D / 32 dimensions.  A sum of -1
-// marks a refused partition: the row is zero.
+// The log-sum-exp merge of the np partials of every (sequence, head),
+// launched as a programmatic dependent of the partitions' kernel.  A head's
+// partials are dealt to `per_head` warps (a power of two up to 8) of one CTA;
+// a lane holds D / 32 dimensions.  A sum of -1 marks a refused partition: the
+// row is zero.
 constexpr int kMergeWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32)
-list_merge_kernel(const __grid_constant__ ListParams p)
+list_merge_kernel(const __grid_constant__ ListParams p, int per_head)
 {
-    constexpr int N = D / 32, U = 4;
+    constexpr int N = D / 32, U = 8;
     using V = typename std::conditional<N == 4, float4, float2>::type;
     __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
     __shared__ int s_bad[kMergeWarps];
-    __shared__ float s_acc[kMergeWarps][D];
+    __shared__ V s_acc[kMergeWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t sh = blockIdx.x;
-    const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml) + sh * p.np;
-    const float *acc = p.ws_acc + sh * p.np * D + lane * N;
+    const int64_t heads = (int64_t)p.num_seqs * p.num_kv_heads * p.group;
+    const int64_t sh = ((int64_t)blockIdx.x * kMergeWarps + warp) / per_head;
+    const int first = warp % per_head;
+    const bool live = sh < heads;
+    const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml) + (live ? sh : 0) * p.np;
+    const V *acc = reinterpret_cast<const V *>(p.ws_acc + (live ? sh : 0) * p.np * D) + lane;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float mx = -INFINITY, den = 0.f, num[N];
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < N; ++i)
         num[i] = 0.f;
-    for (int k0 = warp; k0 < p.np; k0 += kMergeWarps * U) {
+    for (int k0 = first; live && k0 < p.np; k0 += per_head * U) {
         float2 t[U];
-        float a[U][N];
+        V a[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k = k0 + u * kMergeWarps;
-            t[u] = k < p.np ? __ldcg(ml + k) : make_float2(-INFINITY, 0.f);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t k = k0 + u * kMergeWarps;
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                a[u][i] = 0.f;
-            if (t[u].y != 0.f && !(t[u].y < 0.f)) {   // a partial of sum 0 was not written
-                const V v = __ldcg(reinterpret_cast<const V *>(acc + k * D));
-                a[u][0] = v.x;
-                a[u][1] = v.y;
-                if constexpr (N == 4) {
-                    a[u][2] = v.z;
-                    a[u][3] = v.w;
-                }
+            // every load leaves before one is used: an empty partial's sums
+            // of values are read too, and dropped
+            const int k = k0 + u * per_head;
+            t[u] = make_float2(-INFINITY, 0.f);
+            a[u] = V{};
+            if (k < p.np) {
+                t[u] = __ldcg(ml + k);
+                a[u] = __ldcg(acc + (int64_t)k * 32);
             }
         }
         float mn = mx;
@@ -665,39 +720,69 @@ list_merge_kernel(const __grid_constant__ ListParams p)
             num[i] *= f0;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float f = exp2f(t[u].x - ref);
-            den += f * t[u].y;
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                num[i] += f * a[u][i];
+            if (t[u].y != 0.f) {
+                const float f = exp2f(t[u].x - ref);
+                den += f * t[u].y;
+                num[0] += f * a[u].x;
+                num[1] += f * a[u].y;
+                if constexpr (N == 4) {
+                    num[2] += f * a[u].z;
+                    num[3] += f * a[u].w;
+                }
+            }
         }
         mx = mn;
     }
-    if (lane == 0) {
-        s_m[warp] = mx;
-        s_l[warp] = den;
-        s_bad[warp] = bad;
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        s_acc[warp][lane * N + i] = num[i];
-    __syncthreads();
-    if (threadIdx.x < D) {
-        float M = -INFINITY, n = 0.f, d = 0.f;
-        bool zero = false;
-#pragma unroll
-        for (int w = 0; w < kMergeWarps; ++w) {
+    if (per_head > 1) {
+        V v;
+        v.x = num[0];
+        v.y = num[1];
+        if constexpr (N == 4) {
+            v.z = num[2];
+            v.w = num[3];
+        }
+        s_acc[warp][lane] = v;
+        if (lane == 0) {
+            s_m[warp] = mx;
+            s_l[warp] = den;
+            s_bad[warp] = bad;
+        }
+        __syncthreads();
+        if (first != 0)
+            return;
+        float M = -INFINITY;
+        for (int w = warp; w < warp + per_head; ++w) {
             M = fmaxf(M, s_m[w]);
-            zero |= s_bad[w] != 0;
+            bad |= s_bad[w] != 0;
         }
         const float ref = fmaxf(M, -1e30f);
+        den = 0.f;
 #pragma unroll
-        for (int w = 0; w < kMergeWarps; ++w) {
+        for (int i = 0; i < N; ++i)
+            num[i] = 0.f;
+        for (int w = warp; w < warp + per_head; ++w) {
             const float f = exp2f(s_m[w] - ref);
-            n += f * s_acc[w][threadIdx.x];
-            d += f * s_l[w];
+            const V x = s_acc[w][lane];
+            den += f * s_l[w];
+            num[0] += f * x.x;
+            num[1] += f * x.y;
+            if constexpr (N == 4) {
+                num[2] += f * x.z;
+                num[3] += f * x.w;
+            }
         }
-        store_out(p.out, p.out_dtype, sh * D + threadIdx.x, zero || d == 0.f ? 0.f : n / d);
+    }
+    if (!live)
+        return;
+    const bool zero = bad || den == 0.f;
+    const float inv = 1.f / den;
+    const int64_t at = sh * D + lane * N;
+    if constexpr (N == 4)
+        store_out4(p.out, p.out_dtype, at, zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                : make_float4(num[0] * inv, num[1] * inv, num[2] * inv, num[3] * inv));
+    else {
+        store_out(p.out, p.out_dtype, at, zero ? 0.f : num[0] * inv);
+        store_out(p.out, p.out_dtype, at + 1, zero ? 0.f : num[1] * inv);
     }
 }
 
