@@ -588,9 +588,9 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 def _ready(names: str, *tensors: Optional[torch.Tensor]) -> int:
     """Every tensor (None: absent) contiguous and on one CUDA device -> its
     index.  names: the tensors' names, for the error."""
-    index = tensors[0].get_device()
+    index = tensors[0].get_device()   # -1 on the host
     for t in tensors:
-        if t is not None and (not t.is_cuda or not t.is_contiguous() or t.get_device() != index):
+        if t is not None and (t.get_device() != index or index < 0 or not t.is_contiguous()):
             name = names.split()[next(i for i, x in enumerate(tensors) if x is t)]
             if not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous CUDA tensor")

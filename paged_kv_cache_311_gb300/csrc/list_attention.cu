@@ -13,26 +13,43 @@ namespace {
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// List entries per partition for `rows` (sequence, kv head) rows of at most
-// `blocks` entries.
-int list_part_blocks(long long rows, int blocks, int block_size, int partition_size)
+// The cut of a row's list of at most `blocks` entries: entries per partition,
+// partitions, and whether a row's partitions are a cluster.
+struct ListCut {
+    int part, np;
+    bool cluster;
+};
+
+ListCut list_cut(long long rows, int blocks, int block_size, int partition_size)
 {
     if (blocks < 1)
         blocks = 1;
-    if (partition_size > 0)
-        return partition_size / block_size;
-    // rows that fill the SMs stay whole up to 4096 tokens; else enough
-    // partitions for four CTAs per SM, of 64 to 2048 tokens
-    const long long want = 4LL * device_sm_count();
-    const bool fills = rows >= device_sm_count();
-    const long long most = (fills ? 4096 : 2048) / block_size;
-    long long np = fills ? 1 : (want + rows - 1) / rows;
-    if ((blocks + np - 1) / np > most)
-        np = (blocks + (2048 / block_size) - 1) / (2048 / block_size);
+    ListCut c{0, 1, false};
     const int least = 64 / block_size;
-    long long part = (blocks + np - 1) / np;
-    part = (part + least - 1) / least * least;
-    return (int)(part < kListCap ? part : kListCap);
+    const int sms = device_sm_count();
+    long long part = blocks;
+    if (partition_size > 0) {
+        part = partition_size / block_size;
+    } else if (rows >= sms) {
+        // rows that fill the SMs stay whole up to 4096 tokens, else 2048 each
+        if (blocks > 4096 / block_size)
+            part = 2048 / block_size;
+    } else {
+        // four CTAs per SM; as a cluster where that leaves a CTA 512 tokens
+        const long long np = (4LL * sms + rows - 1) / rows;
+        part = (blocks + np - 1) / np;
+        const long long eighth = (blocks + 7) / 8;
+        if (part < eighth && eighth <= 512 / block_size)
+            part = eighth;
+        part = part > 2048 / block_size ? 2048 / block_size : part;
+        part = (part + least - 1) / least * least;
+    }
+    if (partition_size == 0 && part > kListCap)
+        part = kListCap;
+    c.part = (int)part;
+    c.np = (int)((blocks + part - 1) / part);
+    c.cluster = partition_size == 0 && c.np > 1 && c.np <= 8;
+    return c;
 }
 
 struct ListLayout {
@@ -69,8 +86,21 @@ int run_list(const ListParams &p, cudaStream_t stream)
     int rc = ensure_smem_attr(reinterpret_cast<const void *>(kern), C::SMEM_BYTES, &done);
     if (rc)
         return rc;
-    kern<<<dim3((unsigned)p.np, (unsigned)p.num_kv_heads, (unsigned)p.num_seqs), kListThreads, C::SMEM_BYTES, stream>>>(p, tmk, tmv);
-    if (p.np > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.np, (unsigned)p.num_kv_heads, (unsigned)p.num_seqs);
+    cfg.blockDim = dim3(kListThreads);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.np;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kern, p, tmk, tmv) != cudaSuccess)
+        return PKV_ECUDA;
+    if (p.np > 1 && !p.cluster) {
         static unsigned long long merge_done = 0;
         rc = ensure_smem_attr(reinterpret_cast<const void *>(list_merge_kernel<D>), 0, &merge_done);
         if (rc)
@@ -138,14 +168,14 @@ int decode_list(void *out, int out_dtype, const void *q, int q_dtype, const void
 
     const int table_blocks = (max_context_len + block_size - 1) / block_size;
     const int blocks = select ? num_selected : (table_blocks > 0 ? table_blocks : 1);
-    const int part = list_part_blocks((long long)num_seqs * num_kv_heads, blocks, block_size, partition_size);
-    const int np = (blocks + part - 1) / part;
+    const ListCut cut = list_cut((long long)num_seqs * num_kv_heads, blocks, block_size, partition_size);
+    const int part = cut.part, np = cut.np;
     if (part > kListCap && blocks > kListCap)
         return PKV_EUNSUPPORTED;
     ListParams p;
     p.ws_ml = nullptr;
     p.ws_acc = nullptr;
-    if (np > 1) {
+    if (np > 1 && !cut.cluster) {
         ListLayout lay;
         if (!list_layout(num_seqs, num_heads, np, head_dim, &lay))
             return PKV_EUNSUPPORTED;
@@ -174,6 +204,7 @@ int decode_list(void *out, int out_dtype, const void *q, int q_dtype, const void
     p.scale_stride = q8_scale_stride(num_kv_heads);
     p.part_blocks = part;
     p.np = np;
+    p.cluster = cut.cluster;
     p.out_dtype = out_dtype;
     p.q_dtype = q_dtype;
     p.qscale = scale * 1.4426950408889634f;
@@ -199,12 +230,11 @@ size_t pkv_paged_attention_list_workspace_bytes(int num_seqs, int num_heads, int
         block_size > 32 || max_list_blocks <= 0 || partition_size < 0 || partition_size % block_size ||
         (partition_size > 0 && partition_size < block_size))
         return 0;
-    const int part = list_part_blocks((long long)num_seqs * num_kv_heads, max_list_blocks, block_size, partition_size);
-    const int np = (int)(((long long)max_list_blocks + part - 1) / part);
-    if (np <= 1)
+    const ListCut cut = list_cut((long long)num_seqs * num_kv_heads, max_list_blocks, block_size, partition_size);
+    if (cut.np <= 1 || cut.cluster)
         return 0;
     ListLayout lay;
-    return list_layout(num_seqs, num_heads, np, head_dim, &lay) ? lay.total : 0;
+    return list_layout(num_seqs, num_heads, cut.np, head_dim, &lay) ? lay.total : 0;
 }
 
 int pkv_paged_attention_decode_q8(void *out, int out_dtype, const void *q, int q_dtype, const void *k_cache,

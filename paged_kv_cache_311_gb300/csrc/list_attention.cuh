@@ -8,8 +8,10 @@
 //
 // One CTA per (partition of the list, kv head, sequence); it owns the kv
 // head's G <= 8 query heads, so each K/V byte is read from HBM once.  With more
-// than one partition the CTAs write (max, sum, unnormalised sum of values)
-// and list_merge_kernel combines them.
+// than one partition each CTA has (max, sum, unnormalised sum of values) to
+// give.  Up to eight partitions are a cluster: they exchange them through
+// their shared memory, and each writes a part of the output.  More of them
+// write them to the workspace for list_merge_kernel.
 //
 // Each of the CTA's four warps streams tiles of 16 tokens through a ring of
 // TMA loads of its own (128-byte swizzled boxes, one per block) and runs the
@@ -30,6 +32,8 @@
 // multiplies the tile's product as it joins the accumulators, so no weight
 // has to fit a 16-bit range together with it.
 #pragma once
+
+#include <cooperative_groups.h>
 
 #include "pa_decode.cuh"
 #include "q8_cache.cuh"
@@ -54,6 +58,7 @@ struct ListParams {
     int num_selected, scale_stride;
     int part_blocks;             // list entries per partition
     int np;                      // partitions
+    int cluster;                 // nonzero: the np CTAs of a row are a cluster
     int out_dtype, q_dtype;
     float qscale;                // softmax scale * log2(e)
 };
@@ -112,7 +117,9 @@ struct ListCfg {
     static constexpr int SMEM_BYTES = OFF_FLAG + 32 + 1024;    // slack for the alignment to 1024
 
     static_assert(BOX_BYTES % 512 == 0 && BOX_STRIDE % 1024 == 0 && S >= 2, "ring");
-    static_assert(kListWarps * kListMaxGroup * (AWS + 2) * 4 <= OFF_PHYS, "merge scratch fits in the ring");
+    // the CTA's result, behind the warps' in the rings' memory
+    static constexpr int OFF_RESULT = kListWarps * kListMaxGroup * (AWS + 2) * 4;
+    static_assert(OFF_RESULT % 16 == 0 && OFF_RESULT + kListMaxGroup * (D + 2) * 4 <= OFF_PHYS, "merge scratch fits in the ring");
 
     // Shared-memory offset of 16-byte piece q of token t of a tile.
     __device__ __forceinline__ static uint32_t addr(int t, int q)
@@ -204,19 +211,84 @@ struct ListEntries {
     }
 };
 
-// A row that has no result: zeros, or a partial that says so (sum -1) or that
-// holds nothing (sum 0).
+// What a CTA has of its row's heads: (max, sum) and, for a positive sum, the
+// sums of values; a sum of -1: refused.  In the rings' memory once they are
+// done with.
 template <int D>
-__device__ __forceinline__ void write_empty(const ListParams &p, int seq, int kvh, int part, bool refused)
+struct ListResult {
+    float m[kListMaxGroup], l[kListMaxGroup];
+    float acc[kListMaxGroup][D];
+};
+
+// Writes the CTA's result where it goes: the output (one partition, or a
+// cluster, which all CTAs of it have to reach) or the workspace.  All threads
+// call it after a barrier behind the result's last store.
+template <int D>
+__device__ __forceinline__ void write_result(const ListParams &p, ListResult<D> *res, int seq, int kvh, int part)
 {
-    for (int i = threadIdx.x; i < p.group * D; i += kListThreads) {
-        const int64_t sh = ((int64_t)seq * p.num_kv_heads + kvh) * p.group + i / D;
+    const int64_t head0 = ((int64_t)seq * p.num_kv_heads + kvh) * p.group;
+    const int total = p.group * D;
+    if (p.cluster) {
+        namespace cg = cooperative_groups;
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        for (int i = (part * kListThreads + (int)threadIdx.x) * 4; i < total; i += p.np * kListThreads * 4) {
+            const int r = i / D, d = i % D;
+            float m[8], l[8], M = -INFINITY;
+            float4 a[8];
+            bool bad = false;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                m[k] = -INFINITY;
+                l[k] = 0.f;
+                a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k < p.np) {
+                    const ListResult<D> *other = cluster.map_shared_rank(res, k);
+                    m[k] = other->m[r];
+                    l[k] = other->l[r];
+                    a[k] = *reinterpret_cast<const float4 *>(&other->acc[r][d]);
+                }
+                M = fmaxf(M, m[k]);
+                bad |= l[k] < 0.f;
+            }
+            const float ref = fmaxf(M, -1e30f);
+            float den = 0.f;
+            float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (l[k] != 0.f) {   // else its sums of values were not stored
+                    const float f = exp2f(m[k] - ref);
+                    den += f * l[k];
+                    num.x += f * a[k].x;
+                    num.y += f * a[k].y;
+                    num.z += f * a[k].z;
+                    num.w += f * a[k].w;
+                }
+            }
+            const bool zero = bad || den == 0.f;
+            const float inv = 1.f / den;
+            store_out4(p.out, p.out_dtype, (head0 + r) * D + d,
+                       zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                            : make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv));
+        }
+        cluster.sync();   // no CTA leaves while another reads its shared memory
+        return;
+    }
+    for (int i = (int)threadIdx.x * 4; i < total; i += kListThreads * 4) {
+        const int r = i / D, d = i % D;
+        const float l = res->l[r];
+        const float4 a = *reinterpret_cast<const float4 *>(&res->acc[r][d]);
         if (p.np == 1) {
-            store_out(p.out, p.out_dtype, sh * D + i % D, 0.f);
-        } else if (i % D == 0) {
-            const int64_t slot = sh * p.np + part;
-            p.ws_ml[slot * 2 + 0] = -INFINITY;
-            p.ws_ml[slot * 2 + 1] = refused ? -1.f : 0.f;
+            const float inv = 1.f / l;
+            const bool zero = l == 0.f || l < 0.f;
+            store_out4(p.out, p.out_dtype, (head0 + r) * D + d,
+                       zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
+        } else {
+            const int64_t slot = (head0 + r) * p.np + part;
+            if (l != 0.f)
+                *reinterpret_cast<float4 *>(p.ws_acc + slot * D + d) = a;
+            if (d == 0)
+                *reinterpret_cast<float2 *>(p.ws_ml + slot * 2) = make_float2(res->m[r], l);
         }
     }
 }
@@ -534,14 +606,13 @@ list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constan
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
     }
+    ListResult<D> *res = reinterpret_cast<ListResult<D> *>(smem + C::OFF_RESULT);
+    int tokens = 0;
     if (L < 0 || L > p.max_context_len) {
         if (part == 0 && kvh == 0 && threadIdx.x == 0)
             report(p.status, PKV_DEV_BAD_CONTEXT_LEN);
-        write_empty<D>(p, seq, kvh, part, true);
-        return;
-    }
-    int tokens = 0;
-    if (p.selected || e0 * BS < L) {
+        tokens = -1;
+    } else if (p.selected || e0 * BS < L) {
         tokens = entries.resolve(p, phys, seq, e0, L);
         const int most = __reduce_max_sync(0xffffffffu, tokens);
         if (lane == 0)
@@ -557,7 +628,12 @@ list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constan
         }
     }
     if (tokens <= 0) {
-        write_empty<D>(p, seq, kvh, part, tokens < 0);
+        if (threadIdx.x < kListMaxGroup) {
+            res->m[threadIdx.x] = -INFINITY;
+            res->l[threadIdx.x] = tokens < 0 ? -1.f : 0.f;
+        }
+        __syncthreads();
+        write_result<D>(p, res, seq, kvh, part);
         return;
     }
 
@@ -633,7 +709,6 @@ list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constan
     float *aw = lw + NW * kListMaxGroup;
     eng.finish(mw, lw, aw, warp, p.group);
     __syncthreads();
-    const int64_t head0 = ((int64_t)seq * p.num_kv_heads + kvh) * p.group;
     for (int i = threadIdx.x; i < p.group * D; i += kListThreads) {
         const int r = i / D, d = i % D;
         float Mx = -INFINITY, num = 0.f, den = 0.f;
@@ -647,18 +722,15 @@ list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constan
             num += f * aw[(w * kListMaxGroup + r) * C::AWS + d];
             den += f * lw[w * kListMaxGroup + r];
         }
-        if (p.np == 1) {
-            store_out(p.out, p.out_dtype, (head0 + r) * D + d, failed || den == 0.f ? 0.f : num / den);
-        } else {
-            const int64_t slot = (head0 + r) * p.np + part;
-            p.ws_acc[slot * D + d] = num;
-            if (d == 0) {
-                p.ws_ml[slot * 2 + 0] = Mx;
-                p.ws_ml[slot * 2 + 1] = failed ? -1.f : den;
-            }
+        res->acc[r][d] = num;
+        if (d == 0) {
+            res->m[r] = Mx;
+            res->l[r] = failed ? -1.f : den;
         }
     }
-    if (p.np > 1)
+    __syncthreads();
+    write_result<D>(p, res, seq, kvh, part);
+    if (p.np > 1 && !p.cluster)
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
