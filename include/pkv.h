@@ -519,6 +519,8 @@ int pkv_summarize_blocks(const void *k_cache, int cache_dtype, const float *k_sc
  *   q            [num_seqs, num_heads, head_dim] of q_dtype
  *   summaries    as pkv_summarize_blocks leaves them
  *   keep_first, keep_last  >= 0, together at most num_selected
+ *   workspace    at least pkv_select_blocks_workspace_bytes(...) bytes, 16-byte
+ *                aligned (may be NULL where that is 0)
  * q_dtype and summary_dtype: PKV_F16 or PKV_BF16 (PKV_F32: PKV_EUNSUPPORTED).
  * Shapes as for pkv_paged_attention_decode_q8; contexts of at most 40,960
  * blocks.  A length outside [0, max_context_len] (PKV_DEV_BAD_CONTEXT_LEN) or
@@ -528,8 +530,13 @@ int pkv_select_blocks(int32_t *selected, const void *q, int q_dtype, const void 
                       int summary_dtype, const int32_t *block_tables, int max_blocks_per_seq,
                       const int32_t *context_lens, int num_seqs, int num_heads, int num_kv_heads,
                       int head_dim, int block_size, int64_t num_blocks, int max_context_len,
-                      int num_selected, int keep_first, int keep_last, uint32_t *device_status,
-                      void *stream);
+                      int num_selected, int keep_first, int keep_last, void *workspace,
+                      size_t workspace_bytes, uint32_t *device_status, void *stream);
+
+/* Bytes of workspace of pkv_select_blocks on the current device; 0 if none is
+ * needed or on invalid sizes. */
+size_t pkv_select_blocks_workspace_bytes(int num_seqs, int num_kv_heads, int max_context_len,
+                                         int block_size);
 
 /*
  * paged_attention_decode_selected -- single-query attention of every sequence

@@ -39,6 +39,7 @@ __all__ = [
     "HEADER_PATH", "bounded_wait_hook",
     "append_cache_q8", "summarize_blocks", "select_blocks", "paged_attention_decode_q8",
     "paged_attention_decode_selected", "paged_attention_list_workspace_bytes", "q8_scales",
+    "select_blocks_workspace_bytes",
 ]
 
 HEADER_PATH = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
@@ -128,8 +129,10 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                        i64, vp, vp]
     L.pkv_summarize_blocks.restype = i32
     L.pkv_select_blocks.argtypes = [vp, vp, i32, vp, i32, vp, i32, vp, i32, i32, i32, i32, i32, i64,
-                                    i32, i32, i32, i32, vp, vp]
+                                    i32, i32, i32, i32, vp, u64, vp, vp]
     L.pkv_select_blocks.restype = i32
+    L.pkv_select_blocks_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.pkv_select_blocks_workspace_bytes.restype = u64
     L.pkv_paged_attention_list_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32]
     L.pkv_paged_attention_list_workspace_bytes.restype = u64
     L.pkv_paged_attention_decode_q8.argtypes = [vp, i32, vp, i32, vp, vp, vp, vp, vp, i32, vp, i32, i32,
@@ -726,6 +729,7 @@ def summarize_blocks(k_cache: torch.Tensor, summaries: torch.Tensor, block_table
 def select_blocks(selected: torch.Tensor, q: torch.Tensor, summaries: torch.Tensor,
                   block_tables: torch.Tensor, context_lens: torch.Tensor, block_size: int, *,
                   keep_first: int = 1, keep_last: int = 1, max_context_len: Optional[int] = None,
+                  workspace: Optional[torch.Tensor] = None,
                   device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """selected[s, h] = the K blocks of sequence s that kv head h's query group
     should attend to, in ascending order (-1 behind the last where the
@@ -734,9 +738,10 @@ def select_blocks(selected: torch.Tensor, q: torch.Tensor, summaries: torch.Tens
 
     selected: int32 [B, Hk, K]; q: [B, H, D]; summaries: [NB, Hk, 2, D], both
     float16 or bfloat16.  max_context_len: host bound of context_lens (what the
-    table can hold if omitted)."""
-    index = _ready("selected q summaries block_tables context_lens device_status", selected, q, summaries, block_tables,
-                   context_lens, device_status)
+    table can hold if omitted).  workspace: select_blocks_workspace_bytes,
+    allocated here if needed and not given."""
+    index = _ready("selected q summaries block_tables context_lens workspace device_status", selected, q, summaries,
+                   block_tables, context_lens, workspace, device_status)
     B, H, D = q.shape
     NB, Hk, two, D2 = summaries.shape
     out_shape = selected.shape
@@ -746,13 +751,19 @@ def select_blocks(selected: torch.Tensor, q: torch.Tensor, summaries: torch.Tens
     if selected.dtype != torch.int32 or q_dtype is None or s_dtype is None:
         raise ValueError("selected must be int32, q and summaries floating")
     MB = _tables(block_tables, context_lens, B)
-    if max_context_len is None:
-        max_context_len = MB * block_size
+    max_context_len = MB * block_size if max_context_len is None else int(max_context_len)
+    workspace, ws, nbytes = _workspace(workspace, index, stream, select_blocks_workspace_bytes, B, Hk, max_context_len,
+                                       int(block_size))
     _launch((_lib or load_library()).pkv_select_blocks, "pkv_select_blocks", index, stream,
             selected.data_ptr(), q.data_ptr(), q_dtype, summaries.data_ptr(), s_dtype, block_tables.data_ptr(), MB,
-            context_lens.data_ptr(), B, H, Hk, D, int(block_size), NB, int(max_context_len), out_shape[2],
-            int(keep_first), int(keep_last), _status_arg(device_status))
+            context_lens.data_ptr(), B, H, Hk, D, int(block_size), NB, max_context_len, out_shape[2], int(keep_first),
+            int(keep_last), ws, nbytes, _status_arg(device_status))
     return selected
+
+
+def select_blocks_workspace_bytes(num_seqs: int, num_kv_heads: int, max_context_len: int, block_size: int) -> int:
+    """Workspace bytes of select_blocks on the current device (0: none)."""
+    return int(load_library().pkv_select_blocks_workspace_bytes(num_seqs, num_kv_heads, max_context_len, block_size))
 
 
 def paged_attention_list_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
@@ -764,13 +775,16 @@ def paged_attention_list_workspace_bytes(num_seqs: int, num_heads: int, num_kv_h
         num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_list_blocks, partition_size))
 
 
-def _list_workspace(workspace, index: int, stream, *sizes):
+def _workspace(workspace, index: int, stream, bytes_of, *sizes):
     """The caller's workspace, or one allocated here for the stream that uses it
     -> (tensor or None, address, bytes)."""
     if workspace is not None:
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    with torch.cuda.device(index):
-        nbytes = paged_attention_list_workspace_bytes(*sizes)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            nbytes = bytes_of(*sizes)
+    else:
+        nbytes = bytes_of(*sizes)
     if not nbytes:
         return None, None, 0
     device = torch.device("cuda", index)
@@ -813,8 +827,8 @@ def paged_attention_decode_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torch
     _q8_scale_args(NB, Hk, k_scales, v_scales)
     MB = _tables(block_tables, context_lens, B)
     max_context_len = MB * bs if max_context_len is None else int(max_context_len)
-    workspace, ws, nbytes = _list_workspace(workspace, index, stream, B, H, Hk, D, bs, (max_context_len + bs - 1) // bs,
-                                            partition_size)
+    workspace, ws, nbytes = _workspace(workspace, index, stream, paged_attention_list_workspace_bytes, B, H, Hk, D, bs,
+                                       (max_context_len + bs - 1) // bs, partition_size)
     _launch((_lib or load_library()).pkv_paged_attention_decode_q8, "pkv_paged_attention_decode_q8", index, stream,
             out.data_ptr(), out_dtype, q.data_ptr(), q_dtype, k_cache.data_ptr(), v_cache.data_ptr(),
             k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), MB, context_lens.data_ptr(), B, H, Hk, D,
@@ -851,7 +865,8 @@ def paged_attention_decode_selected(out: torch.Tensor, q: torch.Tensor, k_cache:
         raise ValueError("selected must be int32 [B, Hk, K]")
     K = list_shape[2]
     MB = _tables(block_tables, context_lens, B)
-    workspace, ws, nbytes = _list_workspace(workspace, index, stream, B, H, Hk, D, bs, K, partition_size)
+    workspace, ws, nbytes = _workspace(workspace, index, stream, paged_attention_list_workspace_bytes, B, H, Hk, D, bs, K,
+                                       partition_size)
     _launch((_lib or load_library()).pkv_paged_attention_decode_selected, "pkv_paged_attention_decode_selected", index,
             stream, out.data_ptr(), out_dtype, q.data_ptr(), q_dtype, k_cache.data_ptr(), v_cache.data_ptr(),
             PKV_E4M3 if q8 else q_dtype, _address(k_scales), _address(v_scales), block_tables.data_ptr(), MB,

@@ -4,37 +4,90 @@
 #include "block_select.cuh"
 #include "pkv_host.cuh"
 
+// Most rows x blocks of a call in one launch.
+#ifndef PKV_SELECT_ONE
+#define PKV_SELECT_ONE 32768
+#endif
+
 namespace pkv {
 namespace {
 
-constexpr int kSelectMaxBlocks = 40960;   // their scores fit CTA 0's shared memory
+constexpr int kSelectMaxBlocks = 40960;   // a row's scores fit one CTA's shared memory
+constexpr int kSelectOneBlocks = 2048;    // of a row in one launch
 
-size_t select_smem(int chunk, int most, int head_dim)
+// How a call runs: `ctas` CTAs score `chunk` blocks of a row each, in one
+// launch as a cluster or in two through the workspace.
+struct SelectCut {
+    int chunk, ctas, bounds;
+    bool cluster;
+    size_t bound_off, total;   // workspace: keys, then bounds
+};
+
+// One launch while its summaries are few: it saves a launch, but clusters are
+// not spread evenly over the SMs.
+SelectCut select_cut(int64_t rows, int most)
 {
-    return sizeof(SelectShared) + (size_t)head_dim * 8 + (size_t)chunk * 4 + (size_t)most * 4 + (size_t)(most + 31) / 32 * 8;
+    SelectCut c{};
+    const int n = most > 0 ? most : 1;
+    constexpr int kOne = kSelectThreads / 2;   // blocks of a cluster's CTA, a tile per warp
+    c.cluster = n <= kOne || (n <= kSelectOneBlocks && rows * n <= PKV_SELECT_ONE);
+    if (c.cluster) {
+        // CTAs per row: as many as have a tile per warp while two an
+        // SM are resident together
+        c.ctas = 1;
+        while (c.ctas < kSelectCluster && n > c.ctas * kOne && rows * c.ctas * 2 <= 2LL * device_sm_count())
+            c.ctas *= 2;
+        c.chunk = (n + c.ctas - 1) / c.ctas;
+        c.bounds = c.ctas * (kSelectThreads / 32);
+    } else {
+        c.chunk = kScoreWarps * kScoreTiles * 16;
+        c.ctas = (n + c.chunk - 1) / c.chunk;
+        c.bounds = c.ctas * kScoreWarps;
+        c.bound_off = ((size_t)rows * n * 4 + 255) & ~size_t(255);
+        c.total = c.bound_off + (size_t)rows * c.bounds * 4;
+    }
+    return c;
 }
 
+size_t row_smem(int most) { return sizeof(SelectShared) + (size_t)most * 4 + (size_t)(most + 31) / 32 * 8; }
+
 template <typename T, int D>
-int launch_select(const SelectParams &p, int ctas, cudaStream_t stream)
+int launch_select(const SelectParams &p, int ctas, bool one, cudaStream_t stream)
 {
-    static unsigned long long done = 0;
-    auto kern = select_blocks_kernel<T, D>;
-    const int rc = ensure_smem_attr(reinterpret_cast<const void *>(kern), (int)select_smem(kSelectMaxBlocks / kSelectCluster, kSelectMaxBlocks, D), &done);
+    static unsigned long long done_one = 0, done_score = 0, done_rows = 0;
+    if (one) {
+        auto kern = select_blocks_kernel<T, D>;
+        constexpr size_t score = sizeof(ScoreShared<D, kSelectThreads / 32, 1>);
+        const int rc = ensure_smem_attr(reinterpret_cast<const void *>(kern), (int)(score + row_smem(kSelectOneBlocks)), &done_one);
+        if (rc)
+            return rc;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)ctas, (unsigned)p.num_kv_heads, (unsigned)p.num_seqs);
+        cfg.blockDim = dim3(kSelectThreads);
+        cfg.dynamicSmemBytes = score + row_smem(p.most);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)ctas;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+    }
+    constexpr int score = (int)sizeof(ScoreShared<D, kScoreWarps, kScoreStages>);
+    int rc = ensure_smem_attr(reinterpret_cast<const void *>(score_blocks_kernel<T, D>), score, &done_score);
+    if (!rc)
+        rc = ensure_smem_attr(reinterpret_cast<const void *>(select_rows_kernel<T, D>), (int)row_smem(kSelectMaxBlocks), &done_rows);
     if (rc)
         return rc;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)p.num_kv_heads, (unsigned)p.num_seqs);
-    cfg.blockDim = dim3(kSelectThreads);
-    cfg.dynamicSmemBytes = select_smem(p.chunk, p.most, D);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ctas;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+    score_blocks_kernel<T, D><<<dim3((unsigned)p.num_kv_heads, (unsigned)ctas, (unsigned)p.num_seqs), kScoreWarps * 32, score,
+                                stream>>>(p);
+    rc = launch_pdl(select_rows_kernel<T, D>, dim3((unsigned)p.num_kv_heads, (unsigned)p.num_seqs), dim3(kSelectThreads),
+                    row_smem(p.most), stream, p);
+    if (rc)
+        return rc;
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -44,12 +97,20 @@ bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 using namespace pkv;
 
+extern "C" size_t pkv_select_blocks_workspace_bytes(int num_seqs, int num_kv_heads, int max_context_len, int block_size)
+{
+    if (num_seqs <= 0 || num_kv_heads <= 0 || max_context_len < 0 || block_size <= 0 ||
+        (max_context_len + (int64_t)block_size - 1) / block_size > kSelectMaxBlocks)
+        return 0;
+    return select_cut((int64_t)num_seqs * num_kv_heads, (int)((max_context_len + (int64_t)block_size - 1) / block_size)).total;
+}
+
 extern "C" int pkv_select_blocks(int32_t *selected, const void *q, int q_dtype, const void *summaries,
                                  int summary_dtype, const int32_t *block_tables, int max_blocks_per_seq,
                                  const int32_t *context_lens, int num_seqs, int num_heads, int num_kv_heads,
                                  int head_dim, int block_size, int64_t num_blocks, int max_context_len,
-                                 int num_selected, int keep_first, int keep_last, uint32_t *device_status,
-                                 void *stream)
+                                 int num_selected, int keep_first, int keep_last, void *workspace,
+                                 size_t workspace_bytes, uint32_t *device_status, void *stream)
 {
     if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_dim <= 0 ||
         block_size <= 0 || num_blocks <= 0 || num_blocks > INT32_MAX || max_blocks_per_seq <= 0 ||
@@ -74,12 +135,9 @@ extern "C" int pkv_select_blocks(int32_t *selected, const void *q, int q_dtype, 
         !aligned(context_lens, 4))
         return PKV_EINVAL;
 
-    // CTAs per row: as many as leave each 64 blocks (a load of eight per warp)
-    // and as are resident together, four to an SM
-    const long long rows = (long long)num_seqs * num_kv_heads;
-    int ctas = 1;
-    while (ctas < kSelectCluster && most > ctas * 64 && rows * ctas * 2 <= 4LL * device_sm_count())
-        ctas *= 2;
+    const SelectCut cut = select_cut((int64_t)num_seqs * num_kv_heads, most);
+    if (cut.total && (!workspace || workspace_bytes < cut.total || !aligned(workspace, 16)))
+        return PKV_EWORKSPACE;
     SelectParams p;
     p.selected = selected;
     p.q = q;
@@ -98,11 +156,15 @@ extern "C" int pkv_select_blocks(int32_t *selected, const void *q, int q_dtype, 
     p.keep_first = keep_first;
     p.keep_last = keep_last;
     p.most = most;
-    p.chunk = most > 0 ? (most + ctas - 1) / ctas : 1;
+    p.chunk = cut.chunk;
+    p.bounds = cut.bounds;
+    p.ws_keys = static_cast<uint32_t *>(workspace);
+    p.ws_bound = reinterpret_cast<float *>(static_cast<char *>(workspace) + cut.bound_off);
     p.q_dtype = q_dtype;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (summary_dtype == PKV_F16)
-        return head_dim == 64 ? launch_select<__half, 64>(p, ctas, s) : launch_select<__half, 128>(p, ctas, s);
-    return head_dim == 64 ? launch_select<__nv_bfloat16, 64>(p, ctas, s)
-                          : launch_select<__nv_bfloat16, 128>(p, ctas, s);
+        return head_dim == 64 ? launch_select<__half, 64>(p, cut.ctas, cut.cluster, s)
+                              : launch_select<__half, 128>(p, cut.ctas, cut.cluster, s);
+    return head_dim == 64 ? launch_select<__nv_bfloat16, 64>(p, cut.ctas, cut.cluster, s)
+                          : launch_select<__nv_bfloat16, 128>(p, cut.ctas, cut.cluster, s);
 }

@@ -7,18 +7,31 @@
 // Q+ = sum_g max(q_g, 0) and Q- = sum_g max(-q_g, 0) it is one product of
 // length 2 D:  score = Q+ . hi - Q- . lo.
 //
-// One cluster of C CTAs serves a (sequence, kv head).  CTA c scores the
-// consecutive blocks [c * chunk, (c + 1) * chunk), a warp eight at a time, and
-// stores the scores into the shared memory of CTA 0, which selects: scores
-// never touch HBM, and one launch does it all.
+// The scores are a matrix product on the tensor cores (m16n8k16, fp32 sums):
+// 16 blocks' summaries are A; B's columns hold the row's weights in three parts
+// of the summaries' type, 24 bits in all, and a fourth column |weights|, which
+// with |A| gives each block's error bound.  (In fp32 arithmetic a warp spent 65
+// instructions on a block -- unpacking, sums over lanes, the bound -- and 34 us
+// on 101 MB.)  A warp streams its tiles of 16 blocks through a ring of bulk
+// copies, one per summary (512 bytes at head_dim 128, in rows padded by 16
+// bytes so that ldmatrix meets no bank twice), whose first leave as soon as
+// the ids are there, before the weights are computed.  (With the tiles in
+// registers the CTAs of a wave computed weights together and waited together:
+// 30 us.)  select_row then finds the row's selection.  Two ways to run them:
+//   one launch (select_blocks_kernel): a cluster of C CTAs per row, whose
+//     warps store their scores into the shared memory of CTA 0, which selects;
+//   two (score_blocks_kernel, select_rows_kernel): scores go through the
+//     workspace, for calls whose clusters would not fill the SMs evenly
+//     (128 rows of up to 2048 blocks as clusters of four: some SMs got six CTAs
+//     and some none).
 //
 // Exactness.  Which blocks are selected is a set of whole numbers, so it must
-// not depend on how a sum was rounded.  The fp32 scores carry an error bound
-// eps = 14 2^-24 S, S >= sum_d (Q+ + Q-)_d * max|summary|_d (see kScoreErr).
-// CTA 0 finds the m-th largest fp32 score T; scores above T + 2 eps are in,
-// those below T - 2 eps are out, and only if what lies between does not fit
-// are those blocks scored again in fp64 and selected by (score, then lowest
-// block).
+// not depend on how a sum was rounded.  A score carries an error of at most
+// eps = 2^-17.5 S, S the largest sum_d |weight_d summary_d| of the row's blocks
+// (see kScoreErr).  select_row finds the m-th largest score T; scores above
+// T + 2 eps are in, those below T - 2 eps are out, and only if what lies
+// between does not fit are those blocks (a few) scored again in pairs of fp32
+// numbers (48 bits) and selected by (score, then lowest block).
 #pragma once
 
 #include <cooperative_groups.h>
@@ -38,18 +51,32 @@ struct SelectParams {
     int64_t num_blocks;
     int num_seqs, num_kv_heads, group, max_blocks_per_seq, max_context_len, block_size;
     int num_selected, keep_first, keep_last;
-    int chunk;                    // blocks per CTA
+    int chunk;                    // blocks a CTA scores
     int most;                     // blocks of max_context_len
+    int bounds;                   // warps that score a row
+    uint32_t *ws_keys;            // two launches: [B * Hk][most] scores' keys
+    float *ws_bound;              // [B * Hk][bounds]: score_blocks' results
     int q_dtype;
 };
 
+#ifndef PKV_SCORE_STAGES
+#define PKV_SCORE_STAGES 2
+#endif
+#ifndef PKV_SCORE_TILES
+#define PKV_SCORE_TILES 4
+#endif
 constexpr int kSelectThreads = 256;
+constexpr int kScoreWarps = 4;                   // warps of a scoring CTA
+constexpr int kScoreStages = PKV_SCORE_STAGES;   // tiles in flight per warp, two launches
+constexpr int kScoreTiles = PKV_SCORE_TILES;     // tiles of 16 blocks per warp, two launches
 
-// Error of an fp32 score relative to S, in roundings of 2^-24: each Q+- sums
-// its G <= 8 terms in a tree (3), a lane adds 8 products in two chains (4 + 1),
-// the sum over lanes takes at most 5: 13; one more covers the rounding of S
-// and of the edges T +- 2 eps.
-constexpr float kScoreErr = 14.0f / (1 << 24);
+// Error of a score relative to S.  A step on the tensor cores adds 16 exact
+// products and the running sum, aligned to the largest of them and cut off
+// (taken as) at one unit in its last place, 2^-23.  Eight chains of two steps
+// each: 2 x 17 x 2^-23 of what the chain adds up.  Joining the chains and the
+// three parts takes 5 roundings of 2^-24, the weights another 4 and the edges
+// T +- 2 eps two.  Together 40 x 2^-23; 44 are taken.
+constexpr float kScoreErr = 44.0f / (1 << 23);
 
 // A float's bits as an unsigned number of the same order; NaN counts as +inf.
 __device__ __forceinline__ uint32_t order_key(float x)
@@ -64,27 +91,38 @@ __device__ __forceinline__ float key_value(uint32_t k)
 {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
-__device__ __forceinline__ unsigned long long order_key64(double x)
-{
-    if (x != x)
-        x = INFINITY;
-    x += 0.0;
-    const unsigned long long b = (unsigned long long)__double_as_longlong(x);
-    return b >> 63 ? ~b : b | 1ull << 63;
-}
-
 constexpr int kSelectBins = 2048;
 constexpr int kSelectCluster = 8;   // CTAs per cluster, at most
 constexpr int kSelectList = 256;
 
-// CTA 0's shared memory before its arrays.
-struct SelectShared {
+// h + l with |l| at most half a unit of h: 48 bits.  Each operation is off by
+// a few 2^-47 of its operands.
+struct Pair {
+    float h, l;
+};
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b)
+{
+    // the sum of the high parts and its exact rounding error, then the rest
+    const float s = a.h + b.h, t = s - a.h;
+    const float e = (a.h - (s - t)) + (b.h - t) + (a.l + b.l);
+    const float h = s + e;
+    return Pair{h, e - (h - s)};
+}
+__device__ __forceinline__ Pair pair_mul(Pair a, float b)
+{
+    const float p = a.h * b, e = fmaf(a.l, b, fmaf(a.h, b, -p));
+    const float h = p + e;
+    return Pair{h, e - (h - p)};
+}
+
+// Shared memory of a CTA before its arrays.
+struct alignas(16) SelectShared {
     uint32_t hist[kSelectBins];
     uint32_t list[kSelectList];
     uint32_t scan[kSelectThreads / 32];
     uint32_t pick[4];
-    float bound[kSelectCluster];   // written by the cluster's CTAs
-    int bad[kSelectCluster];
+    float bound[kSelectCluster * kSelectThreads / 32];   // written by the cluster's warps
+    Pair weight[2 * 128];          // -Q-, Q+ for exact scores
 };
 
 // Exclusive sum of v over the CTA's threads; *total receives the sum.
@@ -169,12 +207,14 @@ __device__ uint32_t kth_largest(SelectShared *sh, const uint32_t *key, int n, ui
         // thread t adds up bins [first, first + 8), from the highest down
         constexpr int BPT = kSelectBins / kSelectThreads;
         const int first = kSelectBins - BPT * (tid + 1);
-        uint32_t h[BPT], sum = 0, total;
+        alignas(16) uint32_t h[BPT];
+        uint32_t sum = 0, total;
+        static_assert(BPT == 8, "two 16-byte reads");
+        *reinterpret_cast<uint4 *>(h) = *reinterpret_cast<const uint4 *>(sh->hist + first);
+        *reinterpret_cast<uint4 *>(h + 4) = *reinterpret_cast<const uint4 *>(sh->hist + first + 4);
 #pragma unroll
-        for (int k = 0; k < BPT; ++k) {
-            h[k] = sh->hist[first + k];
+        for (int k = 0; k < BPT; ++k)
             sum += h[k];
-        }
         uint32_t above = cta_exclusive(sum, sh->scan, &total);
         if (above < m && m <= above + sum) {
 #pragma unroll
@@ -234,165 +274,246 @@ __device__ __forceinline__ float select_q(const SelectParams &p, int64_t i)
                                 : to_float(static_cast<const __nv_bfloat16 *>(p.q)[i]);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kSelectThreads)
-select_blocks_kernel(const __grid_constant__ SelectParams p)
+template <typename T> __device__ __forceinline__ T from_float(float x);
+template <> __device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// A row's number of blocks; a refused length has none (`report`: says so).
+__device__ __forceinline__ int row_blocks(const SelectParams &p, int L, bool tell)
 {
-    namespace cg = cooperative_groups;
-    cg::cluster_group cluster = cg::this_cluster();
-    constexpr int HALF = D / 8;              // lanes that hold one of a summary's two rows
-    constexpr int LPB = 2 * HALF;            // lanes per block
-    constexpr int BPW = 32 / LPB;            // blocks of one load
-    constexpr int U = 8;                     // loads in flight
-    constexpr int NW = kSelectThreads / 32;
-    extern __shared__ __align__(16) uint8_t smem[];
-    SelectShared *sh = reinterpret_cast<SelectShared *>(smem);
-    float *qsum = reinterpret_cast<float *>(smem + sizeof(SelectShared));   // Q+ [D], Q- [D]
-    int32_t *phys = reinterpret_cast<int32_t *>(qsum + 2 * D);              // [chunk]
-    uint32_t *key = reinterpret_cast<uint32_t *>(phys + p.chunk);           // [most], CTA 0's in use
-    uint32_t *in = key + p.most;                                            // bit i: block i is selected
-    uint32_t *pend = in + (p.most + 31) / 32;                               // bit i: block i is in doubt
-
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int me = (int)cluster.block_rank(), C = (int)cluster.num_blocks();
-    const int kvh = blockIdx.y, seq = blockIdx.z;
-    cluster.barrier_arrive();   // CTA 0 has started once this completes: its memory may be written
-    const int L = p.context_lens[seq];
-    const bool bad_len = L < 0 || L > p.max_context_len;
-    if (bad_len && kvh == 0 && me == 0 && tid == 0)
-        report(p.status, PKV_DEV_BAD_CONTEXT_LEN);
-    const int n = bad_len ? 0 : (L + p.block_size - 1) / p.block_size;
-    const int K = p.num_selected;
-    const int b0 = min(me * p.chunk, n);
-    const int mine = min(p.chunk, n - b0);
-    const int32_t *table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
-    const int64_t q0 = ((int64_t)seq * p.num_kv_heads + kvh) * p.group * D;
-
-    int bad = 0;
-    for (int i = tid; i < mine; i += kSelectThreads) {
-        int b = table[b0 + i];
-        if (b < 0 || (int64_t)b >= p.num_blocks) {
-            bad = 1;
-            b = 0;
-        }
-        phys[i] = b;
+    if (L < 0 || L > p.max_context_len) {
+        if (tell)
+            report(p.status, PKV_DEV_BAD_CONTEXT_LEN);
+        return 0;
     }
-    if (n > K && tid < D) {
+    return (L + p.block_size - 1) / p.block_size;
+}
+
+constexpr float kBadChunk = -1.f;
+
+// Shared memory of a scoring CTA of NW warps with rings of S tiles: the
+// weights [part][2 D] in the summaries' type -- three parts of -Q- (minima) and
+// Q+ (maxima), and a bound of their magnitude -- and the rings.
+template <int D, int NW, int S>
+struct alignas(16) ScoreShared {
+    static constexpr int LINE = 4 * D + 16;      // bytes from one summary of a tile to the next
+    uint8_t ring[NW][S][16 * LINE];
+    uint16_t part[4][2 * D + 8];
+    uint64_t bar[NW][S];
+    uint32_t big[NW];
+};
+
+// Untiled bulk copy global -> shared with mbarrier byte accounting; addresses
+// and size in multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(void *dst_smem, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst_smem)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// Keys of blocks [b0, b0 + p.chunk) of row (seq, kvh) into keys[0 ..], by a CTA
+// of NW warps.  Returns each warp's S (in units of the weights' scale), or
+// kBadChunk if one of its blocks' ids is outside the pool or a copy timed out;
+// nothing is scored in a row that is selected whole.  n receives the row's
+// number of blocks; before_stores() runs before the first store.
+template <typename T, int D, int NW, int ST, typename Before>
+__device__ __forceinline__ float score_blocks(const SelectParams &p, ScoreShared<D, NW, ST> *sw, int seq, int kvh, int b0,
+                                              uint32_t *keys, int &n, bool tell, Before before_stores)
+{
+    using Sh = ScoreShared<D, NW, ST>;
+    constexpr int KS = 2 * D / 16;           // k steps
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, c = lane & 3;
+    uint64_t *bar = sw->bar[warp];
+    // what needs only the arguments leaves at once: the length, the first
+    // tiles' ids (as far as the table goes; lane i holds block i of a tile)
+    // and q
+    const int L = p.context_lens[seq];
+    const int32_t *table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq + b0;
+    const int there = lane < 16 ? min(p.chunk, p.max_blocks_per_seq - b0) : 0;
+    int id[ST];
+#pragma unroll
+    for (int k = 0; k < ST; ++k) {
+        const int i = (warp + k * NW) * 16 + lane;
+        id[k] = i < there ? table[i] : 0;
+    }
+    float x[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+        x[h] = tid < D && h < p.group ? select_q(p, (((int64_t)seq * p.num_kv_heads + kvh) * p.group + h) * D + tid) : 0.f;
+    if (lane == 0) {
+        for (int s = 0; s < ST; ++s)
+            mbar_init(&bar[s], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+
+    n = row_blocks(p, L, tell);
+    const int mine = max(0, min(p.chunk, n - b0));
+    const int tiles = (mine + 15) / 16, my_n = warp < tiles ? (tiles - 1 - warp) / NW + 1 : 0;
+    const bool score = n > p.num_selected && mine > 0;
+    bool bad = false;
+    const uint8_t *sums = reinterpret_cast<const uint8_t *>(p.summaries) + (int64_t)kvh * (4 * D);
+    const int64_t stride = (int64_t)p.num_kv_heads * (4 * D);
+    // the warp's k-th tile into stage k % ST
+    auto issue = [&](int k, int block) {
+        const int i0 = (warp + k * NW) * 16, live = min(16, mine - i0);
+        const bool good = block >= 0 && (int64_t)block < p.num_blocks;
+        bad |= lane < live && !good;
+        if (!score)
+            return;
+        uint64_t *b = &bar[k % ST];
+        if (lane == 0)
+            mbar_arrive_expect_tx(b, (uint32_t)(live * 4 * D));
+        __syncwarp();
+        if (lane < live)
+            bulk_load(&sw->ring[warp][k % ST][lane * Sh::LINE], sums + (good ? block : 0) * stride, 4 * D, b);
+    };
+#pragma unroll
+    for (int k = 0; k < ST; ++k)
+        if (k < my_n)
+            issue(k, id[k]);
+
+    uint32_t bf[KS][2];   // B fragments: column g of k step ks
+    if (score) {
         float up[8], down[8];
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-            const float x = g < p.group ? select_q(p, q0 + (int64_t)g * D + tid) : 0.f;
+        for (int h = 0; h < 8; ++h) {
             // NaN goes into both sums
-            up[g] = x < 0.f ? 0.f : x;
-            down[g] = x > 0.f ? 0.f : -x;
+            up[h] = x[h] < 0.f ? 0.f : x[h];
+            down[h] = x[h] > 0.f ? 0.f : -x[h];
         }
 #pragma unroll
         for (int k = 4; k >= 1; k >>= 1) {
 #pragma unroll
-            for (int g = 0; g < k; ++g) {
-                up[g] += up[g + k];
-                down[g] += down[g + k];
+            for (int h = 0; h < k; ++h) {
+                up[h] += up[h + k];
+                down[h] += down[h + k];
             }
         }
-        qsum[tid] = up[0];
-        qsum[D + tid] = down[0];
-    }
-    bad = __syncthreads_or(bad);
-    cluster.barrier_wait();
-
-    // ---- scores, into CTA 0's shared memory
-    float S = 0.f;
-    if (n > K && !bad) {
-        uint32_t *keys = cluster.map_shared_rank(key, 0) + b0;
-        const bool is_lo = (lane % LPB) < HALF;
-        const int c8 = (lane % HALF) * 8;
-        float w[8];   // this lane's weights: -Q- on the minima, Q+ on the maxima
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            w[k] = is_lo ? -qsum[D + c8 + k] : qsum[c8 + k];
-        using V = typename Pair16<T>::V;
-        V biggest[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            biggest[k] = as_pair<T>(0u);
-        const uint4 *sums = reinterpret_cast<const uint4 *>(p.summaries) + kvh * LPB + lane % LPB;
-        const int64_t stride = (int64_t)p.num_kv_heads * LPB;
-        for (int i0 = warp * U * BPW; i0 < mine; i0 += NW * U * BPW) {
-            uint4 x[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = i0 + u * BPW + lane / LPB;
-                x[u] = make_uint4(0, 0, 0, 0);
-                if (i < mine)
-                    x[u] = __ldg(sums + phys[i] * stride);
-            }
-            float s[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint32_t word[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-                float2 two = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    two = ffma2(make_float2(w[2 * k], w[2 * k + 1]), Unpack<T>::pair(word[k]), two);
-                    biggest[k] = __hmax2(biggest[k], as_pair<T>(word[k] & 0x7fff7fffu));
-                }
-                s[u] = two.x + two.y;
-            }
-            // sums over a block's lanes: the halves of the lanes take halves
-            // of the blocks until each lane has one, then add up the rest
-            int u0 = 0;
-#pragma unroll
-            for (int k = U / 2, off = LPB / 2; k >= 1; k >>= 1, off >>= 1) {
-                const bool up = lane & off;
-#pragma unroll
-                for (int u = 0; u < k; ++u) {
-                    const float give = up ? s[u] : s[u + k];
-                    const float keep = up ? s[u + k] : s[u];
-                    s[u] = keep + __shfl_xor_sync(0xffffffffu, give, off);
-                }
-                u0 += up ? k : 0;
-            }
-#pragma unroll
-            for (int off = LPB / 2 / U; off >= 1; off >>= 1)
-                s[0] += __shfl_xor_sync(0xffffffffu, s[0], off);
-            const int i = i0 + u0 * BPW + lane / LPB;
-            if (i < mine && lane % (LPB / U) == 0)
-                keys[i] = order_key(s[0]);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 f = Unpack<T>::pair(as_word(biggest[k]));
-            S += fabsf(w[2 * k]) * f.x;
-            S += fabsf(w[2 * k + 1]) * f.y;
-        }
-#pragma unroll
-        for (int off = 1; off < LPB; off <<= 1)
-            S += __shfl_xor_sync(0xffffffffu, S, off);
-        // NaN and infinity order above every number
-        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(S) & 0x7fffffffu);
+        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(up[0], down[0])));
         if (lane == 0)
-            sh->scan[warp] = most;
+            sw->big[warp] = most;
         __syncthreads();
         uint32_t all = 0;
 #pragma unroll
         for (int k = 0; k < NW; ++k)
-            all = max(all, sh->scan[k]);
-        S = __uint_as_float(all);
+            all = max(all, sw->big[k]);
+        // the largest weight to [2^14, 2^15), inside both types' range
+        const int e = min(max((int)(all >> 23) - 127 - 14, -120), 120);
+        const float scale = __uint_as_float((uint32_t)(127 - e) << 23);
+        if (tid < D) {
+            auto split = [&](float w, int at) {
+                T one;
+                float rest = w;
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    one = from_float<T>(rest);
+                    sw->part[k][at] = *reinterpret_cast<const uint16_t *>(&one);
+                    rest -= to_float(one);
+                }
+                // an upper bound, also of what the three parts leave out
+                one = from_float<T>(fabsf(w) * 1.015625f + 0x1p-9f);
+                sw->part[3][at] = *reinterpret_cast<const uint16_t *>(&one);
+            };
+            split(-down[0] * scale, tid);
+            split(up[0] * scale, D + tid);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(sw->part[g & 3]) + 8 * ks + c;
+            bf[ks][0] = g < 4 ? w[0] : 0u;
+            bf[ks][1] = g < 4 ? w[4] : 0u;
+        }
     }
-    if (tid == 0) {
-        SelectShared *to = cluster.map_shared_rank(sh, 0);
-        to->bound[me] = S;
-        to->bad[me] = bad;
-    }
-    cluster.sync();
-    if (me != 0)
-        return;
+    before_stores();
 
-    // ---- CTA 0 selects
-    S = 0.f;
-    for (int c = 0; c < C; ++c) {
-        S = !(sh->bound[c] <= 3.0e38f) ? INFINITY : fmaxf(S, sh->bound[c]);
-        bad |= sh->bad[c];
+    uint32_t S = 0;   // as its bits: NaN and infinity order above every number
+    // this lane's ldmatrix row in a tile
+    const uint32_t row = ((lane & 7) + ((lane >> 3) & 1) * 8) * Sh::LINE + (lane >> 4) * 16;
+    for (int k = 0; k < my_n; ++k) {
+        const int i0 = (warp + k * NW) * 16, st = k % ST;
+        const int i_next = i0 + ST * NW * 16 + lane;
+        const int next = k + ST < my_n && i_next < there ? table[i_next] : 0;
+        if (score) {
+            if (!mbar_wait_bounded(&bar[st], (uint32_t)((k / ST) & 1))) {
+                // no CTA leaves with copies in flight
+                for (int u = k; u < min(my_n, k + ST); ++u)
+                    drain_wait(&bar[u % ST], (uint32_t)((u / ST) & 1), p.status);
+                if (lane == 0)
+                    report(p.status, PKV_DEV_TIMEOUT);
+                return kBadChunk;
+            }
+            const uint32_t base = smem_u32(sw->ring[warp][st]) + row;
+            float s[8][4], b[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                constexpr int PER = KS / 8;   // steps of a chain
+                uint32_t a[4];
+                ldsm_x4(base + ks * 32, a);
+                if (ks % PER == 0)
+                    s[ks / PER][0] = s[ks / PER][1] = s[ks / PER][2] = s[ks / PER][3] = 0.f;
+                Mma<T>::run(s[ks / PER], a, bf[ks][0], bf[ks][1]);
+                // rows past the last block hold anything: theirs alone are wrong
+                const uint32_t m[4] = {a[0] & 0x7fff7fffu, a[1] & 0x7fff7fffu, a[2] & 0x7fff7fffu, a[3] & 0x7fff7fffu};
+                Mma<T>::run(b, m, bf[ks][0], bf[ks][1]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                s[0][j] = ((s[0][j] + s[1][j]) + (s[2][j] + s[3][j])) + ((s[4][j] + s[5][j]) + (s[6][j] + s[7][j]));
+            // columns 0, 1 are in lane c = 0, columns 2, 3 in lane c = 1
+            const float p0 = __shfl_down_sync(0xffffffffu, s[0][0], 1), p1 = __shfl_down_sync(0xffffffffu, s[0][2], 1);
+            const float m0 = __shfl_down_sync(0xffffffffu, b[1], 1), m1 = __shfl_down_sync(0xffffffffu, b[3], 1);
+            if (c == 0) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int i = i0 + g + 8 * h;
+                    if (i < mine) {
+                        keys[i] = order_key((s[0][2 * h] + s[0][2 * h + 1]) + (h ? p1 : p0));
+                        S = max(S, __float_as_uint(h ? m1 : m0) & 0x7fffffffu);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        if (k + ST < my_n) {
+            if (lane < 16)
+                fence_proxy_async_smem();
+            issue(k + ST, next);
+        }
+    }
+    if (__any_sync(0xffffffffu, bad))
+        return kBadChunk;
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, S));
+}
+
+// The selection of row (seq, kvh) of n blocks from its keys and its chunks'
+// bounds, by one CTA.  in, pend: a bit for each block.
+template <typename T, int D>
+__device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *sh, uint32_t *key, uint32_t *in,
+                                           uint32_t *pend, const float *bounds, int seq, int kvh, int n)
+{
+    constexpr int NW = kSelectThreads / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int K = p.num_selected;
+    const int32_t *table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
+    const int64_t q0 = ((int64_t)seq * p.num_kv_heads + kvh) * p.group * D;
+    // the chunks' bounds, a lane each: NaN and infinity order above numbers
+    float S;
+    bool bad = false;
+    {
+        uint32_t most = 0;
+        for (int c = lane; c < p.bounds; c += 32) {
+            const float x = bounds[c];
+            bad |= x == kBadChunk;
+            most = max(most, __float_as_uint(x) & 0x7fffffffu);
+        }
+        bad = __any_sync(0xffffffffu, bad);
+        S = __uint_as_float(__reduce_max_sync(0xffffffffu, most));
+        S = !(S <= 3.0e38f) ? INFINITY : S;
     }
     int32_t *out = p.selected + ((int64_t)seq * p.num_kv_heads + kvh) * K;
     if (bad || n <= K) {
@@ -438,31 +559,62 @@ select_blocks_kernel(const __grid_constant__ SelectParams p)
     (void)cta_exclusive(doubt, sh->scan, &doubt_total);
     ties = m - sure_total;
     if (doubt_total > ties && S > 0.f) {
-        // The blocks in doubt by their fp64 scores.
+        // the blocks in doubt by their exact scores: weights in pairs first,
+        // brought to about 1 by a power of two; summaries too, by 2^-64,
+        // where S is huge or overflowed
+        float x[8], big = 0.f;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+            x[g] = tid < D && g < p.group ? select_q(p, q0 + (int64_t)g * D + tid) : 0.f;
+            big = fmaxf(big, fabsf(x[g]));
+        }
+        {
+            const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+            __syncthreads();
+            if (lane == 0)
+                sh->scan[warp] = most;
+            __syncthreads();
+            uint32_t all = 0;
+            for (int k = 0; k < NW; ++k)
+                all = max(all, sh->scan[k]);
+            big = __uint_as_float(all);
+        }
+        const int up = min(max((int)(__float_as_uint(big) >> 23) - 127 + 3, -120), 120);
+        const float w_scale = __uint_as_float((uint32_t)(127 - up) << 23);
+        const float v_scale = S < 0x1p75f ? 1.f : 0x1p-64f;   // S is for weights up to 2^15
+        if (tid < D) {
+            Pair lo{0.f, 0.f}, hi{0.f, 0.f};
+#pragma unroll 1
+            for (int g = 0; g < 8; ++g) {
+                const float y = x[0] * w_scale;
+#pragma unroll
+                for (int k = 0; k < 7; ++k)
+                    x[k] = x[k + 1];
+                lo = pair_add(lo, Pair{y > 0.f ? 0.f : y, 0.f});
+                hi = pair_add(hi, Pair{y < 0.f ? 0.f : y, 0.f});
+            }
+            sh->weight[tid] = lo;
+            sh->weight[D + tid] = hi;
+        }
+        __syncthreads();
         auto exact = [&](int i) -> unsigned long long {   // by a warp
-            double s = 0.0;
-            const int64_t at = ((int64_t)table[i] * p.num_kv_heads + kvh) * 2 * D;
-            double wgt[2 * D / 32], v[2 * D / 32];
-#pragma unroll
-            for (int k = 0; k < 2 * D / 32; ++k) {
-                v[k] = (double)to_float(static_cast<const T *>(p.summaries)[at + k * 32 + lane]);
-                wgt[k] = 0.0;
-            }
-            for (int g = 0; g < p.group; ++g) {
-#pragma unroll
-                for (int k = 0; k < D / 32; ++k) {
-                    const float x = select_q(p, q0 + (int64_t)g * D + k * 32 + lane);
-                    wgt[k] += x > 0.f ? 0.f : x;
-                    wgt[k + D / 32] += x < 0.f ? 0.f : x;
-                }
-            }
+            const int64_t at = ((int64_t)table[i] * p.num_kv_heads + kvh) * 2 * D + lane;
+            float v[2 * D / 32];
 #pragma unroll
             for (int k = 0; k < 2 * D / 32; ++k)
-                s += wgt[k] * v[k];
+                v[k] = to_float(static_cast<const T *>(p.summaries)[at + k * 32]) * v_scale;
+            Pair s{0.f, 0.f};
+#pragma unroll 1
+            for (int k = 0; k < 2 * D / 32; ++k) {
+                s = pair_add(s, pair_mul(sh->weight[k * 32 + lane], v[0]));
 #pragma unroll
+                for (int j = 0; j + 1 < 2 * D / 32; ++j)
+                    v[j] = v[j + 1];
+            }
+#pragma unroll 1
             for (int off = 16; off > 0; off >>= 1)
-                s += __shfl_xor_sync(0xffffffffu, s, off);
-            return order_key64(s);
+                s = pair_add(s, Pair{__shfl_xor_sync(0xffffffffu, s.h, off), __shfl_xor_sync(0xffffffffu, s.l, off)});
+            return (unsigned long long)order_key(s.h) << 32 | order_key(fabsf(s.h) < INFINITY ? s.l : 0.f);
         };
         if (doubt_total <= kSelectList) {
             // a few (two, mostly): listed in ascending order, ranked against each other
@@ -556,9 +708,94 @@ select_blocks_kernel(const __grid_constant__ SelectParams p)
     }
     uint32_t at = cta_exclusive(c, sh->scan, &total);
     for (int k = w0; k < w1; ++k) {
-        for (uint32_t w = in[k]; w; w &= w - 1)
-            out[at++] = k * 32 + __ffs(w) - 1;
+        pend[k] = at;   // selected blocks before the word's
+        at += __popc(in[k]);
     }
+    __syncthreads();
+    for (int i = tid; i < n; i += kSelectThreads) {
+        const uint32_t w = in[i / 32];
+        if (w >> (i % 32) & 1u)
+            out[pend[i / 32] + __popc(w & ((1u << (i % 32)) - 1u))] = i;
+    }
+}
+
+// One launch: a cluster per row; grid (CTAs of a row, kv head, sequence).
+template <typename T, int D>
+__global__ void __launch_bounds__(kSelectThreads)
+select_blocks_kernel(const __grid_constant__ SelectParams p)
+{
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    constexpr int NW = kSelectThreads / 32;
+    extern __shared__ __align__(16) uint8_t smem[];
+    SelectShared *sh = reinterpret_cast<SelectShared *>(smem);
+    using Score = ScoreShared<D, NW, 1>;
+    Score *sw = reinterpret_cast<Score *>(smem + sizeof(SelectShared));
+    uint32_t *key = reinterpret_cast<uint32_t *>(smem + sizeof(SelectShared) + sizeof(Score));   // [most], CTA 0's in use
+    uint32_t *in = key + p.most;                                            // bit i: block i is selected
+    uint32_t *pend = in + (p.most + 31) / 32;                               // bit i: block i is in doubt
+    const int me = (int)cluster.block_rank(), kvh = blockIdx.y, seq = blockIdx.z;
+    cluster.barrier_arrive();   // CTA 0 has started once this completes: its memory may be written
+    int n;
+    const float S = score_blocks<T, D, NW, 1>(p, sw, seq, kvh, me * p.chunk, cluster.map_shared_rank(key, 0) + me * p.chunk, n,
+                                           kvh == 0 && me == 0 && threadIdx.x == 0, [&] { cluster.barrier_wait(); });
+    if ((threadIdx.x & 31) == 0)
+        cluster.map_shared_rank(sh, 0)->bound[me * NW + (threadIdx.x >> 5)] = S;
+    cluster.sync();
+    if (me == 0)
+        select_row<T, D>(p, sh, key, in, pend, sh->bound, seq, kvh, n);
+}
+
+// Two launches: scores into the workspace; grid (kv head, chunk, sequence), so
+// that the CTAs that read neighbouring parts of a block's summaries run
+// together.
+template <typename T, int D>
+__global__ void __launch_bounds__(kScoreWarps * 32)
+score_blocks_kernel(const __grid_constant__ SelectParams p)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    using Score = ScoreShared<D, kScoreWarps, kScoreStages>;
+    Score *sw = reinterpret_cast<Score *>(smem);
+    const int kvh = blockIdx.x, me = blockIdx.y, seq = blockIdx.z;
+    const int64_t row = (int64_t)seq * p.num_kv_heads + kvh;
+    int n;
+    const float S = score_blocks<T, D, kScoreWarps, kScoreStages>(p, sw, seq, kvh, me * p.chunk, p.ws_keys + row * p.most + me * p.chunk, n,
+                                                    false, [] {});
+    if ((threadIdx.x & 31) == 0)
+        p.ws_bound[row * p.bounds + me * kScoreWarps + (threadIdx.x >> 5)] = S;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// The second launch, a programmatic dependent of the first: grid (kv head,
+// sequence).
+template <typename T, int D>
+__global__ void __launch_bounds__(kSelectThreads)
+select_rows_kernel(const __grid_constant__ SelectParams p)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    SelectShared *sh = reinterpret_cast<SelectShared *>(smem);
+    uint32_t *key = reinterpret_cast<uint32_t *>(smem + sizeof(SelectShared));   // [most]
+    uint32_t *in = key + p.most;
+    uint32_t *pend = in + (p.most + 31) / 32;
+    const int kvh = blockIdx.x, seq = blockIdx.y;
+    const int64_t row = (int64_t)seq * p.num_kv_heads + kvh;
+    const int n = row_blocks(p, p.context_lens[seq], kvh == 0 && threadIdx.x == 0);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (n > p.num_selected) {
+        const uint32_t *src = p.ws_keys + row * p.most;
+        for (int i0 = threadIdx.x; i0 < n; i0 += kSelectThreads * 8) {
+            uint32_t k[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                k[u] = i0 + u * kSelectThreads < n ? __ldcg(src + i0 + u * kSelectThreads) : 0u;
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (i0 + u * kSelectThreads < n)
+                    key[i0 + u * kSelectThreads] = k[u];
+        }
+    }
+    __syncthreads();
+    select_row<T, D>(p, sh, key, in, pend, p.ws_bound + row * p.bounds, seq, kvh, n);
 }
 
 }  // namespace pkv

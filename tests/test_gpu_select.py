@@ -175,6 +175,33 @@ def test_select_nan_and_infinities():
     np.testing.assert_array_equal(got, want_select(c, 12, 1, 1))
 
 
+def test_select_through_the_workspace():
+    """Many rows of many blocks: scored by one launch, selected by another.
+    Lengths from 0 on, a sequence of equal blocks, NaN, a bad table and a bad
+    length among them; the workspace given and not."""
+    rng = np.random.RandomState(2)
+    lens = rng.randint(1, 400 * 8, 28)
+    lens[3], lens[5], lens[7] = 0, 400 * 8, 399 * 8 + 1
+    c = select_case(12, lens, G=2, Hk=4, D=64, bs=8, t="bf16")
+    assert pkv.select_blocks_workspace_bytes(28, 4, 400 * 8, 8) > 0
+    t = c["tables"]
+    c["sums"][t[5, :400]] = c["sums"][t[5, 0]].clone()
+    c["sums"][t[7, 100], 2, 0, 5] = float("nan")
+    for K in (3, 48, 200):
+        got, st = run_select(c, K, 1, 2, max_len=400 * 8)
+        assert st == 0
+        np.testing.assert_array_equal(got, want_select(c, K, 1, 2))
+    ws = torch.full((pkv.select_blocks_workspace_bytes(28, 4, 400 * 8, 8),), 255, dtype=torch.uint8, device=DEV)
+    sel, st = torch.zeros(28, 4, 48, dtype=torch.int32, device=DEV), status()
+    good, _ = run_select(c, 48, 0, 1, max_len=400 * 8)
+    c["tables"][11, (lens[11] - 1) // 8], c["lens"][12] = -1, 401 * 8
+    pkv.select_blocks(sel, c["q"].to(DEV), c["sums"].to(DEV), dev(c["tables"]), dev(c["lens"]), 8, keep_first=0, keep_last=1,
+                      max_context_len=400 * 8, workspace=ws, device_status=st)
+    assert st.item() == pkv.DEV_BAD_BLOCK | pkv.DEV_BAD_CONTEXT_LEN
+    good[[11, 12]] = -1
+    np.testing.assert_array_equal(sel.cpu().numpy(), good)
+
+
 def test_select_refuses_bad_rows():
     c = select_case(8, [3000, 3000, 3000, 3000])
     good, _ = run_select(c, 16)

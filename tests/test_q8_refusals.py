@@ -60,11 +60,11 @@ def test_summarize_host_checks(lib, kw, code):
 
 
 def select(lib, **kw):
-    a = dict(sel=A, q=A, qdt=1, sm=A, sdt=2, bt=A, mb=64, cl=A, B=2, H=8, Hk=2, D=128, bs=16, NB=64, maxL=1000, K=8, first=1, last=2)
+    a = dict(sel=A, q=A, qdt=1, sm=A, sdt=2, bt=A, mb=64, cl=A, B=2, H=8, Hk=2, D=128, bs=16, NB=64, maxL=1000, K=8, first=1, last=2, ws=None, wsb=0)
     a.update(kw)
     return lib.pkv_select_blocks(vp(a["sel"]), vp(a["q"]), a["qdt"], vp(a["sm"]), a["sdt"], vp(a["bt"]), a["mb"], vp(a["cl"]),
                                  a["B"], a["H"], a["Hk"], a["D"], a["bs"], a["NB"], a["maxL"], a["K"], a["first"], a["last"],
-                                 None, None)
+                                 a["ws"], a["wsb"], None, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -72,6 +72,8 @@ def select(lib, **kw):
     (dict(first=-1), EINVAL), (dict(last=2147483647), EINVAL), (dict(qdt=0), EUNSUPPORTED), (dict(sdt=0), EUNSUPPORTED),
     (dict(qdt=3), EINVAL), (dict(D=32), EUNSUPPORTED), (dict(mb=1 << 20, maxL=40961 * 16), EUNSUPPORTED),
     (dict(sel=0), EINVAL), (dict(q=A + 4), EINVAL), (dict(B=65536), EUNSUPPORTED), (dict(B=0, sel=0), 0),
+    (dict(B=4096, mb=4096, maxL=65536), EWORKSPACE), (dict(B=4096, mb=4096, maxL=65536, ws=vp(A), wsb=4096 * 2 * 4096), EWORKSPACE),
+    (dict(B=4096, mb=4096, maxL=65536, ws=vp(A + 8), wsb=1 << 40), EWORKSPACE),
 ])
 def test_select_host_checks(lib, kw, code):
     assert select(lib, **kw) == code
@@ -121,6 +123,14 @@ def test_list_workspace(lib):
     assert w(2, 4, 2, 128, 16, 7, 1024) == 0
     assert w(0, 4, 2, 128, 16, 7, 0) == 0 and w(2, 4, 2, 128, 16, 7, 40) == 0 and w(2, 4, 2, 128, 16, 0, 0) == 0
     assert w(65535, 65535, 8191, 128, 8, 1 << 28, 32) == 0     # past 64 bits: the call then refuses
+
+
+def test_select_workspace(lib):
+    w = lib.pkv_select_blocks_workspace_bytes
+    assert w(4, 8, 8192, 16) == 0                                       # one launch
+    # 4096 keys of each of 16 x 8 rows, then a bound for each 64 of them (a warp's)
+    assert w(16, 8, 65536, 16) == 128 * 4096 * 4 + 128 * 64 * 4
+    assert w(0, 8, 65536, 16) == 0 and w(16, 8, 40961 * 16, 16) == 0
 
 
 def test_binding_refuses_host_tensors():
