@@ -15,6 +15,8 @@ namespace {
 constexpr int kSelectMaxBlocks = 40960;   // a row's scores fit one CTA's shared memory
 constexpr int kSelectOneBlocks = 2048;    // of a row in one launch
 
+int key_stride(int n) { return (n + 3) / 4 * 4; }
+
 // How a call runs: `ctas` CTAs score `chunk` blocks of a row each, in one
 // launch as a cluster or in two through the workspace.
 struct SelectCut {
@@ -43,13 +45,13 @@ SelectCut select_cut(int64_t rows, int most)
         c.chunk = kScoreWarps * kScoreTiles * 16;
         c.ctas = (n + c.chunk - 1) / c.chunk;
         c.bounds = c.ctas * kScoreWarps;
-        c.bound_off = ((size_t)rows * n * 4 + 255) & ~size_t(255);
+        c.bound_off = ((size_t)rows * key_stride(n) * 4 + 255) & ~size_t(255);
         c.total = c.bound_off + (size_t)rows * c.bounds * 4;
     }
     return c;
 }
 
-size_t row_smem(int most) { return sizeof(SelectShared) + (size_t)most * 4 + (size_t)(most + 31) / 32 * 8; }
+size_t row_smem(int most) { return sizeof(SelectShared) + (size_t)key_stride(most) * 4 + (size_t)(most + 31) / 32 * 8; }
 
 template <typename T, int D>
 int launch_select(const SelectParams &p, int ctas, bool one, cudaStream_t stream)
@@ -156,6 +158,7 @@ extern "C" int pkv_select_blocks(int32_t *selected, const void *q, int q_dtype, 
     p.keep_first = keep_first;
     p.keep_last = keep_last;
     p.most = most;
+    p.key_stride = key_stride(most > 0 ? most : 1);
     p.chunk = cut.chunk;
     p.bounds = cut.bounds;
     p.ws_keys = static_cast<uint32_t *>(workspace);

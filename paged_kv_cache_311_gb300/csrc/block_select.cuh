@@ -53,8 +53,9 @@ struct SelectParams {
     int num_selected, keep_first, keep_last;
     int chunk;                    // blocks a CTA scores
     int most;                     // blocks of max_context_len
+    int key_stride;               // keys of a row, whole 16-byte pieces
     int bounds;                   // warps that score a row
-    uint32_t *ws_keys;            // two launches: [B * Hk][most] scores' keys
+    uint32_t *ws_keys;            // two launches: [B * Hk][key_stride] scores' keys
     float *ws_bound;              // [B * Hk][bounds]: score_blocks' results
     int q_dtype;
 };
@@ -63,7 +64,7 @@ struct SelectParams {
 #define PKV_SCORE_STAGES 2
 #endif
 #ifndef PKV_SCORE_TILES
-#define PKV_SCORE_TILES 4
+#define PKV_SCORE_TILES 8
 #endif
 constexpr int kSelectThreads = 256;
 constexpr int kScoreWarps = 4;                   // warps of a scoring CTA
@@ -121,150 +122,143 @@ struct alignas(16) SelectShared {
     uint32_t list[kSelectList];
     uint32_t scan[kSelectThreads / 32];
     uint32_t pick[4];
+    uint64_t bar;
     float bound[kSelectCluster * kSelectThreads / 32];   // written by the cluster's warps
     Pair weight[2 * 128];          // -Q-, Q+ for exact scores
 };
 
+// The code of a selection runs once per CTA, so its time is that of fetching
+// it (128 bytes of instructions in some 45 cycles): loops stay rolled and
+// what is used twice is a function.
+
 // Exclusive sum of v over the CTA's threads; *total receives the sum.
-__device__ __forceinline__ uint32_t cta_exclusive(uint32_t v, uint32_t *warp_sums, uint32_t *total)
+__device__ __noinline__ uint32_t cta_exclusive(uint32_t v, uint32_t *warp_sums, uint32_t *total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t x = v;
-#pragma unroll
+#pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, x, off);
-        if (lane >= off)
-            x += y;
+        x += lane >= off ? y : 0u;
     }
     __syncthreads();   // the sums of an earlier call are read
     if (lane == 31)
         warp_sums[warp] = x;
     __syncthreads();
-    uint32_t before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kSelectThreads / 32; ++w) {
-        if (w < warp)
-            before += warp_sums[w];
-        all += warp_sums[w];
-    }
-    *total = all;
-    return before + x - v;
+    // a warp's lanes hold the warps' sums
+    const uint32_t s = lane < kSelectThreads / 32 ? warp_sums[lane] : 0u;
+    *total = __reduce_add_sync(0xffffffffu, s);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? s : 0u) + x - v;
 }
 
-// The m-th largest (1 <= m <= number of live entries) of key[i], i in [0, n),
-// live(i); *left = how many of the entries equal to it are among the m
-// largest.  Each round spreads what is left over 2048 bins between its
-// smallest and largest key -- scores of one row share their leading bits, and
-// bins of fixed bits would put them all into a few, whose atomics then queue
-// -- and keeps the bin of the m-th; once at most 256 keys are left, each is
-// ranked against all.
-template <typename Live>
-__device__ uint32_t kth_largest(SelectShared *sh, const uint32_t *key, int n, uint32_t m, Live live, uint32_t *left)
+// The m-th largest (1 <= m <= their number) of the keys i in [first, last)
+// whose bit is set in `mask` (null: all); *left = how many of those equal to it
+// are among the m largest.  Each round spreads what is left over 2048 bins
+// between its smallest and largest key -- scores of one row share their
+// leading bits, and bins of fixed bits would put them all into a few, whose
+// atomics then queue -- and keeps the bin of the m-th; once at most 256 keys
+// are left, each is ranked against all.
+__device__ __noinline__ uint32_t kth_largest(SelectShared *sh, const uint32_t *key, int first, int last, const uint32_t *mask,
+                                             uint32_t m, uint32_t *left)
 {
     const int tid = threadIdx.x;
     uint32_t lo = 0xffffffffu, hi = 0;
-    for (int i = tid; i < n; i += kSelectThreads) {
-        if (live(i)) {
-            lo = min(lo, key[i]);
-            hi = max(hi, key[i]);
+    // 0: the range; 1: the histogram; 2: the keys of the bin
+    auto pass = [&](int what, uint32_t from, uint32_t to, int shift) {
+#pragma unroll 2
+        for (int i = first + tid; i < last; i += kSelectThreads) {
+            const uint32_t k = key[i];
+            if ((mask && !(mask[i / 32] >> (i % 32) & 1u)) || k < from || k > to)
+                continue;
+            if (what == 0) {
+                lo = min(lo, k);
+                hi = max(hi, k);
+            } else if (what == 1) {
+                atomicAdd(&sh->hist[(k - from) >> shift], 1u);
+            } else {
+                sh->list[atomicAdd(&sh->pick[3], 1u)] = k;   // equal keys are alike: their order does not matter
+            }
         }
-    }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
+    };
+    uint32_t from = 0, to = 0xffffffffu;
+    int what = 0, shift = 0;
     __syncthreads();
     if (tid == 0) {
         sh->pick[0] = 0xffffffffu;
         sh->pick[1] = 0;
     }
-    __syncthreads();
-    if ((tid & 31) == 0) {
-        atomicMin(&sh->pick[0], lo);
-        atomicMax(&sh->pick[1], hi);
-    }
-    __syncthreads();
-    lo = sh->pick[0];
-    hi = sh->pick[1];
+#pragma unroll 1
     for (;;) {
-        // keys in [lo, hi] hold the m-th largest of themselves
-        if (lo == hi) {
-            *left = m;
-            return lo;
+        if (what == 1) {
+#pragma unroll 1
+            for (int k = tid; k < kSelectBins / 4; k += kSelectThreads)
+                *reinterpret_cast<uint4 *>(sh->hist + 4 * k) = make_uint4(0, 0, 0, 0);
         }
-        const uint32_t span = hi - lo;
-        const int shift = max(0, 32 - __clz(span) - 11);   // span >> shift < 2048
-#pragma unroll
-        for (int k = 0; k < kSelectBins / kSelectThreads; ++k)
-            sh->hist[k * kSelectThreads + tid] = 0;
         __syncthreads();
-        for (int i = tid; i < n; i += kSelectThreads) {
-            if (live(i)) {
-                const uint32_t k = key[i];
-                if (k >= lo && k <= hi)
-                    atomicAdd(&sh->hist[(k - lo) >> shift], 1u);
+        pass(what, from, to, shift);
+        if (what == 0) {
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            hi = __reduce_max_sync(0xffffffffu, hi);
+            if ((tid & 31) == 0) {
+                atomicMin(&sh->pick[0], lo);
+                atomicMax(&sh->pick[1], hi);
             }
-        }
-        __syncthreads();
-        // thread t adds up bins [first, first + 8), from the highest down
-        constexpr int BPT = kSelectBins / kSelectThreads;
-        const int first = kSelectBins - BPT * (tid + 1);
-        alignas(16) uint32_t h[BPT];
-        uint32_t sum = 0, total;
-        static_assert(BPT == 8, "two 16-byte reads");
-        *reinterpret_cast<uint4 *>(h) = *reinterpret_cast<const uint4 *>(sh->hist + first);
-        *reinterpret_cast<uint4 *>(h + 4) = *reinterpret_cast<const uint4 *>(sh->hist + first + 4);
-#pragma unroll
-        for (int k = 0; k < BPT; ++k)
-            sum += h[k];
-        uint32_t above = cta_exclusive(sum, sh->scan, &total);
-        if (above < m && m <= above + sum) {
-#pragma unroll
-            for (int k = BPT - 1; k >= 0; --k) {
-                if (above < m && m <= above + h[k]) {
-                    sh->pick[0] = (uint32_t)(first + k);
-                    sh->pick[1] = m - above;
-                    sh->pick[2] = h[k];
+            __syncthreads();
+            from = sh->pick[0];
+            to = sh->pick[1];
+            what = 1;
+        } else if (what == 1) {
+            __syncthreads();
+            // thread t adds up bins [at, at + 8), from the highest down
+            constexpr int BPT = kSelectBins / kSelectThreads;
+            static_assert(BPT == 8, "two 16-byte reads");
+            const int at = kSelectBins - BPT * (tid + 1);
+            const uint4 a = *reinterpret_cast<const uint4 *>(sh->hist + at), b = *reinterpret_cast<const uint4 *>(sh->hist + at + 4);
+            const uint32_t sum = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+            uint32_t total;
+            uint32_t above = cta_exclusive(sum, sh->scan, &total);
+            if (above < m && m <= above + sum) {
+                int k = at + BPT - 1;
+                while (above + sh->hist[k] < m)
+                    above += sh->hist[k--];
+                sh->pick[0] = (uint32_t)k;
+                sh->pick[1] = m - above;
+                sh->pick[2] = sh->hist[k];
+                sh->pick[3] = 0;
+            }
+            __syncthreads();
+            m = sh->pick[1];
+            const uint32_t base = from + (sh->pick[0] << shift);
+            to = base + min(to - base, (1u << shift) - 1u);
+            from = base;
+            what = shift > 0 && sh->pick[2] <= kSelectList ? 2 : 1;
+        } else {
+            __syncthreads();
+            const uint32_t inside = sh->pick[2];
+            if (tid < (int)inside) {
+                const uint32_t k = sh->list[tid];
+                uint32_t more = 0, same = 0;
+#pragma unroll 1
+                for (uint32_t j = 0; j < inside; ++j) {
+                    more += sh->list[j] > k;
+                    same += sh->list[j] == k;
                 }
-                above += h[k];
+                if (more < m && m <= more + same) {
+                    sh->pick[0] = k;
+                    sh->pick[1] = m - more;
+                }
             }
-            sh->pick[3] = 0;
+            __syncthreads();
+            *left = sh->pick[1];
+            return sh->pick[0];
         }
-        __syncthreads();
-        const uint32_t bin = sh->pick[0], inside = sh->pick[2];
-        m = sh->pick[1];
-        const uint32_t base = lo + (bin << shift);
-        hi = base + min(hi - base, (1u << shift) - 1u);
-        lo = base;
-        if (shift == 0) {
+        if (from == to) {   // the keys left are equal
             *left = m;
-            return lo;
+            return from;
         }
-        if (inside > kSelectList) {
-            __syncthreads();   // pick is read
-            continue;
-        }
-        for (int i = tid; i < n; i += kSelectThreads) {
-            if (live(i)) {
-                const uint32_t k = key[i];
-                if (k >= lo && k <= hi)
-                    sh->list[atomicAdd(&sh->pick[3], 1u)] = k;   // equal keys are alike: their order does not matter
-            }
-        }
-        __syncthreads();
-        if (tid < (int)inside) {
-            const uint32_t k = sh->list[tid];
-            uint32_t more = 0, same = 0;
-            for (uint32_t j = 0; j < inside; ++j) {
-                more += sh->list[j] > k;
-                same += sh->list[j] == k;
-            }
-            if (more < m && m <= more + same) {
-                sh->pick[0] = k;
-                sh->pick[1] = m - more;
-            }
-        }
-        __syncthreads();
-        *left = sh->pick[1];
-        return sh->pick[0];
+        shift = max(0, 32 - __clz(to - from) - 11);   // (to - from) >> shift < 2048
+        // the bin's keys are listed with the range as it is
+        __syncthreads();   // pick is read
     }
 }
 
@@ -272,6 +266,43 @@ __device__ __forceinline__ float select_q(const SelectParams &p, int64_t i)
 {
     return p.q_dtype == PKV_F16 ? to_float(static_cast<const __half *>(p.q)[i])
                                 : to_float(static_cast<const __nv_bfloat16 *>(p.q)[i]);
+}
+
+// -Q- and Q+ of dimension tid < D in pairs, from the group's q, into weight
+// [2 D]: for exact scores.  `scale`: a power of two that keeps them below 2^15
+// (any that does: only the order of scores counts).
+template <int D>
+__device__ __forceinline__ void exact_weights(Pair *weight, float (&x)[8], float scale)
+{
+    Pair lo{0.f, 0.f}, hi{0.f, 0.f};
+#pragma unroll 2
+    for (int h = 0; h < 8; ++h) {
+        const float y = x[0] * scale;
+#pragma unroll
+        for (int k = 0; k < 7; ++k)
+            x[k] = x[k + 1];
+        lo = pair_add(lo, Pair{y > 0.f ? 0.f : y, 0.f});
+        hi = pair_add(hi, Pair{y < 0.f ? 0.f : y, 0.f});
+    }
+    weight[threadIdx.x] = lo;
+    weight[D + threadIdx.x] = hi;
+}
+
+// The power of two that brings the largest of the CTA's `big` (>= 0) to [2^14,
+// 2^15); warp_big: a word per warp.  All threads call it.
+template <int NW>
+__device__ __forceinline__ float weight_scale(float big, uint32_t *warp_big)
+{
+    const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+    if ((threadIdx.x & 31) == 0)
+        warp_big[threadIdx.x >> 5] = most;
+    __syncthreads();
+    uint32_t all = 0;
+#pragma unroll
+    for (int k = 0; k < NW; ++k)
+        all = max(all, warp_big[k]);
+    const int e = min(max((int)(all >> 23) - 127 - 14, -120), 120);
+    return __uint_as_float((uint32_t)(127 - e) << 23);
 }
 
 template <typename T> __device__ __forceinline__ T from_float(float x);
@@ -317,10 +348,11 @@ __device__ __forceinline__ void bulk_load(void *dst_smem, const void *src, uint3
 // of NW warps.  Returns each warp's S (in units of the weights' scale), or
 // kBadChunk if one of its blocks' ids is outside the pool or a copy timed out;
 // nothing is scored in a row that is selected whole.  n receives the row's
-// number of blocks; before_stores() runs before the first store.
+// number of blocks, weight (unless null) the weights of exact scores;
+// before_stores() runs before the first store.
 template <typename T, int D, int NW, int ST, typename Before>
 __device__ __forceinline__ float score_blocks(const SelectParams &p, ScoreShared<D, NW, ST> *sw, int seq, int kvh, int b0,
-                                              uint32_t *keys, int &n, bool tell, Before before_stores)
+                                              uint32_t *keys, int &n, Pair *weight, bool tell, Before before_stores)
 {
     using Sh = ScoreShared<D, NW, ST>;
     constexpr int KS = 2 * D / 16;           // k steps
@@ -393,17 +425,10 @@ __device__ __forceinline__ float score_blocks(const SelectParams &p, ScoreShared
                 down[h] += down[h + k];
             }
         }
-        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(up[0], down[0])));
-        if (lane == 0)
-            sw->big[warp] = most;
-        __syncthreads();
-        uint32_t all = 0;
-#pragma unroll
-        for (int k = 0; k < NW; ++k)
-            all = max(all, sw->big[k]);
-        // the largest weight to [2^14, 2^15), inside both types' range
-        const int e = min(max((int)(all >> 23) - 127 - 14, -120), 120);
-        const float scale = __uint_as_float((uint32_t)(127 - e) << 23);
+        // inside both types' range
+        const float scale = weight_scale<NW>(fmaxf(up[0], down[0]), sw->big);
+        if (weight && tid < D)
+            exact_weights<D>(weight, x, scale);
         if (tid < D) {
             auto split = [&](float w, int at) {
                 T one;
@@ -500,7 +525,6 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int K = p.num_selected;
     const int32_t *table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
-    const int64_t q0 = ((int64_t)seq * p.num_kv_heads + kvh) * p.group * D;
     // the chunks' bounds, a lane each: NaN and infinity order above numbers
     float S;
     bool bad = false;
@@ -533,20 +557,20 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
     if (m > 0) {
         const float eps = S * kScoreErr;
         uint32_t left;
-        const float t = key_value(kth_largest(sh, key, n, m, [&](int i) { return i >= first && i < last; }, &left));
+        const float t = key_value(kth_largest(sh, key, first, last, nullptr, m, &left));
         const bool finite = fabsf(t) < INFINITY && eps < INFINITY;   // else all are in doubt
         hi_edge = finite ? t + 2.f * eps : INFINITY;
         lo_edge = finite ? t - 2.f * eps : -INFINITY;
     }
-    uint32_t sure = 0, doubt = 0;
+    uint32_t counts = 0;   // sure ones below, those in doubt above 16 bits, of this thread's
+#pragma unroll 2
     for (int i = tid; i < words * 32; i += kSelectThreads) {   // a warp's 32 blocks are one word
         bool a = i < n, b = false;
         if (i >= first && i < last) {
             const float s = key_value(key[i]);
             a = m > 0 && s > hi_edge;
             b = m > 0 && !a && !(s < lo_edge);
-            sure += a;
-            doubt += b;
+            counts += (uint32_t)a + ((uint32_t)b << 16);
         }
         const uint32_t wa = __ballot_sync(0xffffffffu, a), wb = __ballot_sync(0xffffffffu, b);
         if (lane == 0) {
@@ -555,48 +579,22 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
         }
     }
     uint32_t sure_total, doubt_total;
-    (void)cta_exclusive(sure, sh->scan, &sure_total);
-    (void)cta_exclusive(doubt, sh->scan, &doubt_total);
-    ties = m - sure_total;
-    if (doubt_total > ties && S > 0.f) {
-        // the blocks in doubt by their exact scores: weights in pairs first,
-        // brought to about 1 by a power of two; summaries too, by 2^-64,
-        // where S is huge or overflowed
-        float x[8], big = 0.f;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-            x[g] = tid < D && g < p.group ? select_q(p, q0 + (int64_t)g * D + tid) : 0.f;
-            big = fmaxf(big, fabsf(x[g]));
-        }
-        {
-            const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
-            __syncthreads();
-            if (lane == 0)
-                sh->scan[warp] = most;
-            __syncthreads();
-            uint32_t all = 0;
-            for (int k = 0; k < NW; ++k)
-                all = max(all, sh->scan[k]);
-            big = __uint_as_float(all);
-        }
-        const int up = min(max((int)(__float_as_uint(big) >> 23) - 127 + 3, -120), 120);
-        const float w_scale = __uint_as_float((uint32_t)(127 - up) << 23);
-        const float v_scale = S < 0x1p75f ? 1.f : 0x1p-64f;   // S is for weights up to 2^15
-        if (tid < D) {
-            Pair lo{0.f, 0.f}, hi{0.f, 0.f};
-#pragma unroll 1
-            for (int g = 0; g < 8; ++g) {
-                const float y = x[0] * w_scale;
-#pragma unroll
-                for (int k = 0; k < 7; ++k)
-                    x[k] = x[k + 1];
-                lo = pair_add(lo, Pair{y > 0.f ? 0.f : y, 0.f});
-                hi = pair_add(hi, Pair{y < 0.f ? 0.f : y, 0.f});
-            }
-            sh->weight[tid] = lo;
-            sh->weight[D + tid] = hi;
+    {
+        const uint32_t a = __reduce_add_sync(0xffffffffu, counts & 0xffffu), b = __reduce_add_sync(0xffffffffu, counts >> 16);
+        __syncthreads();
+        if (lane == 0) {
+            sh->scan[warp] = a;
+            sh->list[warp] = b;
         }
         __syncthreads();
+        sure_total = __reduce_add_sync(0xffffffffu, lane < NW ? sh->scan[lane] : 0u);
+        doubt_total = __reduce_add_sync(0xffffffffu, lane < NW ? sh->list[lane] : 0u);
+    }
+    ties = m - sure_total;
+    if (doubt_total > ties && S > 0.f) {
+        // the blocks in doubt by their exact scores; summaries are scaled by
+        // 2^-64 where S, for weights up to 2^15, is huge or overflowed
+        const float v_scale = S < 0x1p75f ? 1.f : 0x1p-64f;
         auto exact = [&](int i) -> unsigned long long {   // by a warp
             const int64_t at = ((int64_t)table[i] * p.num_kv_heads + kvh) * 2 * D + lane;
             float v[2 * D / 32];
@@ -658,7 +656,7 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
             }
             __syncthreads();
             uint32_t left;
-            const uint32_t t = kth_largest(sh, key, n, ties, [&](int i) { return (pend[i / 32] >> (i % 32) & 1u) != 0; }, &left);
+            const uint32_t t = kth_largest(sh, key, 0, n, pend, ties, &left);
             __syncthreads();
             uint32_t still = 0;
             for (int i = tid; i < words * 32; i += kSelectThreads) {
@@ -712,6 +710,7 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
         at += __popc(in[k]);
     }
     __syncthreads();
+#pragma unroll 2
     for (int i = tid; i < n; i += kSelectThreads) {
         const uint32_t w = in[i / 32];
         if (w >> (i % 32) & 1u)
@@ -732,13 +731,13 @@ select_blocks_kernel(const __grid_constant__ SelectParams p)
     using Score = ScoreShared<D, NW, 1>;
     Score *sw = reinterpret_cast<Score *>(smem + sizeof(SelectShared));
     uint32_t *key = reinterpret_cast<uint32_t *>(smem + sizeof(SelectShared) + sizeof(Score));   // [most], CTA 0's in use
-    uint32_t *in = key + p.most;                                            // bit i: block i is selected
+    uint32_t *in = key + p.key_stride;                                            // bit i: block i is selected
     uint32_t *pend = in + (p.most + 31) / 32;                               // bit i: block i is in doubt
     const int me = (int)cluster.block_rank(), kvh = blockIdx.y, seq = blockIdx.z;
     cluster.barrier_arrive();   // CTA 0 has started once this completes: its memory may be written
     int n;
     const float S = score_blocks<T, D, NW, 1>(p, sw, seq, kvh, me * p.chunk, cluster.map_shared_rank(key, 0) + me * p.chunk, n,
-                                           kvh == 0 && me == 0 && threadIdx.x == 0, [&] { cluster.barrier_wait(); });
+                                           me == 0 ? sh->weight : nullptr, kvh == 0 && me == 0 && threadIdx.x == 0, [&] { cluster.barrier_wait(); });
     if ((threadIdx.x & 31) == 0)
         cluster.map_shared_rank(sh, 0)->bound[me * NW + (threadIdx.x >> 5)] = S;
     cluster.sync();
@@ -756,14 +755,15 @@ score_blocks_kernel(const __grid_constant__ SelectParams p)
     extern __shared__ __align__(16) uint8_t smem[];
     using Score = ScoreShared<D, kScoreWarps, kScoreStages>;
     Score *sw = reinterpret_cast<Score *>(smem);
+    // the second launch's CTAs may come up, and prepare, beside the last of these
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int kvh = blockIdx.x, me = blockIdx.y, seq = blockIdx.z;
     const int64_t row = (int64_t)seq * p.num_kv_heads + kvh;
     int n;
-    const float S = score_blocks<T, D, kScoreWarps, kScoreStages>(p, sw, seq, kvh, me * p.chunk, p.ws_keys + row * p.most + me * p.chunk, n,
-                                                    false, [] {});
+    const float S = score_blocks<T, D, kScoreWarps, kScoreStages>(p, sw, seq, kvh, me * p.chunk, p.ws_keys + row * p.key_stride + me * p.chunk, n,
+                                                    nullptr, false, [] {});
     if ((threadIdx.x & 31) == 0)
         p.ws_bound[row * p.bounds + me * kScoreWarps + (threadIdx.x >> 5)] = S;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // The second launch, a programmatic dependent of the first: grid (kv head,
@@ -775,24 +775,40 @@ select_rows_kernel(const __grid_constant__ SelectParams p)
     extern __shared__ __align__(16) uint8_t smem[];
     SelectShared *sh = reinterpret_cast<SelectShared *>(smem);
     uint32_t *key = reinterpret_cast<uint32_t *>(smem + sizeof(SelectShared));   // [most]
-    uint32_t *in = key + p.most;
+    uint32_t *in = key + p.key_stride;
     uint32_t *pend = in + (p.most + 31) / 32;
     const int kvh = blockIdx.x, seq = blockIdx.y;
     const int64_t row = (int64_t)seq * p.num_kv_heads + kvh;
-    const int n = row_blocks(p, p.context_lens[seq], kvh == 0 && threadIdx.x == 0);
+    const int tid = threadIdx.x;
+    float x[8], big = 0.f;
+#pragma unroll
+    for (int h = 0; h < 8; ++h) {
+        x[h] = tid < D && h < p.group ? select_q(p, (row * p.group + h) * D + tid) : 0.f;
+        big = fmaxf(big, fabsf(x[h]) * 8.f);
+    }
+    int n = row_blocks(p, p.context_lens[seq], kvh == 0 && tid == 0);
+    if (tid == 0) {
+        mbar_init(&sh->bar, 1);
+        fence_mbar_init();
+    }
+    const float scale = weight_scale<kSelectThreads / 32>(big, sh->scan);
+    if (tid < D)
+        exact_weights<D>(sh->weight, x, scale);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (n > p.num_selected) {
-        const uint32_t *src = p.ws_keys + row * p.most;
-        for (int i0 = threadIdx.x; i0 < n; i0 += kSelectThreads * 8) {
-            uint32_t k[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                k[u] = i0 + u * kSelectThreads < n ? __ldcg(src + i0 + u * kSelectThreads) : 0u;
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (i0 + u * kSelectThreads < n)
-                    key[i0 + u * kSelectThreads] = k[u];
+        if (tid == 0) {
+            const uint32_t bytes = (uint32_t)(n + 3) / 4 * 16;
+            mbar_arrive_expect_tx(&sh->bar, bytes);
+            bulk_load(key, p.ws_keys + row * p.key_stride, bytes, &sh->bar);
         }
+        if (!mbar_wait_bounded(&sh->bar, 0)) {
+            if (tid == 0) {
+                report(p.status, PKV_DEV_TIMEOUT);
+                drain_wait(&sh->bar, 0, p.status);
+            }
+            n = 0;   // selects nothing
+        }
+        n = __syncthreads_and(n != 0) ? n : 0;
     }
     __syncthreads();
     select_row<T, D>(p, sh, key, in, pend, p.ws_bound + row * p.bounds, seq, kvh, n);

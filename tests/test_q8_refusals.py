@@ -128,8 +128,8 @@ def test_list_workspace(lib):
 def test_select_workspace(lib):
     w = lib.pkv_select_blocks_workspace_bytes
     assert w(4, 8, 8192, 16) == 0                                       # one launch
-    # 4096 keys of each of 16 x 8 rows, then a bound for each 64 of them (a warp's)
-    assert w(16, 8, 65536, 16) == 128 * 4096 * 4 + 128 * 64 * 4
+    # 4096 keys of each of 16 x 8 rows, then a bound for each 128 of them (a warp's)
+    assert w(16, 8, 65536, 16) == 128 * 4096 * 4 + 128 * 32 * 4
     assert w(0, 8, 65536, 16) == 0 and w(16, 8, 40961 * 16, 16) == 0
 
 
