@@ -27,7 +27,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from .build import library_path
+from .build import library_path, torch_module_path
 
 __all__ = [
     "PkvError", "load_library", "paged_attention_decode", "reshape_and_cache", "copy_blocks",
@@ -580,76 +580,39 @@ def q8_scales(num_blocks: int, num_kv_heads: int, device=None) -> torch.Tensor:
     return torch.zeros(num_blocks, -(-num_kv_heads // 4) * 4, dtype=torch.float32, device=device)
 
 
-# The current device and a device's current stream as plain numbers: the calls
-# below are made once per layer and step, and torch.cuda.current_stream() alone
-# costs more than a small kernel's launch.
-_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                              lambda i: torch.cuda.current_stream(i).cuda_stream)
+# The functions that the extension module calls, in its order.
+_BOUND = ("pkv_append_cache_q8", "pkv_summarize_blocks", "pkv_select_blocks", "pkv_select_blocks_workspace_bytes",
+          "pkv_paged_attention_decode_q8", "pkv_paged_attention_decode_selected",
+          "pkv_paged_attention_list_workspace_bytes")
+_module = None
 
 
-def _ready(names: str, *tensors: Optional[torch.Tensor]) -> int:
-    """Every tensor (None: absent) contiguous and on one CUDA device -> its
-    index.  names: the tensors' names, for the error."""
-    index = tensors[0].get_device()   # -1 on the host
-    for t in tensors:
-        if t is not None and (t.get_device() != index or index < 0 or not t.is_contiguous()):
-            name = names.split()[next(i for i, x in enumerate(tensors) if x is t)]
-            if not t.is_cuda or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous CUDA tensor")
-            raise ValueError(f"{name} is on {t.device}, other arguments on {tensors[0].device}")
-    return index
+def _native():
+    """The extension module that checks tensors and calls the library with
+    them, bound to the loaded library."""
+    global _module
+    if _module is None:
+        import importlib.util
+        path = torch_module_path()
+        if not os.path.exists(path):
+            raise ImportError(f"extension module not built at {path}; run python -m paged_kv_cache_311_gb300.build")
+        lib = load_library()
+        spec = importlib.util.spec_from_file_location("_pkv_torch", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _BOUND])
+        _module = module
+    return _module
 
 
-def _launch(fn, what: str, index: int, stream, *args) -> None:
-    """fn(*args, stream) with the tensors' device current; stream None: that
-    device's current stream."""
-    if _current_device() != index:
-        with torch.cuda.device(index):
-            return _launch(fn, what, index, stream, *args)
-    if stream is None:
-        stream = _current_raw_stream(index)
-    else:
-        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    rc = fn(*args, stream)
-    if rc != 0:
-        raise PkvError(rc, what)
-
-
-def _address(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _status_arg(t: Optional[torch.Tensor]):
-    if t is None:
-        return None
-    if t.numel() < 1 or t.element_size() != 4 or t.is_floating_point():
-        raise ValueError("device_status must be an int32 or uint32 tensor")
-    return t.data_ptr()
-
-
-def _tables(block_tables: torch.Tensor, context_lens: torch.Tensor, B: int) -> int:
-    """Checks the tables and lengths of B sequences -> table entries per sequence."""
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
-        raise ValueError("block_tables and context_lens must be int32")
-    shape = block_tables.shape
-    if len(shape) != 2 or shape[0] != B or context_lens.shape != (B,):
-        raise ValueError("block_tables must be [B, MB] and context_lens [B]")
-    return shape[1]
-
-
-def _q8_scale_args(NB: int, Hk: int, *scales: torch.Tensor) -> None:
-    for s in scales:
-        if s.dtype != torch.float32 or s.shape != (NB, (Hk + 3) // 4 * 4):
-            raise ValueError("scales must be float32 [num_blocks, num_kv_heads rounded up to a multiple of 4]")
-
-
-def _new_tokens(query_start: Optional[torch.Tensor], B: int, T: int) -> None:
-    if query_start is None:
-        if T != B:
-            raise ValueError("without query_start every sequence has one new token")
-    elif query_start.dtype != torch.int32 or query_start.shape != (B + 1,):
-        raise ValueError("query_start must be int32 [B + 1]")
+def _scratch(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
+    """A workspace on like's device for a call on `stream` (None: the current one)."""
+    t = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if stream is not None:
+        # the allocator must not hand it out again before that stream is done with it
+        t.record_stream(stream if hasattr(stream, "cuda_stream")
+                        else torch.cuda.ExternalStream(int(stream), device=like.device))
+    return t
 
 
 def append_cache_q8(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -666,26 +629,10 @@ def append_cache_q8(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tenso
     block's scale grows with its rows; rows it holds are then rescaled.  Blocks
     shared by sequences are copied first (copy_blocks on the caches and on the
     scales)."""
-    index = _ready("key value k_cache v_cache k_scales v_scales block_tables context_lens query_start device_status",
-                   key, value, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, query_start,
-                   device_status)
-    T, Hk, D = shape = key.shape
-    NB, Hk2, bs, D2 = cache_shape = k_cache.shape
-    if Hk2 != Hk or D2 != D or value.shape != shape or v_cache.shape != cache_shape:
-        raise ValueError("shape mismatch")
-    dtype = _DTYPE.get(key.dtype)
-    if dtype is None or value.dtype != key.dtype:
-        raise ValueError("key and value must share a floating dtype")
-    if k_cache.dtype != torch.float8_e4m3fn or v_cache.dtype != torch.float8_e4m3fn:
-        raise ValueError("k_cache and v_cache must be float8_e4m3fn")
-    _q8_scale_args(NB, Hk, k_scales, v_scales)
-    B = context_lens.numel()
-    MB = _tables(block_tables, context_lens, B)
-    _new_tokens(query_start, B, T)
-    _launch((_lib or load_library()).pkv_append_cache_q8, "pkv_append_cache_q8", index, stream,
-            key.data_ptr(), value.data_ptr(), dtype, k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
-            v_scales.data_ptr(), block_tables.data_ptr(), MB, context_lens.data_ptr(), _address(query_start), B, T,
-            Hk, D, bs, NB, _status_arg(device_status))
+    rc = (_module or _native()).append(key, value, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                                       query_start, device_status, stream)
+    if rc:
+        raise PkvError(rc, "pkv_append_cache_q8")
 
 
 def summarize_blocks(k_cache: torch.Tensor, summaries: torch.Tensor, block_tables: torch.Tensor,
@@ -699,30 +646,10 @@ def summarize_blocks(k_cache: torch.Tensor, summaries: torch.Tensor, block_table
 
     summaries: [NB, Hk, 2, D] of the cache's dtype, bfloat16 for an 8-bit cache
     (k_cache float8_e4m3fn, with its k_scales)."""
-    index = _ready("k_cache summaries block_tables context_lens query_start k_scales device_status", k_cache, summaries,
-                   block_tables, context_lens, query_start, k_scales, device_status)
-    NB, Hk, bs, D = k_cache.shape
-    q8 = k_cache.dtype == torch.float8_e4m3fn
-    dtype = PKV_E4M3 if q8 else _DTYPE.get(k_cache.dtype)
-    if dtype is None:
-        raise ValueError("k_cache must be float16, bfloat16 or float8_e4m3fn")
-    if q8 != (k_scales is not None):
-        raise ValueError("k_scales go with a float8_e4m3fn cache")
-    if q8:
-        _q8_scale_args(NB, Hk, k_scales)
-    if summaries.shape != (NB, Hk, 2, D) or summaries.dtype != (torch.bfloat16 if q8 else k_cache.dtype):
-        raise ValueError("summaries must be [NB, Hk, 2, D] of the cache's dtype (bfloat16 for an 8-bit cache)")
-    B = context_lens.numel()
-    MB = _tables(block_tables, context_lens, B)
-    if num_tokens is None:
-        if query_start is not None:
-            raise ValueError("query_start needs num_tokens")
-        num_tokens = B
-    _new_tokens(query_start, B, num_tokens)
-    _launch((_lib or load_library()).pkv_summarize_blocks, "pkv_summarize_blocks", index, stream,
-            k_cache.data_ptr(), dtype, _address(k_scales), summaries.data_ptr(), PKV_BF16 if q8 else dtype,
-            block_tables.data_ptr(), MB, context_lens.data_ptr(), _address(query_start), B, int(num_tokens), Hk, D, bs,
-            NB, _status_arg(device_status))
+    rc = (_module or _native()).summarize(k_cache, summaries, block_tables, context_lens, query_start, num_tokens,
+                                          k_scales, device_status, stream)
+    if rc:
+        raise PkvError(rc, "pkv_summarize_blocks")
     return summaries
 
 
@@ -740,24 +667,13 @@ def select_blocks(selected: torch.Tensor, q: torch.Tensor, summaries: torch.Tens
     float16 or bfloat16.  max_context_len: host bound of context_lens (what the
     table can hold if omitted).  workspace: select_blocks_workspace_bytes,
     allocated here if needed and not given."""
-    index = _ready("selected q summaries block_tables context_lens workspace device_status", selected, q, summaries,
-                   block_tables, context_lens, workspace, device_status)
-    B, H, D = q.shape
-    NB, Hk, two, D2 = summaries.shape
-    out_shape = selected.shape
-    if two != 2 or D2 != D or len(out_shape) != 3 or out_shape[:2] != (B, Hk):
-        raise ValueError("shape mismatch")
-    q_dtype, s_dtype = _DTYPE.get(q.dtype), _DTYPE.get(summaries.dtype)
-    if selected.dtype != torch.int32 or q_dtype is None or s_dtype is None:
-        raise ValueError("selected must be int32, q and summaries floating")
-    MB = _tables(block_tables, context_lens, B)
-    max_context_len = MB * block_size if max_context_len is None else int(max_context_len)
-    workspace, ws, nbytes = _workspace(workspace, index, stream, select_blocks_workspace_bytes, B, Hk, max_context_len,
-                                       int(block_size))
-    _launch((_lib or load_library()).pkv_select_blocks, "pkv_select_blocks", index, stream,
-            selected.data_ptr(), q.data_ptr(), q_dtype, summaries.data_ptr(), s_dtype, block_tables.data_ptr(), MB,
-            context_lens.data_ptr(), B, H, Hk, D, int(block_size), NB, max_context_len, out_shape[2], int(keep_first),
-            int(keep_last), ws, nbytes, _status_arg(device_status))
+    rc = (_module or _native()).select(selected, q, summaries, block_tables, context_lens, block_size, keep_first,
+                                       keep_last, max_context_len, workspace, device_status, stream)
+    if rc > 0:
+        rc = _module.select(selected, q, summaries, block_tables, context_lens, block_size, keep_first, keep_last,
+                            max_context_len, _scratch(rc, q, stream), device_status, stream)
+    if rc:
+        raise PkvError(rc, "pkv_select_blocks")
     return selected
 
 
@@ -770,41 +686,9 @@ def paged_attention_list_workspace_bytes(num_seqs: int, num_heads: int, num_kv_h
                                          block_size: int, max_list_blocks: int, partition_size: int = 0) -> int:
     """Workspace bytes of paged_attention_decode_q8 (max_list_blocks: the blocks
     of max_context_len) and paged_attention_decode_selected (the K of selected)
-    on the current device."""
+    on the current device (0: none)."""
     return int(load_library().pkv_paged_attention_list_workspace_bytes(
         num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_list_blocks, partition_size))
-
-
-def _workspace(workspace, index: int, stream, bytes_of, *sizes):
-    """The caller's workspace, or one allocated here for the stream that uses it
-    -> (tensor or None, address, bytes)."""
-    if workspace is not None:
-        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    if _current_device() != index:
-        with torch.cuda.device(index):
-            nbytes = bytes_of(*sizes)
-    else:
-        nbytes = bytes_of(*sizes)
-    if not nbytes:
-        return None, None, 0
-    device = torch.device("cuda", index)
-    workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        # the allocator must not hand it out again before that stream is done with it
-        workspace.record_stream(stream if hasattr(stream, "cuda_stream")
-                                else torch.cuda.ExternalStream(int(stream), device=device))
-    return workspace, workspace.data_ptr(), nbytes
-
-
-def _decode_shapes(out, q, k_cache, v_cache) -> tuple:
-    B, H, D = shape = q.shape
-    NB, Hk, bs, D2 = cache_shape = k_cache.shape
-    if D2 != D or v_cache.shape != cache_shape or out.shape != shape:
-        raise ValueError("shape mismatch")
-    out_dtype, q_dtype = _DTYPE.get(out.dtype), _DTYPE.get(q.dtype)
-    if out_dtype is None or q_dtype is None:
-        raise ValueError("q and out must be floating")
-    return B, H, D, NB, Hk, bs, out_dtype, q_dtype
 
 
 def paged_attention_decode_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -819,20 +703,13 @@ def paged_attention_decode_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torch
     max_context_len: host bound of context_lens (what the table can hold if
     omitted).  workspace: paged_attention_list_workspace_bytes, allocated here
     if needed and not given."""
-    index = _ready("out q k_cache v_cache k_scales v_scales block_tables context_lens workspace device_status", out, q,
-                   k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, workspace, device_status)
-    B, H, D, NB, Hk, bs, out_dtype, q_dtype = _decode_shapes(out, q, k_cache, v_cache)
-    if k_cache.dtype != torch.float8_e4m3fn or v_cache.dtype != torch.float8_e4m3fn:
-        raise ValueError("k_cache and v_cache must be float8_e4m3fn")
-    _q8_scale_args(NB, Hk, k_scales, v_scales)
-    MB = _tables(block_tables, context_lens, B)
-    max_context_len = MB * bs if max_context_len is None else int(max_context_len)
-    workspace, ws, nbytes = _workspace(workspace, index, stream, paged_attention_list_workspace_bytes, B, H, Hk, D, bs,
-                                       (max_context_len + bs - 1) // bs, partition_size)
-    _launch((_lib or load_library()).pkv_paged_attention_decode_q8, "pkv_paged_attention_decode_q8", index, stream,
-            out.data_ptr(), out_dtype, q.data_ptr(), q_dtype, k_cache.data_ptr(), v_cache.data_ptr(),
-            k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), MB, context_lens.data_ptr(), B, H, Hk, D,
-            bs, NB, max_context_len, scale, partition_size, ws, nbytes, _status_arg(device_status))
+    rc = (_module or _native()).decode(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, None,
+                                       scale, max_context_len, partition_size, workspace, device_status, stream)
+    if rc > 0:
+        rc = _module.decode(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, None, scale,
+                            max_context_len, partition_size, _scratch(rc, q, stream), device_status, stream)
+    if rc:
+        raise PkvError(rc, "pkv_paged_attention_decode_q8")
     return out
 
 
@@ -849,27 +726,13 @@ def paged_attention_decode_selected(out: torch.Tensor, q: torch.Tensor, k_cache:
 
     q, k_cache, v_cache share float16 or bfloat16, or the caches are
     float8_e4m3fn with their k_scales and v_scales."""
-    index = _ready("out q k_cache v_cache block_tables context_lens selected k_scales v_scales workspace device_status",
-                   out, q, k_cache, v_cache, block_tables, context_lens, selected, k_scales, v_scales, workspace,
-                   device_status)
-    B, H, D, NB, Hk, bs, out_dtype, q_dtype = _decode_shapes(out, q, k_cache, v_cache)
-    q8 = k_cache.dtype == torch.float8_e4m3fn
-    if v_cache.dtype != k_cache.dtype or (not q8 and k_cache.dtype != q.dtype):
-        raise ValueError("q, k_cache and v_cache must share a dtype, or the caches be float8_e4m3fn")
-    if (k_scales is not None) != q8 or (v_scales is not None) != q8:
-        raise ValueError("k_scales and v_scales go with float8_e4m3fn caches")
-    if q8:
-        _q8_scale_args(NB, Hk, k_scales, v_scales)
-    list_shape = selected.shape
-    if selected.dtype != torch.int32 or len(list_shape) != 3 or list_shape[:2] != (B, Hk):
-        raise ValueError("selected must be int32 [B, Hk, K]")
-    K = list_shape[2]
-    MB = _tables(block_tables, context_lens, B)
-    workspace, ws, nbytes = _workspace(workspace, index, stream, paged_attention_list_workspace_bytes, B, H, Hk, D, bs, K,
-                                       partition_size)
-    _launch((_lib or load_library()).pkv_paged_attention_decode_selected, "pkv_paged_attention_decode_selected", index,
-            stream, out.data_ptr(), out_dtype, q.data_ptr(), q_dtype, k_cache.data_ptr(), v_cache.data_ptr(),
-            PKV_E4M3 if q8 else q_dtype, _address(k_scales), _address(v_scales), block_tables.data_ptr(), MB,
-            context_lens.data_ptr(), selected.data_ptr(), K, B, H, Hk, D, bs, NB, MB * bs, scale, partition_size, ws,
-            nbytes, _status_arg(device_status))
+    if selected is None:
+        raise TypeError("selected must be a tensor")
+    rc = (_module or _native()).decode(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                                       selected, scale, None, partition_size, workspace, device_status, stream)
+    if rc > 0:
+        rc = _module.decode(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, selected, scale,
+                            None, partition_size, _scratch(rc, q, stream), device_status, stream)
+    if rc:
+        raise PkvError(rc, "pkv_paged_attention_decode_selected")
     return out

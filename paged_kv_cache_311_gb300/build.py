@@ -1,7 +1,9 @@
-"""Builds libpkv.so in-tree for sm_103a with nvcc (no cmake).
+"""Builds libpkv.so in-tree for sm_103a with nvcc (no cmake), and beside it the
+extension module that passes torch tensors to some of its calls.
 
 The translation units compile in parallel; the CUDA runtime is linked
-statically, so the library depends only on the driver at run time.
+statically, so the library depends only on the driver at run time.  The module
+is compiled against the installed torch's headers.
 Usage: python -m paged_kv_cache_311_gb300.build [--verbose-ptxas]
 """
 from __future__ import annotations
@@ -22,6 +24,9 @@ SOURCES = ["pkv_abi.cu", "pa_decode_f32.cu", "pa_decode_f16.cu", "pa_decode_bf16
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
+TORCH_SOURCE = "pkv_torch.cpp"
+
+
 def nvcc() -> str:
     path = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
     if not os.path.exists(path):
@@ -31,6 +36,34 @@ def nvcc() -> str:
 
 def library_path() -> str:
     return os.path.join(LIB_DIR, "libpkv.so")
+
+
+def torch_module_path() -> str:
+    return os.path.join(LIB_DIR, "_pkv_torch.so")
+
+
+def build_torch_module(out_path: str | None = None) -> str:
+    """Compiles the extension module (CPython API, torch's tensor and CUDA stream headers)."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    out = out_path or torch_module_path()
+    os.makedirs(os.path.dirname(out), exist_ok=True)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    includes = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include"), os.path.join(ROOT, "include")]
+    lib = os.path.join(base, "lib")
+    tmp = f"{out}.{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[a for i in includes for a in ("-isystem", i)], os.path.join(CSRC, TORCH_SOURCE), "-o", tmp,
+           "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {TORCH_SOURCE}:\n{r.stderr}")
+    os.replace(tmp, out)
+    return out
 
 
 def build(extra_flags=(), out_path: str | None = None, verbose_ptxas: bool = False) -> str:
@@ -52,8 +85,10 @@ def build(extra_flags=(), out_path: str | None = None, verbose_ptxas: bool = Fal
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        module = ex.submit(build_torch_module, os.path.join(os.path.dirname(out), "_pkv_torch.so"))
         objs = list(ex.map(compile_one, SOURCES))
+        module.result()
     tmp = f"{out}.{os.getpid()}.tmp"
     subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, out)
