@@ -68,13 +68,15 @@ int launch_select(const SelectParams &p, int ctas, bool one, cudaStream_t stream
         cfg.blockDim = dim3(kSelectThreads);
         cfg.dynamicSmemBytes = score + row_smem(p.most);
         cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)ctas;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)ctas;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = 2;
         return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? PKV_OK : PKV_ECUDA;
     }
     constexpr int score = (int)sizeof(ScoreShared<D, kScoreWarps, kScoreStages>);
@@ -83,8 +85,10 @@ int launch_select(const SelectParams &p, int ctas, bool one, cudaStream_t stream
         rc = ensure_smem_attr(reinterpret_cast<const void *>(select_rows_kernel<T, D>), (int)row_smem(kSelectMaxBlocks), &done_rows);
     if (rc)
         return rc;
-    score_blocks_kernel<T, D><<<dim3((unsigned)p.num_kv_heads, (unsigned)ctas, (unsigned)p.num_seqs), kScoreWarps * 32, score,
-                                stream>>>(p);
+    rc = launch_pdl(score_blocks_kernel<T, D>, dim3((unsigned)p.num_kv_heads, (unsigned)ctas, (unsigned)p.num_seqs),
+                    dim3(kScoreWarps * 32), score, stream, p);
+    if (rc)
+        return rc;
     rc = launch_pdl(select_rows_kernel<T, D>, dim3((unsigned)p.num_kv_heads, (unsigned)p.num_seqs), dim3(kSelectThreads),
                     row_smem(p.most), stream, p);
     if (rc)

@@ -735,6 +735,7 @@ select_blocks_kernel(const __grid_constant__ SelectParams p)
     uint32_t *pend = in + (p.most + 31) / 32;                               // bit i: block i is in doubt
     const int me = (int)cluster.block_rank(), kvh = blockIdx.y, seq = blockIdx.z;
     cluster.barrier_arrive();   // CTA 0 has started once this completes: its memory may be written
+    wait_for_stream();
     int n;
     const float S = score_blocks<T, D, NW, 1>(p, sw, seq, kvh, me * p.chunk, cluster.map_shared_rank(key, 0) + me * p.chunk, n,
                                            me == 0 ? sh->weight : nullptr, kvh == 0 && me == 0 && threadIdx.x == 0, [&] { cluster.barrier_wait(); });
@@ -755,6 +756,7 @@ score_blocks_kernel(const __grid_constant__ SelectParams p)
     extern __shared__ __align__(16) uint8_t smem[];
     using Score = ScoreShared<D, kScoreWarps, kScoreStages>;
     Score *sw = reinterpret_cast<Score *>(smem);
+    wait_for_stream();
     // the second launch's CTAs may come up, and prepare, beside the last of these
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int kvh = blockIdx.x, me = blockIdx.y, seq = blockIdx.z;

@@ -91,13 +91,15 @@ int run_list(const ListParams &p, cudaStream_t stream)
     cfg.blockDim = dim3(kListThreads);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)p.np;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.np;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = p.cluster ? 1 : 0;
+    cfg.numAttrs = p.cluster ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kern, p, tmk, tmv) != cudaSuccess)
         return PKV_ECUDA;
     if (p.np > 1 && !p.cluster) {

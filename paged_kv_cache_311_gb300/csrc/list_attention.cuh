@@ -588,14 +588,6 @@ list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constan
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + warp * S;
     uint32_t *flag = reinterpret_cast<uint32_t *>(smem + C::OFF_FLAG);
     int *warp_tokens = reinterpret_cast<int *>(smem + C::OFF_FLAG + 16);
-    // what needs nothing but the arguments leaves first: the length, the
-    // list's entries and q
-    const int L = p.context_lens[seq];
-    const int e0 = part * p.part_blocks;
-    ListEntries<BS> entries;
-    entries.load(p, seq, kvh, e0);
-    ListEngine<T, D, BS> eng;
-    eng.load(p, seq, kvh, lane);
     if (lane == 0) {
         for (int s = 0; s < S; ++s)
             mbar_init(&bars[s], 1);
@@ -606,6 +598,15 @@ list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constan
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
     }
+    wait_for_stream();
+    // what needs nothing but the arguments leaves first: the length, the
+    // list's entries and q
+    const int L = p.context_lens[seq];
+    const int e0 = part * p.part_blocks;
+    ListEntries<BS> entries;
+    entries.load(p, seq, kvh, e0);
+    ListEngine<T, D, BS> eng;
+    eng.load(p, seq, kvh, lane);
     ListResult<D> *res = reinterpret_cast<ListResult<D> *>(smem + C::OFF_RESULT);
     int tokens = 0;
     if (L < 0 || L > p.max_context_len) {

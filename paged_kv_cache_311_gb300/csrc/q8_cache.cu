@@ -37,8 +37,7 @@ int launch(K kern, P p, int units, cudaStream_t stream)
         p.tokens_per_cta *= 2;
     const unsigned x = (unsigned)(((int64_t)p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta);
     const unsigned y = p.tokens_per_cta == 1 ? (unsigned)((units + kUnitWarps - 1) / kUnitWarps) : 1u;
-    kern<<<dim3(x, y), kUnitThreads, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ECUDA;
+    return launch_pdl(kern, dim3(x, y), dim3(kUnitThreads), 0, stream, p);
 }
 
 template <typename T, int D>

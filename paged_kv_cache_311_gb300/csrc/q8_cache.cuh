@@ -28,6 +28,11 @@
 
 namespace pkv {
 
+// The kernels below are launched as programmatic dependents of whatever runs
+// before them on the stream: their CTAs may come up while that drains, and
+// wait here before they touch memory.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Floats between two blocks' scales: the kv heads, rounded up so that a
 // block's scales are whole 16-byte pieces (copy_blocks and swap_blocks move
 // them as they move blocks).
@@ -129,6 +134,7 @@ __device__ __forceinline__ int list_units(const P &p, AppendUnit *list, int *cou
     if (threadIdx.x == 0)
         *count = 0;
     __syncthreads();
+    wait_for_stream();
     const int64_t t = (int64_t)blockIdx.x * p.tokens_per_cta + threadIdx.x;
     AppendUnit u;
     if ((int)threadIdx.x < p.tokens_per_cta && t < p.num_tokens && append_unit<BS>(p, (int)t, u))
