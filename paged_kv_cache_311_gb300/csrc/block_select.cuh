@@ -591,7 +591,8 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
         doubt_total = __reduce_add_sync(0xffffffffu, lane < NW ? sh->list[lane] : 0u);
     }
     ties = m - sure_total;
-    if (doubt_total > ties && S > 0.f) {
+    bool some_tie = doubt_total > ties;   // of the blocks in doubt, not all are in
+    if (some_tie && S > 0.f) {
         // the blocks in doubt by their exact scores; summaries are scaled by
         // 2^-64 where S, for weights up to 2^15, is huge or overflowed
         const float v_scale = S < 0x1p75f ? 1.f : 0x1p-64f;
@@ -644,6 +645,7 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
                     atomicOr(&in[sh->list[tid] / 32], 1u << (sh->list[tid] % 32));
             }
             ties = 0;
+            some_tie = false;
         } else
         // many: by their high words and then, among equals, by their low words
         for (int half = 0; half < 2; ++half) {
@@ -683,28 +685,34 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
     // ---- emission in ascending order: thread t owns words [w0, w1)
     const int per = (words + kSelectThreads - 1) / kSelectThreads;
     const int w0 = min(tid * per, words), w1 = min(w0 + per, words);
-    uint32_t c = 0, total;
-    for (int k = w0; k < w1; ++k)
-        c += __popc(pend[k]);
-    uint32_t seen = cta_exclusive(c, sh->scan, &total);
-    c = 0;
-    for (int k = w0; k < w1; ++k) {
+    uint32_t total;
+    if (some_tie) {
         // the lowest `ties` blocks in doubt are in
-        uint32_t w = pend[k], kept = 0;
-        const uint32_t here = (uint32_t)__popc(w);
-        if (seen + here <= ties) {
-            kept = w;
-        } else {
-            for (uint32_t left = seen < ties ? ties - seen : 0u; left > 0; --left) {
+        uint32_t c = 0;
+#pragma unroll 1
+        for (int k = w0; k < w1; ++k)
+            c += __popc(pend[k]);
+        uint32_t seen = cta_exclusive(c, sh->scan, &total);
+#pragma unroll 1
+        for (int k = w0; k < w1; ++k) {
+            uint32_t w = pend[k], kept = 0;
+            const uint32_t here = (uint32_t)__popc(w);
+            for (uint32_t left = seen < ties ? min(ties - seen, here) : 0u; left > 0; --left) {
                 kept |= w & (0u - w);
                 w &= w - 1;
             }
+            seen += here;
+            pend[k] = kept;
         }
-        seen += here;
-        in[k] |= kept;
+    }
+    uint32_t c = 0;
+#pragma unroll 1
+    for (int k = w0; k < w1; ++k) {
+        in[k] |= pend[k];
         c += __popc(in[k]);
     }
     uint32_t at = cta_exclusive(c, sh->scan, &total);
+#pragma unroll 1
     for (int k = w0; k < w1; ++k) {
         pend[k] = at;   // selected blocks before the word's
         at += __popc(in[k]);
