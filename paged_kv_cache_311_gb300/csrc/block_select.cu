@@ -4,16 +4,15 @@
 #include "block_select.cuh"
 #include "pkv_host.cuh"
 
-// Most rows x blocks of a call in one launch.
-#ifndef PKV_SELECT_ONE
-#define PKV_SELECT_ONE 32768
-#endif
-
 namespace pkv {
 namespace {
 
 constexpr int kSelectMaxBlocks = 40960;   // a row's scores fit one CTA's shared memory
-constexpr int kSelectOneBlocks = 2048;    // of a row in one launch
+// One launch: blocks of a row, and rows x blocks of the call, at most (32 rows
+// of up to 512 blocks: one launch 10 us, two 18; 128 rows of up to 2048: 56
+// against 36).
+constexpr int kSelectOneBlocks = 2048;
+constexpr int64_t kSelectOne = 32768;
 
 int key_stride(int n) { return (n + 3) / 4 * 4; }
 
@@ -32,7 +31,7 @@ SelectCut select_cut(int64_t rows, int most)
     SelectCut c{};
     const int n = most > 0 ? most : 1;
     constexpr int kOne = kSelectThreads / 2;   // blocks of a cluster's CTA, a tile per warp
-    c.cluster = n <= kOne || (n <= kSelectOneBlocks && rows * n <= PKV_SELECT_ONE);
+    c.cluster = n <= kOne || (n <= kSelectOneBlocks && rows * n <= kSelectOne);
     if (c.cluster) {
         // CTAs per row: as many as have a tile per warp while two an
         // SM are resident together
@@ -105,8 +104,8 @@ using namespace pkv;
 
 extern "C" size_t pkv_select_blocks_workspace_bytes(int num_seqs, int num_kv_heads, int max_context_len, int block_size)
 {
-    if (num_seqs <= 0 || num_kv_heads <= 0 || max_context_len < 0 || block_size <= 0 ||
-        (max_context_len + (int64_t)block_size - 1) / block_size > kSelectMaxBlocks)
+    if (num_seqs <= 0 || num_seqs > 65535 || num_kv_heads <= 0 || num_kv_heads > 65535 || max_context_len < 0 ||
+        block_size <= 0 || (max_context_len + (int64_t)block_size - 1) / block_size > kSelectMaxBlocks)
         return 0;
     return select_cut((int64_t)num_seqs * num_kv_heads, (int)((max_context_len + (int64_t)block_size - 1) / block_size)).total;
 }
@@ -130,7 +129,7 @@ extern "C" int pkv_select_blocks(int32_t *selected, const void *q, int q_dtype, 
         (block_size != 8 && block_size != 16 && block_size != 32) || num_heads / num_kv_heads > 8 ||
         num_kv_heads > 65535 || num_seqs > 65535)
         return PKV_EUNSUPPORTED;
-    const int most = (max_context_len + block_size - 1) / block_size;
+    const int most = (int)((max_context_len + (int64_t)block_size - 1) / block_size);
     if (most > kSelectMaxBlocks)
         return PKV_EUNSUPPORTED;
     if (num_seqs == 0)

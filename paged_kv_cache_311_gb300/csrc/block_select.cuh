@@ -60,16 +60,13 @@ struct SelectParams {
     int q_dtype;
 };
 
-#ifndef PKV_SCORE_STAGES
-#define PKV_SCORE_STAGES 2
-#endif
-#ifndef PKV_SCORE_TILES
-#define PKV_SCORE_TILES 8
-#endif
 constexpr int kSelectThreads = 256;
-constexpr int kScoreWarps = 4;                   // warps of a scoring CTA
-constexpr int kScoreStages = PKV_SCORE_STAGES;   // tiles in flight per warp, two launches
-constexpr int kScoreTiles = PKV_SCORE_TILES;     // tiles of 16 blocks per warp, two launches
+// Two launches: warps of a scoring CTA, tiles in flight and tiles of 16 blocks
+// per warp.  (Stages, tiles: 2, 8 took 33.3 us on 16 x 8 rows of up to 2048
+// blocks; 2, 4 35.9; 3, 4 39.2; 1, 2 34.1.)
+constexpr int kScoreWarps = 4;
+constexpr int kScoreStages = 2;
+constexpr int kScoreTiles = 8;
 
 // Error of a score relative to S.  A step on the tensor cores adds 16 exact
 // products and the running sum, aligned to the largest of them and cut off

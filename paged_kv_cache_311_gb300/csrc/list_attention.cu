@@ -20,7 +20,7 @@ struct ListCut {
     bool cluster;
 };
 
-ListCut list_cut(long long rows, int blocks, int block_size, int partition_size)
+ListCut list_cut(long long rows, long long blocks, int block_size, int partition_size)
 {
     if (blocks < 1)
         blocks = 1;
@@ -153,7 +153,8 @@ int decode_list(void *out, int out_dtype, const void *q, int q_dtype, const void
         return PKV_EINVAL;
     if (q_dtype == PKV_F32 || (head_dim != 64 && head_dim != 128) ||
         (block_size != 8 && block_size != 16 && block_size != 32) || num_heads / num_kv_heads > kListMaxGroup ||
-        num_kv_heads > 65535 || num_seqs > 65535)
+        num_kv_heads > 65535 || num_seqs > 65535 || (int64_t)num_seqs * num_heads > INT32_MAX / 8 ||
+        max_context_len > INT32_MAX - 64)
         return PKV_EUNSUPPORTED;
     if (partition_size % 32 || partition_size % block_size)
         return PKV_EINVAL;
@@ -168,7 +169,7 @@ int decode_list(void *out, int out_dtype, const void *q, int q_dtype, const void
         !aligned(selected, 4))
         return PKV_EINVAL;
 
-    const int table_blocks = (max_context_len + block_size - 1) / block_size;
+    const int table_blocks = (int)((max_context_len + (int64_t)block_size - 1) / block_size);
     const int blocks = select ? num_selected : (table_blocks > 0 ? table_blocks : 1);
     const ListCut cut = list_cut((long long)num_seqs * num_kv_heads, blocks, block_size, partition_size);
     const int part = cut.part, np = cut.np;

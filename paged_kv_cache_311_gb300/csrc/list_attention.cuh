@@ -80,13 +80,11 @@ template <> struct ListElem<uint8_t> {
     static constexpr CUtensorMapDataType tma = CU_TENSOR_MAP_DATA_TYPE_UINT8;
 };
 
-// Ring bytes of a CTA (at least two stages a warp), and CTAs per SM.
-#ifndef PKV_LIST_RING
-#define PKV_LIST_RING 49152
-#endif
-#ifndef PKV_LIST_CTAS
-#define PKV_LIST_CTAS 4
-#endif
+// Ring bytes of a CTA (at least two stages a warp), and CTAs per SM: four with
+// 48 KB against three with 64 took q8 contexts of 16K to 32K tokens from 142
+// to 138 us, a batch of 64 from 95.6 to 93.6; five with 32 KB: 146 and 96.
+constexpr int kListRing = 49152;
+constexpr int kListCtas = 4;
 
 template <typename T, int D, int BS>
 struct ListCfg {
@@ -104,7 +102,7 @@ struct ListCfg {
     static constexpr int BOX_STRIDE = BOX_BYTES < 1024 ? 1024 : BOX_BYTES;   // swizzle atoms are 1024 bytes
     static constexpr int TILE_BYTES = BOXES * BOX_STRIDE;      // K (or V) of a tile
     static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
-    static constexpr int S0 = PKV_LIST_RING / (kListWarps * STAGE_BYTES);
+    static constexpr int S0 = kListRing / (kListWarps * STAGE_BYTES);
     static constexpr int S = S0 < 2 ? 2 : S0;
     static constexpr int KS = D / 16;                          // k-steps of QK, m-tiles of PV
     static constexpr int AWS = D + 4;                          // row stride of the merge scratch, in floats
@@ -572,7 +570,7 @@ struct ListEngine {
 // T: __half, __nv_bfloat16, or uint8_t for an e4m3 cache.  Grid (partition,
 // kv head, sequence).
 template <typename T, int D, int BS>
-__global__ void __launch_bounds__(kListThreads, PKV_LIST_CTAS)
+__global__ void __launch_bounds__(kListThreads, kListCtas)
 list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv)
 {

@@ -25,19 +25,21 @@ int check_sizes(int num_seqs, int num_tokens, int num_kv_heads, int head_dim, in
     return PKV_OK;
 }
 
-// Tokens per CTA: one while that keeps the grid below eight CTAs per SM (a
-// decode step's tokens all lead a block: their heads then spread over
-// blockIdx.y), else as many as keep it there, up to kUnitTokens.
+// Tokens per CTA: one while the grid has fewer than four CTAs per SM (a decode
+// step's tokens all lead a block: their heads then spread over blockIdx.y, a
+// warp each), else as many as leave it four, up to kUnitTokens, a leader's
+// heads dealt four to a warp.  (Prompts of 12.8K tokens of 40 heads: 65 us; with
+// eight CTAs per SM and all heads in one CTA 70, with one head to a warp 72.)
 template <typename K, typename P>
 int launch(K kern, P p, int units, cudaStream_t stream)
 {
-    const int most = p.num_tokens / (PKV_UNIT_CTAS * device_sm_count());
+    const int most = p.num_tokens / (4 * device_sm_count());
     p.tokens_per_cta = 1;
     while (p.tokens_per_cta * 2 <= most && p.tokens_per_cta < kUnitTokens)
         p.tokens_per_cta *= 2;
+    const int per_cta = kUnitWarps * (p.tokens_per_cta == 1 ? 1 : 4);
     const unsigned x = (unsigned)(((int64_t)p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta);
-    const unsigned y = p.tokens_per_cta == 1 ? (unsigned)((units + kUnitWarps - 1) / kUnitWarps) : 1u;
-    return launch_pdl(kern, dim3(x, y), dim3(kUnitThreads), 0, stream, p);
+    return launch_pdl(kern, dim3(x, (unsigned)((units + per_cta - 1) / per_cta)), dim3(kUnitThreads), 0, stream, p);
 }
 
 template <typename T, int D>

@@ -75,13 +75,7 @@ struct AppendUnit {
 
 constexpr int kUnitWarps = 8;
 constexpr int kUnitThreads = kUnitWarps * 32;
-#ifndef PKV_UNIT_TOKENS
-#define PKV_UNIT_TOKENS 64
-#endif
-#ifndef PKV_UNIT_CTAS
-#define PKV_UNIT_CTAS 8
-#endif
-constexpr int kUnitTokens = PKV_UNIT_TOKENS;   // tokens a CTA looks at, at most
+constexpr int kUnitTokens = 64;   // tokens a CTA looks at, at most
 
 // Whether token t leads a unit (false also for padding and for what is refused).
 template <int BS, typename P>
