@@ -128,84 +128,60 @@ struct ListCfg {
     }
 };
 
-// The list entries of a CTA's partition, in registers: thread t holds entries
-// t, t + 128, ... of it.  Two steps, so that every load that can leave at once
-// does: load() needs nothing but the arguments, resolve() the row's length.
+// The list entries of a CTA's partition: thread t looks at entries t, t + 128,
+// ... of it.  Two steps, so that every load that can leave at once does: load()
+// needs nothing but the arguments, resolve() the row's length.  The loops stay
+// rolled: code that runs once costs its fetching, about 128 bytes in 45 cycles.
 //
 // A selected list is refused unless it is strictly ascending and inside the
 // sequence's blocks, with -1 only behind its last entry: so no block counts
 // twice and only the last entry can be partial.
 template <int BS>
 struct ListEntries {
-    static constexpr int N = kListCap / kListThreads;
-    int id[N];       // load(): table entry, or logical block of a selected list
-    int before[N];   // the list's entry in front (selected lists)
+    const int32_t *src, *table;
+    int id, before;   // entry t, and the list's entry in front (selected lists)
+
+    __device__ __forceinline__ void get(const ListParams &p, int e0, int k)
+    {
+        id = src[k];
+        before = p.selected && e0 + k > 0 ? src[k - 1] : -1;
+    }
 
     __device__ __forceinline__ void load(const ListParams &p, int seq, int kvh, int e0)
     {
-        const int have = min(p.part_blocks, (p.selected ? p.num_selected : p.max_blocks_per_seq) - e0);
-        const int32_t *src = p.selected ? p.selected + ((int64_t)seq * p.num_kv_heads + kvh) * p.num_selected + e0
-                                        : p.block_tables + (int64_t)seq * p.max_blocks_per_seq + e0;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int k = i * kListThreads + (int)threadIdx.x;
-            id[i] = before[i] = -1;
-            if (k < have) {
-                id[i] = src[k];
-                if (p.selected && e0 + k > 0)
-                    before[i] = src[k - 1];
-            }
-        }
+        table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
+        src = p.selected ? p.selected + ((int64_t)seq * p.num_kv_heads + kvh) * p.num_selected + e0 : table + e0;
+        const int k = (int)threadIdx.x;
+        if (k < min(p.part_blocks, (p.selected ? p.num_selected : p.max_blocks_per_seq) - e0))
+            get(p, e0, k);
     }
 
     // Physical block ids into phys; returns the tokens of this thread's
     // entries counted from the partition's start, or -1 for a refused entry.
-    __device__ __forceinline__ int resolve(const ListParams &p, int32_t *phys, int seq, int e0, int L)
+    __device__ __forceinline__ int resolve(const ListParams &p, int32_t *phys, int e0, int L)
     {
         const int nblk = (L + BS - 1) / BS;
         const int have = min(p.part_blocks, (p.selected ? p.num_selected : nblk) - e0);
         int tokens = 0;
         bool bad = false;
-        if (p.selected) {
-            const int32_t *table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int k = i * kListThreads + (int)threadIdx.x, j = id[i];
-                if (k < have && j >= 0 && j < nblk && (e0 + k == 0 || (before[i] >= 0 && before[i] < j))) {
-                    id[i] = table[j];
-                    before[i] = k * BS + min(BS, L - j * BS);
-                } else {
-                    bad |= k < have && j != -1;
-                    before[i] = 0;
+#pragma unroll 1
+        for (int k = (int)threadIdx.x; k < have; k += kListThreads) {
+            if (k >= kListThreads)
+                get(p, e0, k);
+            int b = id, here = L - e0 * BS - k * BS;   // tokens from the entry on
+            if (p.selected) {
+                if (id < 0 || id >= nblk || (e0 + k > 0 && (before < 0 || before >= id))) {
+                    bad |= id != -1;
+                    continue;
                 }
+                b = table[id];
+                here = L - id * BS;
             }
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int k = i * kListThreads + (int)threadIdx.x;
-            const int here = p.selected ? before[i] : k < have ? min(k * BS + BS, L - e0 * BS) : 0;
-            if (here > 0) {
-                bad |= id[i] < 0 || (int64_t)id[i] >= p.num_blocks;
-                phys[k] = id[i];
-                tokens = max(tokens, here);
-            } else {
-                id[i] = -1;
-            }
+            bad |= b < 0 || (int64_t)b >= p.num_blocks;
+            phys[k] = b;
+            tokens = max(tokens, k * BS + min(BS, here));
         }
         return bad ? -1 : tokens;
-    }
-
-    __device__ __forceinline__ void scales(const ListParams &p, float *ks, float *vs, int kvh) const
-    {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int k = i * kListThreads + (int)threadIdx.x;
-            if (id[i] >= 0) {
-                const int64_t at = (int64_t)id[i] * p.scale_stride + kvh;
-                ks[k] = p.k_scales[at];
-                vs[k] = p.v_scales[at];
-            }
-        }
     }
 };
 
@@ -612,7 +588,7 @@ list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constan
             report(p.status, PKV_DEV_BAD_CONTEXT_LEN);
         tokens = -1;
     } else if (p.selected || e0 * BS < L) {
-        tokens = entries.resolve(p, phys, seq, e0, L);
+        tokens = entries.resolve(p, phys, e0, L);
         const int most = __reduce_max_sync(0xffffffffu, tokens);
         if (lane == 0)
             warp_tokens[warp] = most;
@@ -656,8 +632,14 @@ list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constan
         for (int i = 0; i < min(my_n, S); ++i)
             issue(i, i);
     }
-    if constexpr (C::Q8)
-        entries.scales(p, ks_s, vs_s, kvh);
+    if constexpr (C::Q8) {
+#pragma unroll 1
+        for (int k = (int)threadIdx.x; k * BS < tokens; k += kListThreads) {
+            const int64_t at = (int64_t)phys[k] * p.scale_stride + kvh;
+            ks_s[k] = p.k_scales[at];
+            vs_s[k] = p.v_scales[at];
+        }
+    }
     eng.init(p);
     if constexpr (C::Q8)
         __syncthreads();   // every thread's scales
