@@ -35,8 +35,9 @@
  *     out) are OR-ed into *device_status (may be NULL: not reported) with the
  *     PKV_DEV_* bits; the kernels skip the offending element and never trap.
  *     Read *device_status after synchronising the stream.
- *   - Element types: q, k_cache, v_cache share kv_dtype; arithmetic is fp32
- *     (fp32 accumulation for fp16/bf16 inputs).
+ *   - Element types: q, k_cache, v_cache share kv_dtype (except where a cache
+ *     holds 8-bit values); arithmetic is fp32 (fp32 accumulation for fp16/bf16
+ *     inputs).
  */
 #ifndef PKV_H
 #define PKV_H
