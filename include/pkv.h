@@ -511,8 +511,9 @@ int pkv_summarize_blocks(const void *k_cache, int cache_dtype, const float *k_sc
  *     sum over the kv head's query heads g, sum_d max(q_gd lo_d, q_gd hi_d),
  * an upper bound on the sum of the heads' largest q . k in the block (lo, hi:
  * the block's summary).  The selection is that of the exact scores, whatever
- * the rounding of intermediate sums; equal scores go to the lower block, a
- * NaN score counts as +infinity.  (For a softmax scale > 0.)
+ * the rounding of intermediate sums; equal scores go to the lower block.  A
+ * NaN or an infinity in a block's summary makes its score +infinity, one in a
+ * head's q those of all blocks of its group.  (For a softmax scale > 0.)
  *
  *   selected     int32 [num_seqs, num_kv_heads, num_selected] (written):
  *                logical block numbers in ascending order; all blocks, then

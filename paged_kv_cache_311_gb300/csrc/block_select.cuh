@@ -461,7 +461,8 @@ __device__ __forceinline__ float score_blocks(const SelectParams &p, ScoreShared
         const int i_next = i0 + ST * NW * 16 + lane;
         const int next = k + ST < my_n && i_next < there ? table[i_next] : 0;
         if (score) {
-            if (!mbar_wait_bounded(&bar[st], (uint32_t)((k / ST) & 1))) {
+            // the warp gives up as one: its products and shuffles need every lane
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bar[st], (uint32_t)((k / ST) & 1)))) {
                 // no CTA leaves with copies in flight
                 for (int u = k; u < min(my_n, k + ST); ++u)
                     drain_wait(&bar[u % ST], (uint32_t)((u / ST) & 1), p.status);

@@ -647,7 +647,8 @@ list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constan
     int failed_at = -1;
     for (int i = 0; i < my_n; ++i) {
         const int st = i % S;
-        if (!mbar_wait_bounded(&bars[st], (uint32_t)((i / S) & 1))) {
+        // the warp gives up as one: its products and shuffles need every lane
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[st], (uint32_t)((i / S) & 1)))) {
             failed_at = i;
             break;
         }
