@@ -356,7 +356,7 @@ PyObject *select(PyObject *, PyObject *const *args, Py_ssize_t nargs)
         else if (sel->scalar_type() != at::kInt || !floating(q) || !floating(sums))
             c.value_error("selected must be int32, q and summaries floating");
         const int MB = c.tables(bt, cl, B);
-        const int64_t most = args[8] == Py_None ? MB * bs : c.integer(8);
+        const int64_t most = args[8] == Py_None ? (int64_t)MB * c.narrow(bs) : c.integer(8);
         void *stream = c.stream(11);
         const int n[9] = {c.narrow(B), c.narrow(H), c.narrow(Hk), c.narrow(D), c.narrow(bs), c.narrow(most), c.narrow(sel->size(2)),
                           c.narrow(first), c.narrow(last)};
@@ -413,7 +413,7 @@ PyObject *decode(PyObject *, PyObject *const *args, Py_ssize_t nargs)
         if (c.ok && select && (sel->scalar_type() != at::kInt || sel->dim() != 3 || sel->size(0) != B || sel->size(1) != Hk))
             c.value_error("selected must be int32 [B, Hk, K]");
         const int MB = c.tables(bt, cl, B);
-        const int64_t most = args[10] == Py_None ? MB * bs : c.integer(10);
+        const int64_t most = args[10] == Py_None ? (int64_t)MB * c.narrow(bs) : c.integer(10);
         void *stream = c.stream(14);
         const int K = select && c.ok ? c.narrow(sel->size(2)) : 0;
         const int n[7] = {c.narrow(B), c.narrow(H), c.narrow(Hk), c.narrow(D), c.narrow(bs), c.narrow(most), c.narrow(partition)};

@@ -175,6 +175,36 @@ def test_select_nan_and_infinities():
     np.testing.assert_array_equal(got, want_select(c, 12, 1, 1))
 
 
+@pytest.mark.parametrize("e", [-70, -100, -115, -126, -131])
+@pytest.mark.parametrize("n", [500, 4000])
+def test_select_of_tiny_summaries(e, n):
+    """Keys near the end of bfloat16's range: the products leave fp32's normal
+    numbers, the choice stays that of the definition (exact in fp64)."""
+    c = select_case(14, [n * 16, n * 16 - 5], G=2, t="bf16")
+    c["sums"] = (c["sums"].double() * 2.0 ** e).to(torch.bfloat16)
+    for K in (12, 100):
+        got, st = run_select(c, K, 1, 1)
+        assert st == 0
+        np.testing.assert_array_equal(got, want_select(c, K, 1, 1))
+
+
+@pytest.mark.parametrize("x", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("n", [500, 4000])
+def test_select_with_a_query_that_is_not_finite(x, n):
+    """Every score of its row counts as +infinity: the lowest blocks are kept.
+    An infinite key makes its block's score +infinity, of whatever sign."""
+    c = select_case(15, [n * 16] * 3, G=2, t="bf16")
+    c["q"][0, 1, 5] = x
+    c["sums"][c["tables"][1, 41], 0, 0, 9] = -abs(x)
+    c["sums"][c["tables"][1, 52], 0, :, 9] = -abs(x)
+    got, st = run_select(c, 12, 1, 2)
+    assert st == 0
+    want = want_select(c, 12, 1, 2)
+    want[0, 0] = list(range(10)) + [n - 2, n - 1]
+    assert 41 in want[1, 0] and 52 in want[1, 0]
+    np.testing.assert_array_equal(got, want)
+
+
 def test_select_through_the_workspace():
     """Many rows of many blocks: scored by one launch, selected by another.
     Lengths from 0 on, a sequence of equal blocks, NaN, a bad table and a bad
