@@ -25,6 +25,11 @@
 //     (128 rows of up to 2048 blocks as clusters of four: some SMs got six CTAs
 //     and some none).
 //
+// What bounds it: 16 x 8 rows of 1024 to 2048 blocks (101 MB of summaries, 15 us
+// at the HBM's rate) take 30 us, some 23 for the scores -- what any read of
+// 100 MB takes in one launch -- and 7 for the second launch, whose code runs
+// once.  4 x 8 rows of 128 to 512 blocks take 8 us, latencies throughout.
+//
 // Exactness.  Which blocks are selected is a set of whole numbers, so it must
 // not depend on how a sum was rounded.  A score carries an error of at most
 // eps = 2^-17.5 S, S the largest sum_d |weight_d summary_d| of the row's blocks
@@ -62,8 +67,8 @@ struct SelectParams {
 
 constexpr int kSelectThreads = 256;
 // Two launches: warps of a scoring CTA, tiles in flight and tiles of 16 blocks
-// per warp.  (Stages, tiles: 2, 8 took 33.3 us on 16 x 8 rows of up to 2048
-// blocks; 2, 4 35.9; 3, 4 39.2; 1, 2 34.1.)
+// per warp.  (Stages, tiles: 2, 8 took 30 us on 16 x 8 rows of up to 2048
+// blocks, so did 1, 4; 2, 6 34; 2, 16 34.3; 3, 4 34.5; 1, 8 31.7.)
 constexpr int kScoreWarps = 4;
 constexpr int kScoreStages = 2;
 constexpr int kScoreTiles = 8;

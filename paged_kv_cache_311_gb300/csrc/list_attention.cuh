@@ -31,6 +31,13 @@
 // The K scale multiplies the scores (exactly: a power of two); the V scale
 // multiplies the tile's product as it joins the accumulators, so no weight
 // has to fit a 16-bit range together with it.
+//
+// What bounds it: HBM.  Sixteen q8 contexts of 16K to 32K tokens (808 MB) take
+// 135 us, 6.0 TB/s or 89 % of a copy's rate (93 % while the SMs have work);
+// 64 of 128 to 2048 tokens with 32 kv heads 89 to 100 us (96 to 85 %); 128
+// blocks of 16 tokens of a 16-bit cache for 32 x 8 rows 44 us (91 %).  One
+// request of 700 tokens takes 5.6 us, a launch and the latencies of length and
+// table, tile, products and merge.
 #pragma once
 
 #include <cooperative_groups.h>

@@ -20,6 +20,11 @@
 // its warps: in a prompt only one token in block_size leads, and a warp for
 // every token spent its time finding that out (216 us for 12.8K tokens of 40
 // heads, 12.8K x 80 warps, where the bytes need 57).
+//
+// What bounds them: HBM.  Those tokens are written in 59 to 67 us (84 to 96 %
+// of a copy's rate), the blocks of prompts of 4K to 16K tokens summarised
+// from the 8-bit cache in 36 to 42 us (31 needed).  A decode step of 256
+// requests is a launch and a chain of loads: 3.7 us and 2.7.
 #pragma once
 
 #include <cuda_fp8.h>
