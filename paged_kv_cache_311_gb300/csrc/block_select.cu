@@ -8,18 +8,20 @@ namespace pkv {
 namespace {
 
 constexpr int kSelectMaxBlocks = 40960;   // a row's scores fit one CTA's shared memory
-// One launch: blocks of a row, and rows x blocks of the call, at most (32 rows
-// of up to 512 blocks: one launch 10 us, two 18; 128 rows of up to 2048: 56
-// against 36).
+// One launch: blocks of a row, and rows x blocks of the call, at most; half of
+// those where rows exceed the 608 CTAs of 128 threads that are resident.  (One
+// launch against two, us: 512 rows of up to 256 blocks 18 against 22, 64 of
+// 2048 19 against 21, 128 of 512 13 against 18; but 800 of 163 26 against 22,
+// 3200 of 128 44 against 38, 128 of 2048 56 against 36.)
 constexpr int kSelectOneBlocks = 2048;
-constexpr int64_t kSelectOne = 32768;
+constexpr int64_t kSelectOne = 131072;
 
 int key_stride(int n) { return (n + 3) / 4 * 4; }
 
 // How a call runs: `ctas` CTAs score `chunk` blocks of a row each, in one
 // launch as a cluster or in two through the workspace.
 struct SelectCut {
-    int chunk, ctas, bounds;
+    int chunk, ctas, bounds, threads;
     bool cluster;
     size_t bound_off, total;   // workspace: keys, then bounds
 };
@@ -30,17 +32,20 @@ SelectCut select_cut(int64_t rows, int most)
 {
     SelectCut c{};
     const int n = most > 0 ? most : 1;
-    constexpr int kOne = kSelectThreads / 2;   // blocks of a cluster's CTA, a tile per warp
-    c.cluster = n <= kOne || (n <= kSelectOneBlocks && rows * n <= kSelectOne);
+    constexpr int kOne = 128;   // blocks of a cluster's CTA, a tile per warp
+    const int64_t sms = device_sm_count();
+    c.cluster = n <= kSelectOneBlocks && rows * n <= (rows <= 4 * sms ? kSelectOne : kSelectOne / 2);
     if (c.cluster) {
         // CTAs per row: as many as have a tile per warp while two an
         // SM are resident together
         c.ctas = 1;
-        while (c.ctas < kSelectCluster && n > c.ctas * kOne && rows * c.ctas * 2 <= 2LL * device_sm_count())
+        while (c.ctas < kSelectCluster && n > c.ctas * kOne && rows * c.ctas <= sms)
             c.ctas *= 2;
         c.chunk = (n + c.ctas - 1) / c.ctas;
-        c.bounds = c.ctas * (kSelectThreads / 32);
+        c.threads = rows * c.ctas > 2 * sms ? 128 : 256;
+        c.bounds = c.ctas * (c.threads / 32);
     } else {
+        c.threads = rows > 4 * sms ? 128 : 256;
         c.chunk = kScoreWarps * kScoreTiles * 16;
         c.ctas = (n + c.chunk - 1) / c.chunk;
         c.bounds = c.ctas * kScoreWarps;
@@ -52,19 +57,19 @@ SelectCut select_cut(int64_t rows, int most)
 
 size_t row_smem(int most) { return sizeof(SelectShared) + (size_t)key_stride(most) * 4 + (size_t)(most + 31) / 32 * 8; }
 
-template <typename T, int D>
+template <typename T, int D, int NT>
 int launch_select(const SelectParams &p, int ctas, bool one, cudaStream_t stream)
 {
     static unsigned long long done_one = 0, done_score = 0, done_rows = 0;
     if (one) {
-        auto kern = select_blocks_kernel<T, D>;
-        constexpr size_t score = sizeof(ScoreShared<D, kSelectThreads / 32, 1>);
+        auto kern = select_blocks_kernel<T, D, NT>;
+        constexpr size_t score = sizeof(ScoreShared<D, NT / 32, 1>);
         const int rc = ensure_smem_attr(reinterpret_cast<const void *>(kern), (int)(score + row_smem(kSelectOneBlocks)), &done_one);
         if (rc)
             return rc;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)ctas, (unsigned)p.num_kv_heads, (unsigned)p.num_seqs);
-        cfg.blockDim = dim3(kSelectThreads);
+        cfg.blockDim = dim3(NT);
         cfg.dynamicSmemBytes = score + row_smem(p.most);
         cfg.stream = stream;
         cudaLaunchAttribute attr[2];
@@ -81,18 +86,25 @@ int launch_select(const SelectParams &p, int ctas, bool one, cudaStream_t stream
     constexpr int score = (int)sizeof(ScoreShared<D, kScoreWarps, kScoreStages>);
     int rc = ensure_smem_attr(reinterpret_cast<const void *>(score_blocks_kernel<T, D>), score, &done_score);
     if (!rc)
-        rc = ensure_smem_attr(reinterpret_cast<const void *>(select_rows_kernel<T, D>), (int)row_smem(kSelectMaxBlocks), &done_rows);
+        rc = ensure_smem_attr(reinterpret_cast<const void *>(select_rows_kernel<T, D, NT>), (int)row_smem(kSelectMaxBlocks), &done_rows);
     if (rc)
         return rc;
     rc = launch_pdl(score_blocks_kernel<T, D>, dim3((unsigned)p.num_kv_heads, (unsigned)ctas, (unsigned)p.num_seqs),
                     dim3(kScoreWarps * 32), score, stream, p);
     if (rc)
         return rc;
-    rc = launch_pdl(select_rows_kernel<T, D>, dim3((unsigned)p.num_kv_heads, (unsigned)p.num_seqs), dim3(kSelectThreads),
+    rc = launch_pdl(select_rows_kernel<T, D, NT>, dim3((unsigned)p.num_kv_heads, (unsigned)p.num_seqs), dim3(NT),
                     row_smem(p.most), stream, p);
     if (rc)
         return rc;
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+template <typename T, int D>
+int launch_select(const SelectParams &p, const SelectCut &cut, cudaStream_t stream)
+{
+    return cut.threads == 128 ? launch_select<T, D, 128>(p, cut.ctas, cut.cluster, stream)
+                              : launch_select<T, D, 256>(p, cut.ctas, cut.cluster, stream);
 }
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -169,8 +181,8 @@ extern "C" int pkv_select_blocks(int32_t *selected, const void *q, int q_dtype, 
     p.q_dtype = q_dtype;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (summary_dtype == PKV_F16)
-        return head_dim == 64 ? launch_select<__half, 64>(p, cut.ctas, cut.cluster, s)
-                              : launch_select<__half, 128>(p, cut.ctas, cut.cluster, s);
-    return head_dim == 64 ? launch_select<__nv_bfloat16, 64>(p, cut.ctas, cut.cluster, s)
-                          : launch_select<__nv_bfloat16, 128>(p, cut.ctas, cut.cluster, s);
+        return head_dim == 64 ? launch_select<__half, 64>(p, cut, s)
+                              : launch_select<__half, 128>(p, cut, s);
+    return head_dim == 64 ? launch_select<__nv_bfloat16, 64>(p, cut, s)
+                          : launch_select<__nv_bfloat16, 128>(p, cut, s);
 }

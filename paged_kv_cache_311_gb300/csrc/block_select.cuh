@@ -65,6 +65,11 @@ struct SelectParams {
     int q_dtype;
 };
 
+// Threads of a selecting CTA (NT below): 256, or 128 where the rows are more
+// than the CTAs of 256 threads that an SM holds, two in one launch and four in
+// two.  (256 against 128 threads, us, one launch: 256 rows of 128 blocks 8.9
+// and 10.1, 512 17.2 and 13.0, 1584 of 32 28.6 and 16.9; two: 128 of 2048 29.2
+// and 31.4, 680 of 432 25.2 and 22.6, 1024 of 256 36 and 32.8.)
 constexpr int kSelectThreads = 256;
 // Two launches: warps of a scoring CTA, tiles in flight and tiles of 16 blocks
 // per warp.  (Stages, tiles: 2, 8 took 30 us on 16 x 8 rows of up to 2048
@@ -134,6 +139,7 @@ struct alignas(16) SelectShared {
 // what is used twice is a function.
 
 // Exclusive sum of v over the CTA's threads; *total receives the sum.
+template <int NT>
 __device__ __noinline__ uint32_t cta_exclusive(uint32_t v, uint32_t *warp_sums, uint32_t *total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -148,7 +154,7 @@ __device__ __noinline__ uint32_t cta_exclusive(uint32_t v, uint32_t *warp_sums, 
         warp_sums[warp] = x;
     __syncthreads();
     // a warp's lanes hold the warps' sums
-    const uint32_t s = lane < kSelectThreads / 32 ? warp_sums[lane] : 0u;
+    const uint32_t s = lane < NT / 32 ? warp_sums[lane] : 0u;
     *total = __reduce_add_sync(0xffffffffu, s);
     return __reduce_add_sync(0xffffffffu, lane < warp ? s : 0u) + x - v;
 }
@@ -160,6 +166,7 @@ __device__ __noinline__ uint32_t cta_exclusive(uint32_t v, uint32_t *warp_sums, 
 // leading bits, and bins of fixed bits would put them all into a few, whose
 // atomics then queue -- and keeps the bin of the m-th; once at most 256 keys
 // are left, each is ranked against all.
+template <int NT>
 __device__ __noinline__ uint32_t kth_largest(SelectShared *sh, const uint32_t *key, int first, int last, const uint32_t *mask,
                                              uint32_t m, uint32_t *left)
 {
@@ -168,7 +175,7 @@ __device__ __noinline__ uint32_t kth_largest(SelectShared *sh, const uint32_t *k
     // 0: the range; 1: the histogram; 2: the keys of the bin
     auto pass = [&](int what, uint32_t from, uint32_t to, int shift) {
 #pragma unroll 2
-        for (int i = first + tid; i < last; i += kSelectThreads) {
+        for (int i = first + tid; i < last; i += NT) {
             const uint32_t k = key[i];
             if ((mask && !(mask[i / 32] >> (i % 32) & 1u)) || k < from || k > to)
                 continue;
@@ -193,7 +200,7 @@ __device__ __noinline__ uint32_t kth_largest(SelectShared *sh, const uint32_t *k
     for (;;) {
         if (what == 1) {
 #pragma unroll 1
-            for (int k = tid; k < kSelectBins / 4; k += kSelectThreads)
+            for (int k = tid; k < kSelectBins / 4; k += NT)
                 *reinterpret_cast<uint4 *>(sh->hist + 4 * k) = make_uint4(0, 0, 0, 0);
         }
         __syncthreads();
@@ -211,14 +218,17 @@ __device__ __noinline__ uint32_t kth_largest(SelectShared *sh, const uint32_t *k
             what = 1;
         } else if (what == 1) {
             __syncthreads();
-            // thread t adds up bins [at, at + 8), from the highest down
-            constexpr int BPT = kSelectBins / kSelectThreads;
-            static_assert(BPT == 8, "two 16-byte reads");
+            // thread t adds up bins [at, at + BPT), from the highest down
+            constexpr int BPT = kSelectBins / NT;
             const int at = kSelectBins - BPT * (tid + 1);
-            const uint4 a = *reinterpret_cast<const uint4 *>(sh->hist + at), b = *reinterpret_cast<const uint4 *>(sh->hist + at + 4);
-            const uint32_t sum = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+            uint32_t sum = 0;
+#pragma unroll
+            for (int k = 0; k < BPT; k += 4) {
+                const uint4 a = *reinterpret_cast<const uint4 *>(sh->hist + at + k);
+                sum += (a.x + a.y) + (a.z + a.w);
+            }
             uint32_t total;
-            uint32_t above = cta_exclusive(sum, sh->scan, &total);
+            uint32_t above = cta_exclusive<NT>(sum, sh->scan, &total);
             if (above < m && m <= above + sum) {
                 int k = at + BPT - 1;
                 while (above + sh->hist[k] < m)
@@ -233,7 +243,7 @@ __device__ __noinline__ uint32_t kth_largest(SelectShared *sh, const uint32_t *k
             const uint32_t base = from + (sh->pick[0] << shift);
             to = base + min(to - base, (1u << shift) - 1u);
             from = base;
-            what = shift > 0 && sh->pick[2] <= kSelectList ? 2 : 1;
+            what = shift > 0 && sh->pick[2] <= NT ? 2 : 1;
         } else {
             __syncthreads();
             const uint32_t inside = sh->pick[2];
@@ -520,11 +530,11 @@ __device__ __forceinline__ float score_blocks(const SelectParams &p, ScoreShared
 
 // The selection of row (seq, kvh) of n blocks from its keys and its chunks'
 // bounds, by one CTA.  in, pend: a bit for each block.
-template <typename T, int D>
+template <typename T, int D, int NT>
 __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *sh, uint32_t *key, uint32_t *in,
                                            uint32_t *pend, const float *bounds, int seq, int kvh, int n)
 {
-    constexpr int NW = kSelectThreads / 32;
+    constexpr int NW = NT / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int K = p.num_selected;
     const int32_t *table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
@@ -548,7 +558,7 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
         if (bad && tid == 0)
             report(p.status, PKV_DEV_BAD_BLOCK);
         const int have = bad ? 0 : n;
-        for (int i = tid; i < K; i += kSelectThreads)
+        for (int i = tid; i < K; i += NT)
             out[i] = i < have ? i : -1;
         return;
     }
@@ -560,14 +570,14 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
     if (m > 0) {
         const float eps = S * kScoreErr;
         uint32_t left;
-        const float t = key_value(kth_largest(sh, key, first, last, nullptr, m, &left));
+        const float t = key_value(kth_largest<NT>(sh, key, first, last, nullptr, m, &left));
         const bool finite = fabsf(t) < INFINITY && eps < INFINITY;   // else all are in doubt
         hi_edge = finite ? t + 2.f * eps : INFINITY;
         lo_edge = finite ? t - 2.f * eps : -INFINITY;
     }
     uint32_t counts = 0;   // sure ones below, those in doubt above 16 bits, of this thread's
 #pragma unroll 2
-    for (int i = tid; i < words * 32; i += kSelectThreads) {   // a warp's 32 blocks are one word
+    for (int i = tid; i < words * 32; i += NT) {   // a warp's 32 blocks are one word
         bool a = i < n, b = false;
         if (i >= first && i < last) {
             const float s = key_value(key[i]);
@@ -618,14 +628,14 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
                 s = pair_add(s, Pair{__shfl_xor_sync(0xffffffffu, s.h, off), __shfl_xor_sync(0xffffffffu, s.l, off)});
             return (unsigned long long)order_key(s.h) << 32 | order_key(fabsf(s.h) < INFINITY ? s.l : 0.f);
         };
-        if (doubt_total <= kSelectList) {
+        if (doubt_total <= NT) {
             // a few (two, mostly): listed in ascending order, ranked against each other
-            const int per = (words + kSelectThreads - 1) / kSelectThreads;
+            const int per = (words + NT - 1) / NT;
             const int w0 = min(tid * per, words), w1 = min(w0 + per, words);
             uint32_t c = 0, total;
             for (int k = w0; k < w1; ++k)
                 c += __popc(pend[k]);
-            c = cta_exclusive(c, sh->scan, &total);
+            c = cta_exclusive<NT>(c, sh->scan, &total);
             for (int k = w0; k < w1; ++k)
                 for (uint32_t w = pend[k]; w; w &= w - 1)
                     sh->list[c++] = k * 32 + __ffs(w) - 1;
@@ -636,7 +646,7 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
                 if (lane == 0)
                     score[e] = kk;
             }
-            for (int k = tid; k < words; k += kSelectThreads)
+            for (int k = tid; k < words; k += NT)
                 pend[k] = 0;
             __syncthreads();
             if (tid < (int)doubt_total) {
@@ -661,10 +671,10 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
             }
             __syncthreads();
             uint32_t left;
-            const uint32_t t = kth_largest(sh, key, 0, n, pend, ties, &left);
+            const uint32_t t = kth_largest<NT>(sh, key, 0, n, pend, ties, &left);
             __syncthreads();
             uint32_t still = 0;
-            for (int i = tid; i < words * 32; i += kSelectThreads) {
+            for (int i = tid; i < words * 32; i += NT) {
                 const uint32_t old = pend[i / 32];
                 const bool is = i < n && (old >> lane & 1u);
                 const uint32_t k = is ? key[i] : 0u;
@@ -678,7 +688,7 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
             }
             ties = left;
             uint32_t total;
-            (void)cta_exclusive(still, sh->scan, &total);
+            (void)cta_exclusive<NT>(still, sh->scan, &total);
             if (total == ties)
                 break;
         }
@@ -686,7 +696,7 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
     __syncthreads();
 
     // ---- emission in ascending order: thread t owns words [w0, w1)
-    const int per = (words + kSelectThreads - 1) / kSelectThreads;
+    const int per = (words + NT - 1) / NT;
     const int w0 = min(tid * per, words), w1 = min(w0 + per, words);
     uint32_t total;
     if (some_tie) {
@@ -695,7 +705,7 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
 #pragma unroll 1
         for (int k = w0; k < w1; ++k)
             c += __popc(pend[k]);
-        uint32_t seen = cta_exclusive(c, sh->scan, &total);
+        uint32_t seen = cta_exclusive<NT>(c, sh->scan, &total);
 #pragma unroll 1
         for (int k = w0; k < w1; ++k) {
             uint32_t w = pend[k], kept = 0;
@@ -714,7 +724,7 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
         in[k] |= pend[k];
         c += __popc(in[k]);
     }
-    uint32_t at = cta_exclusive(c, sh->scan, &total);
+    uint32_t at = cta_exclusive<NT>(c, sh->scan, &total);
 #pragma unroll 1
     for (int k = w0; k < w1; ++k) {
         pend[k] = at;   // selected blocks before the word's
@@ -722,7 +732,7 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
     }
     __syncthreads();
 #pragma unroll 2
-    for (int i = tid; i < n; i += kSelectThreads) {
+    for (int i = tid; i < n; i += NT) {
         const uint32_t w = in[i / 32];
         if (w >> (i % 32) & 1u)
             out[pend[i / 32] + __popc(w & ((1u << (i % 32)) - 1u))] = i;
@@ -730,13 +740,13 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
 }
 
 // One launch: a cluster per row; grid (CTAs of a row, kv head, sequence).
-template <typename T, int D>
-__global__ void __launch_bounds__(kSelectThreads)
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(NT)
 select_blocks_kernel(const __grid_constant__ SelectParams p)
 {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
-    constexpr int NW = kSelectThreads / 32;
+    constexpr int NW = NT / 32;
     extern __shared__ __align__(16) uint8_t smem[];
     SelectShared *sh = reinterpret_cast<SelectShared *>(smem);
     using Score = ScoreShared<D, NW, 1>;
@@ -754,7 +764,7 @@ select_blocks_kernel(const __grid_constant__ SelectParams p)
         cluster.map_shared_rank(sh, 0)->bound[me * NW + (threadIdx.x >> 5)] = S;
     cluster.sync();
     if (me == 0)
-        select_row<T, D>(p, sh, key, in, pend, sh->bound, seq, kvh, n);
+        select_row<T, D, NT>(p, sh, key, in, pend, sh->bound, seq, kvh, n);
 }
 
 // Two launches: scores into the workspace; grid (kv head, chunk, sequence), so
@@ -781,8 +791,8 @@ score_blocks_kernel(const __grid_constant__ SelectParams p)
 
 // The second launch, a programmatic dependent of the first: grid (kv head,
 // sequence).
-template <typename T, int D>
-__global__ void __launch_bounds__(kSelectThreads)
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(NT)
 select_rows_kernel(const __grid_constant__ SelectParams p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -804,7 +814,7 @@ select_rows_kernel(const __grid_constant__ SelectParams p)
         mbar_init(&sh->bar, 1);
         fence_mbar_init();
     }
-    const float scale = weight_scale<kSelectThreads / 32>(big, sh->scan);
+    const float scale = weight_scale<NT / 32>(big, sh->scan);
     if (tid < D)
         exact_weights<D>(sh->weight, x, scale);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -824,7 +834,7 @@ select_rows_kernel(const __grid_constant__ SelectParams p)
         n = __syncthreads_and(n != 0) ? n : 0;
     }
     __syncthreads();
-    select_row<T, D>(p, sh, key, in, pend, p.ws_bound + row * p.bounds, seq, kvh, n);
+    select_row<T, D, NT>(p, sh, key, in, pend, p.ws_bound + row * p.bounds, seq, kvh, n);
 }
 
 }  // namespace pkv

@@ -210,26 +210,42 @@ def test_select_through_the_workspace():
     Lengths from 0 on, a sequence of equal blocks, NaN, a bad table and a bad
     length among them; the workspace given and not."""
     rng = np.random.RandomState(2)
-    lens = rng.randint(1, 400 * 8, 28)
-    lens[3], lens[5], lens[7] = 0, 400 * 8, 399 * 8 + 1
+    lens = rng.randint(1, 1200 * 8, 28)
+    lens[3], lens[5], lens[7] = 0, 1200 * 8, 1199 * 8 + 1
     c = select_case(12, lens, G=2, Hk=4, D=64, bs=8, t="bf16")
-    assert pkv.select_blocks_workspace_bytes(28, 4, 400 * 8, 8) > 0
+    assert pkv.select_blocks_workspace_bytes(28, 4, 1200 * 8, 8) > 0
     t = c["tables"]
-    c["sums"][t[5, :400]] = c["sums"][t[5, 0]].clone()
+    c["sums"][t[5, :1200]] = c["sums"][t[5, 0]].clone()
     c["sums"][t[7, 100], 2, 0, 5] = float("nan")
     for K in (3, 48, 200):
-        got, st = run_select(c, K, 1, 2, max_len=400 * 8)
+        got, st = run_select(c, K, 1, 2, max_len=1200 * 8)
         assert st == 0
         np.testing.assert_array_equal(got, want_select(c, K, 1, 2))
-    ws = torch.full((pkv.select_blocks_workspace_bytes(28, 4, 400 * 8, 8),), 255, dtype=torch.uint8, device=DEV)
+    ws = torch.full((pkv.select_blocks_workspace_bytes(28, 4, 1200 * 8, 8),), 255, dtype=torch.uint8, device=DEV)
     sel, st = torch.zeros(28, 4, 48, dtype=torch.int32, device=DEV), status()
-    good, _ = run_select(c, 48, 0, 1, max_len=400 * 8)
-    c["tables"][11, (lens[11] - 1) // 8], c["lens"][12] = -1, 401 * 8
+    good, _ = run_select(c, 48, 0, 1, max_len=1200 * 8)
+    c["tables"][11, (lens[11] - 1) // 8], c["lens"][12] = -1, 1201 * 8
     pkv.select_blocks(sel, c["q"].to(DEV), c["sums"].to(DEV), dev(c["tables"]), dev(c["lens"]), 8, keep_first=0, keep_last=1,
-                      max_context_len=400 * 8, workspace=ws, device_status=st)
+                      max_context_len=1200 * 8, workspace=ws, device_status=st)
     assert st.item() == pkv.DEV_BAD_BLOCK | pkv.DEV_BAD_CONTEXT_LEN
     good[[11, 12]] = -1
     np.testing.assert_array_equal(sel.cpu().numpy(), good)
+
+
+@pytest.mark.parametrize("B, Hk, n", [(80, 8, 5), (80, 8, 200), (31, 5, 60), (40, 8, 130), (19, 8, 250)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_select_of_many_rows(B, Hk, n, D):
+    """More rows than SMs hold CTAs: smaller CTAs, in one launch and in two; bins of
+    equal scores among them."""
+    rng = np.random.RandomState(n)
+    lens = rng.randint(0, n * 16 + 1, B)
+    lens[0], lens[1] = n * 16, 0
+    c = select_case(21, lens, G=2, Hk=Hk, D=D, t="bf16")
+    c["sums"][c["tables"][0, :n]] = c["sums"][c["tables"][0, 0]].clone()
+    for K in (4, n // 3 + 2):
+        got, st = run_select(c, K, 1, 2)
+        assert st == 0
+        np.testing.assert_array_equal(got, want_select(c, K, 1, 2))
 
 
 def test_select_refuses_bad_rows():
