@@ -325,6 +325,25 @@ def test_selected_attention(kind, D, bs, G):
                 assert (np.abs(got - ref) <= tol).all(), np.abs(got - ref).max()
 
 
+def test_lists_longer_than_the_contexts():
+    """Many rows, and room for more blocks than any context has: the whole
+    attention, and a list that goes on behind its end is still refused."""
+    rng = np.random.RandomState(5)
+    lens = rng.randint(0, 141, 100)
+    c = S.q8_case(9, G=2, Hk=2, D=64, lens=lens)
+    sel = np.full((100, 2, 300), -1, np.int32)
+    for s, L in enumerate(lens):
+        sel[s, :, : -(-int(L) // 16)] = np.arange(-(-int(L) // 16))
+    got, st = run_selected(c, sel)
+    assert st == 0
+    check(c, got, torch.float32)
+    sel[7, 1, 290] = 0
+    bad, st = run_selected(c, sel)
+    assert st == pkv.DEV_BAD_BLOCK
+    got[7, 2:] = 0
+    np.testing.assert_array_equal(bad, got)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "q8"])
 def test_all_blocks_selected_is_the_whole_attention(kind):
     c = S.q8_case(3, G=4, Hk=2, lens=(700, 16, 1))
