@@ -37,7 +37,8 @@
  *     Read *device_status after synchronising the stream.
  *   - Element types: q, k_cache, v_cache share kv_dtype (except where a cache
  *     holds 8-bit values); arithmetic is fp32 (fp32 accumulation for fp16/bf16
- *     inputs).
+ *     inputs; softmax weights that meet 16-bit or 8-bit values on tensor cores
+ *     do so in two 16-bit parts).
  */
 #ifndef PKV_H
 #define PKV_H
@@ -460,6 +461,9 @@ int pkv_append_cache_q8(const void *key, const void *value, int dtype, void *k_c
  * head_dim 64 or 128; block_size 8, 16 or 32; num_heads / num_kv_heads 1 to 8;
  * num_seqs and num_kv_heads up to 65,535.  Device errors as for
  * pkv_paged_attention_decode: the rows they concern are zero.
+ * Scores, softmax sums and accumulators are fp32.  The softmax weights enter
+ * the product with V in two 16-bit parts: each is off by at most 2^-22 of
+ * itself (2^-16 over a bfloat16 cache), whatever out_dtype is.
  */
 int pkv_paged_attention_decode_q8(void *out, int out_dtype, const void *q, int q_dtype,
                                   const void *k_cache, const void *v_cache, const float *k_scales,

@@ -288,7 +288,6 @@ struct ListEngine {
     float qs[2];             // score factors of heads 2c, 2c + 1
     uint32_t koff[4], voff[4];   // this lane's ldmatrix offsets in a tile, 64 bytes of a row
     int g, c;
-    bool lo;                 // weights in two 16-bit parts
 
     // Issues the loads of q.
     __device__ __forceinline__ void load(const ListParams &p, int seq, int kvh, int lane)
@@ -314,10 +313,6 @@ struct ListEngine {
     __device__ __forceinline__ void init(const ListParams &p)
     {
         const int lane = threadIdx.x & 31;
-        // A weight in f16 is off by 2^-12 of itself at most, less than the
-        // output's rounding to bfloat16; bfloat16 weights, and the other
-        // outputs, take a second part.
-        lo = !std::is_same<M, __half>::value || p.out_dtype != PKV_BF16;
         const int tk = (lane & 7) + ((lane >> 3) & 1) * 8, dk = lane >> 4;
         const int tv = C::Q8 ? tk : (lane & 7) + (lane >> 4) * 8, dv = C::Q8 ? dk : (lane >> 3) & 1;
 #pragma unroll
@@ -454,14 +449,15 @@ struct ListEngine {
             __syncwarp();
         }
 
+        // The weights enter the product in two 16-bit parts (whatever the
+        // output's type: what one part drops is not small beside values that
+        // cancel): off by (half a step)^2 of themselves, 2^-22 in f16, 2^-16 in
+        // bfloat16.
         const uint32_t h0 = Mma<M>::pack(p0[0], p0[1]), h1 = Mma<M>::pack(p1[0], p1[1]);
         const uint32_t bh0 = movmatrix_trans(h0), bh1 = movmatrix_trans(h1);
-        uint32_t bl0 = 0u, bl1 = 0u;
-        if (lo) {
-            const float2 f0 = Mma<M>::unpack(h0), f1 = Mma<M>::unpack(h1);
-            bl0 = movmatrix_trans(Mma<M>::pack(p0[0] - f0.x, p0[1] - f0.y));
-            bl1 = movmatrix_trans(Mma<M>::pack(p1[0] - f1.x, p1[1] - f1.y));
-        }
+        const float2 f0 = Mma<M>::unpack(h0), f1 = Mma<M>::unpack(h1);
+        const uint32_t bl0 = movmatrix_trans(Mma<M>::pack(p0[0] - f0.x, p0[1] - f0.y));
+        const uint32_t bl1 = movmatrix_trans(Mma<M>::pack(p1[0] - f1.x, p1[1] - f1.y));
         if constexpr (C::Q8) {
 #pragma unroll
             for (int j = 0; j < KS / 2; ++j) {
@@ -476,23 +472,20 @@ struct ListEngine {
                     float *acc = o[2 * j + i];
                     if constexpr (BS == 8) {
                         mma_k8(t, a[0], a[1], bh0);
-                        if (lo)
-                            mma_k8(t, a[0], a[1], bl0);
+                        mma_k8(t, a[0], a[1], bl0);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             acc[k] = fmaf(vs0, t[k], acc[k]);
                             t[k] = 0.f;
                         }
                         mma_k8(t, a[2], a[3], bh1);
-                        if (lo)
-                            mma_k8(t, a[2], a[3], bl1);
+                        mma_k8(t, a[2], a[3], bl1);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             acc[k] = fmaf(vs1, t[k], acc[k]);
                     } else {
                         Mma<M>::run(t, a, bh0, bh1);
-                        if (lo)
-                            Mma<M>::run(t, a, bl0, bl1);
+                        Mma<M>::run(t, a, bl0, bl1);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             acc[k] = fmaf(vs0, t[k], acc[k]);
@@ -505,8 +498,7 @@ struct ListEngine {
                 uint32_t a[4];
                 ldsm_x4_trans(vbase + chunk_off(mt) + voff[mt & 3], a);
                 Mma<M>::run(o[mt], a, bh0, bh1);
-                if (lo)
-                    Mma<M>::run(o[mt], a, bl0, bl1);
+                Mma<M>::run(o[mt], a, bl0, bl1);
             }
         }
     }
