@@ -462,8 +462,9 @@ int pkv_append_cache_q8(const void *key, const void *value, int dtype, void *k_c
  * num_seqs and num_kv_heads up to 65,535.  Device errors as for
  * pkv_paged_attention_decode: the rows they concern are zero.
  * Scores, softmax sums and accumulators are fp32.  The softmax weights enter
- * the product with V in two 16-bit parts: each is off by at most 2^-22 of
- * itself (2^-16 over a bfloat16 cache), whatever out_dtype is.
+ * the product with V in two 16-bit parts, whatever out_dtype is: each is off by
+ * at most 2^-22 of itself and 2^-32 of the row's largest weight (2^-16 of
+ * itself over a bfloat16 cache).
  */
 int pkv_paged_attention_decode_q8(void *out, int out_dtype, const void *q, int q_dtype,
                                   const void *k_cache, const void *v_cache, const float *k_scales,

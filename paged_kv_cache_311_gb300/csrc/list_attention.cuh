@@ -281,6 +281,11 @@ struct ListEngine {
     using C = ListCfg<T, D, BS>;
     using M = typename ListElem<T>::M;
     static constexpr int KS = C::KS;
+    // What a weight (at most 2^kSlack) is multiplied by on its way to its parts
+    // of M's type: f16's numbers end at 2^-24, and weights of that size count
+    // where a context has many of them beside one large weight of value 0.
+    // Taken back from a tile's product with the V scale, or at the end.
+    static constexpr float kLift = std::is_same<M, __half>::value ? 128.f : 1.f;
 
     uint32_t qf[KS][2];      // q^T B-fragments of head g
     float o[KS][4];          // O^T C-fragments
@@ -364,7 +369,8 @@ struct ListEngine {
     __device__ __forceinline__ static uint32_t chunk_off(int k) { return (uint32_t)((k >> 2) * C::BOX_LINES * 128); }
 
     // A tile's tokens: rows 0..7 with scales ks0, vs0, rows 8..15 with ks1,
-    // vs1 (the same unless a block holds 8 tokens); nvalid of them count.
+    // vs1 (the same unless a block holds 8 tokens; vs0 and vs1 divided by
+    // kLift); nvalid of them count.
     __device__ __forceinline__ void tile(uint32_t kbase, uint32_t vbase, int nvalid, int lane, float ks0, float ks1,
                                          float vs0, float vs1)
     {
@@ -452,7 +458,13 @@ struct ListEngine {
         // The weights enter the product in two 16-bit parts (whatever the
         // output's type: what one part drops is not small beside values that
         // cancel): off by (half a step)^2 of themselves, 2^-22 in f16, 2^-16 in
-        // bfloat16.
+        // bfloat16; f16 parts of tiny ones by half their last bit, 2^-25 / kLift
+        // of the largest weight.
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            p0[j] *= kLift;
+            p1[j] *= kLift;
+        }
         const uint32_t h0 = Mma<M>::pack(p0[0], p0[1]), h1 = Mma<M>::pack(p1[0], p1[1]);
         const uint32_t bh0 = movmatrix_trans(h0), bh1 = movmatrix_trans(h1);
         const float2 f0 = Mma<M>::unpack(h0), f1 = Mma<M>::unpack(h1);
@@ -515,6 +527,14 @@ struct ListEngine {
     // the merge scratch.
     __device__ __forceinline__ void finish(float *mw, float *lw, float *aw, int warp, int group)
     {
+        if constexpr (!C::Q8 && kLift != 1.f) {
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    o[mt][k] *= 1.f / kLift;
+            }
+        }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             float l = lsum[j];
@@ -636,7 +656,7 @@ list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constan
         for (int k = (int)threadIdx.x; k * BS < tokens; k += kListThreads) {
             const int64_t at = (int64_t)phys[k] * p.scale_stride + kvh;
             ks_s[k] = p.k_scales[at];
-            vs_s[k] = p.v_scales[at];
+            vs_s[k] = p.v_scales[at] * (1.f / ListEngine<T, D, BS>::kLift);   // exact: a power of two
         }
     }
     eng.init(p);

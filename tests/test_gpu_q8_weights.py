@@ -1,6 +1,7 @@
 """Attention over an 8-bit cache and over selected blocks on the GPU, where an
 error of the softmax weights shows: values that cancel, so that the output is
-small beside them; weights close to each other."""
+small beside them; weights close to each other; many that are tiny beside one
+whose value is 0."""
 import numpy as np
 import pytest
 import torch
@@ -108,3 +109,38 @@ def test_scores_near_zero(kind, L):
     v = S.nearest(np.clip(rng.randn(L, D) * 60, -448, 448))
     q = torch.from_numpy(rng.randn(1, 8, D) * 2.0 ** -20).to(S.DT["bf16" if kind == "q8" else kind])
     compare(kind, q, k, v, L, 16, D ** -0.5, (torch.float32, torch.bfloat16), (0, 64))
+
+
+@pytest.mark.parametrize("kind", ["q8", "f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bs", [8, 16, 32])
+def test_tiny_weights_that_count_together(kind, D, bs):
+    """4096 tokens: four with a large score and the value 0 (the first of four
+    tiles of 16), the others with weights of 2^-23 to 2^-30 of theirs and the
+    value 448: the output is those weights' sum.  A weight in f16 parts may
+    also be off by 2^-32 of the largest."""
+    L = 4096
+    k, v = np.zeros((L, D)), np.full((L, D), 448.0)
+    k[[0, 16, 32, 48], 0], v[[0, 16, 32, 48]] = 16.0, 0.0
+    x = torch.tensor([23.0, 23.5, 24.0, 25.0, 26.0, 27.0, 28.5, 30.0])   # all f16 and bfloat16 numbers
+    for t in ("bf16", "f16") if kind == "q8" else (kind,):
+        q = torch.zeros(1, 8, D)
+        q[0, :, 0] = x
+        scale = float(np.float32(np.log(2.0) / 16))
+        tables, kv = cache(kind, k, v, bs)
+        args = (q.double().numpy(), kv[0][0])
+        lens = np.array([L], np.int32)
+        ref, bound = S.attention_reference(*args, kv[1][0], tables, lens, bs, scale)
+        w = np.exp(-scale * 16.0 * x.double().numpy())
+        largest = 1 / (4 + (L - 4) * w)
+        np.testing.assert_allclose(ref[0, :, 0], 448.0 * (L - 4) * w * largest, rtol=1e-12)
+        for out_dtype in (torch.float32, torch.float16, torch.bfloat16):
+            tol = tolerance(ref, ref, bound, L, D, kind, out_dtype)   # every value is positive
+            if kind != "bf16":   # (rounded with the output)
+                tol = tol + (2.0 ** -32 * largest * (L - 4) * 448.0)[None, :, None] * (1 + 2.0 ** -8)
+            assert (tol < ref * 0.6).all()
+            for P in (0, 4096):
+                for listed in (False, True) if kind == "q8" else (True,):
+                    got = attend(kind, q.to(S.DT[t]), tables, kv, L, bs, scale, out_dtype, P, listed)
+                    bad = ~(np.abs(got - ref) <= tol)
+                    assert not bad.any(), (out_dtype, P, listed, np.argwhere(bad)[:3], got[bad][:3], ref[bad][:3], tol[bad][:3])
