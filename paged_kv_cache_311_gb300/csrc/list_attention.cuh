@@ -47,6 +47,10 @@
 
 namespace pkv {
 
+// The reference that weights are taken against: the largest score, or 0 where
+// there is none yet, so that 2^(-inf - reference) is 0 and not NaN.
+__device__ __forceinline__ float reference_of(float m) { return m == -INFINITY ? 0.f : m; }
+
 struct ListParams {
     void *out;
     const void *q;
@@ -232,7 +236,7 @@ __device__ __forceinline__ void write_result(const ListParams &p, ListResult<D> 
                 M = fmaxf(M, m[k]);
                 bad |= l[k] < 0.f;
             }
-            const float ref = fmaxf(M, -1e30f);
+            const float ref = reference_of(M);
             float den = 0.f;
             float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -420,7 +424,7 @@ struct ListEngine {
                 tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
                 const float mn = fmaxf(m[j], tm);
                 // no number yet: the sums are zero (or NaN), whatever alpha is
-                alpha[j] = ex2_fast(m[j] - fmaxf(mn, -1e30f));
+                alpha[j] = ex2_fast(m[j] - reference_of(mn));
                 lsum[j] *= alpha[j];
                 m[j] = mn;
             }
@@ -434,8 +438,7 @@ struct ListEngine {
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            // the finite stand-in keeps 2^(-inf - m) at 0; a NaN score stays NaN
-            const float mr = fmaxf(m[j], -1e30f);
+            const float mr = reference_of(m[j]);   // a NaN score stays NaN
             p0[j] = ex2_fast(x0[j] - mr);
             p1[j] = ex2_fast(x1[j] - mr);
             lsum[j] += p0[j] + p1[j];
@@ -716,7 +719,7 @@ list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constan
 #pragma unroll
         for (int w = 0; w < NW; ++w)
             Mx = fmaxf(Mx, mw[w * kListMaxGroup + r]);
-        const float ref = fmaxf(Mx, -1e30f);
+        const float ref = reference_of(Mx);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
             const float f = exp2f(mw[w * kListMaxGroup + r] - ref);   // 0 for a warp without tokens; NaN sums stay
@@ -785,7 +788,7 @@ list_merge_kernel(const __grid_constant__ ListParams p, int per_head)
             mn = fmaxf(mn, t[u].x);
             bad |= t[u].y < 0.f;
         }
-        const float ref = fmaxf(mn, -1e30f);
+        const float ref = reference_of(mn);
         const float f0 = exp2f(mx - ref);
         den *= f0;
 #pragma unroll
@@ -828,7 +831,7 @@ list_merge_kernel(const __grid_constant__ ListParams p, int per_head)
             M = fmaxf(M, s_m[w]);
             bad |= s_bad[w] != 0;
         }
-        const float ref = fmaxf(M, -1e30f);
+        const float ref = reference_of(M);
         den = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i)

@@ -144,3 +144,20 @@ def test_tiny_weights_that_count_together(kind, D, bs):
                     got = attend(kind, q.to(S.DT[t]), tables, kv, L, bs, scale, out_dtype, P, listed)
                     bad = ~(np.abs(got - ref) <= tol)
                     assert not bad.any(), (out_dtype, P, listed, np.argwhere(bad)[:3], got[bad][:3], ref[bad][:3], tol[bad][:3])
+
+
+@pytest.mark.parametrize("kind", ["q8", "f16", "bf16"])
+@pytest.mark.parametrize("L", [1, 40, 700])
+def test_scores_far_below_zero(kind, L):
+    """Finite scores of -3e32, and some of -6e32: the first share all weight."""
+    k, v = np.zeros((L, 64)), np.zeros((L, 64))
+    k[:, 0], v[:] = -1.0, np.arange(1, 65) % 8
+    k[1::3, 0], v[1::3] = -2.0, 448.0
+    tables, kv = cache(kind, k, v, 8)
+    q = torch.zeros(1, 8, 64, dtype=S.DT["bf16" if kind == "q8" else kind])
+    q[0, :, 0] = 1.0
+    for P in (0, 32, 2048):
+        for listed in (False, True) if kind == "q8" else (True,):
+            got = attend(kind, q, tables, kv, L, 8, 3e32, torch.float32, P, listed)
+            # equal weights: only the sum and the division round
+            np.testing.assert_allclose(got, np.broadcast_to(np.arange(1, 65) % 8, (1, 8, 64)), rtol=(L + 8) * 2.0 ** -24, atol=0)
