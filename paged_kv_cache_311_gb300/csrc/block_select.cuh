@@ -803,27 +803,32 @@ select_rows_kernel(const __grid_constant__ SelectParams p)
     const int kvh = blockIdx.x, seq = blockIdx.y;
     const int64_t row = (int64_t)seq * p.num_kv_heads + kvh;
     const int tid = threadIdx.x;
-    float x[8], big = 0.f;
-#pragma unroll
-    for (int h = 0; h < 8; ++h) {
-        x[h] = tid < D && h < p.group ? select_q(p, (row * p.group + h) * D + tid) : 0.f;
-        big = fmaxf(big, fabsf(x[h]) * 8.f);
-    }
-    int n = row_blocks(p, p.context_lens[seq], kvh == 0 && tid == 0);
     if (tid == 0) {
         mbar_init(&sh->bar, 1);
         fence_mbar_init();
     }
+    // Nothing is read before this wait: the first launch's start says that
+    // what precedes it has ended, not that this one sees what it wrote.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int L = p.context_lens[seq];
+    float x[8], big = 0.f;
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+        x[h] = tid < D && h < p.group ? select_q(p, (row * p.group + h) * D + tid) : 0.f;
+    int n = row_blocks(p, L, kvh == 0 && tid == 0);
+    if (n > p.num_selected && tid == 0) {
+        const uint32_t bytes = (uint32_t)(n + 3) / 4 * 16;
+        mbar_arrive_expect_tx(&sh->bar, bytes);
+        bulk_load(key, p.ws_keys + row * p.key_stride, bytes, &sh->bar);
+    }
+    // the weights of exact scores, while the keys come
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+        big = fmaxf(big, fabsf(x[h]) * 8.f);
     const float scale = weight_scale<NT / 32>(big, sh->scan);
     if (tid < D)
         exact_weights<D>(sh->weight, x, scale);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (n > p.num_selected) {
-        if (tid == 0) {
-            const uint32_t bytes = (uint32_t)(n + 3) / 4 * 16;
-            mbar_arrive_expect_tx(&sh->bar, bytes);
-            bulk_load(key, p.ws_keys + row * p.key_stride, bytes, &sh->bar);
-        }
         if (!mbar_wait_bounded(&sh->bar, 0)) {
             if (tid == 0) {
                 report(p.status, PKV_DEV_TIMEOUT);
