@@ -197,6 +197,18 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _scratch(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
+    """A workspace on like's device for a call on `stream` (None: the current
+    one).  It comes from that stream's own memory: what the allocator freed on
+    another stream may still be in use there."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+
+
 def _check(rc: int, what: str) -> None:
     if rc != 0:
         raise PkvError(rc, what)
@@ -247,7 +259,7 @@ def paged_attention_decode(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Te
     if workspace is None:
         nbytes = paged_attention_workspace_bytes(B, H, max_context_len, D, partition_size)
         if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            workspace = _scratch(nbytes, q, stream)
     L = load_library()
     rc = L.pkv_paged_attention_decode(
         _ptr(out), _DTYPE[out.dtype], _ptr(q), _ptr(k_cache), _ptr(v_cache), _DTYPE[k_cache.dtype],
@@ -473,7 +485,7 @@ def paged_attention_decode_shared(out: torch.Tensor, q: torch.Tensor, k_cache: t
     if max_context_len is None:
         max_context_len = int(context_lens.max().item()) if B else 0
     if workspace is None:
-        workspace = torch.empty(max(plan.workspace_bytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(max(plan.workspace_bytes, 16), q, stream)
     rc = load_library().pkv_paged_attention_decode_shared(
         _ptr(out), _DTYPE[out.dtype], _ptr(q), _ptr(k_cache), _ptr(v_cache), _DTYPE[k_cache.dtype],
         _ptr(block_tables), int(block_tables.shape[1]), _ptr(context_lens), B, H, Hk, D, bs, NB,
@@ -603,16 +615,6 @@ def _native():
         module.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _BOUND])
         _module = module
     return _module
-
-
-def _scratch(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
-    """A workspace on like's device for a call on `stream` (None: the current one)."""
-    t = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    if stream is not None:
-        # the allocator must not hand it out again before that stream is done with it
-        t.record_stream(stream if hasattr(stream, "cuda_stream")
-                        else torch.cuda.ExternalStream(int(stream), device=like.device))
-    return t
 
 
 def append_cache_q8(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
