@@ -84,7 +84,13 @@ constexpr int kScoreTiles = 8;
 // each: 2 x 17 x 2^-23 of what the chain adds up.  Joining the chains and the
 // three parts takes 5 roundings of 2^-24, the weights another 4 and the edges
 // T +- 2 eps two.  Together 40 x 2^-23; 44 are taken.
+//
+// Three parts of a weight w leave out at most 2^-24 |w| in bfloat16 (one of
+// the four above).  In f16 they leave out 2^-33 |w|, but not less than half of
+// f16's last bit, 2^-25, however small w is: kWeightPad, which every |w| in S
+// is raised by, makes eps cover it, 44 x 2^-23 x 2^-7 = 2^-24.5.
 constexpr float kScoreErr = 44.0f / (1 << 23);
+template <typename T> constexpr float kWeightPad = std::is_same<T, __half>::value ? 0x1p-7f : 0x1p-9f;
 
 // A float's bits as an unsigned number of the same order; NaN counts as +inf.
 __device__ __forceinline__ uint32_t order_key(float x)
@@ -451,8 +457,8 @@ __device__ __forceinline__ float score_blocks(const SelectParams &p, ScoreShared
                     sw->part[k][at] = *reinterpret_cast<const uint16_t *>(&one);
                     rest -= to_float(one);
                 }
-                // an upper bound, also of what the three parts leave out
-                one = from_float<T>(fabsf(w) * 1.015625f + 0x1p-9f);
+                // an upper bound, and kWeightPad for what the three parts leave out
+                one = from_float<T>(fabsf(w) * 1.015625f + kWeightPad<T>);
                 sw->part[3][at] = *reinterpret_cast<const uint16_t *>(&one);
             };
             split(-down[0] * scale, tid);
