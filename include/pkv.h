@@ -647,6 +647,16 @@ const char *pkv_status_string(int status);
 int pkv_test_bounded_wait(uint64_t limit_ns, uint64_t max_polls, uint32_t *device_status,
                           void *stream);
 
+/*
+ * Test hook of pkv_select_blocks' waits, as above: runs, on one CTA, what the
+ * selection of a row of 100 blocks does after a wait gave up (limit_ns: 1 ..
+ * 2e9).  what 1: a scoring warp has given up (and has reported it: no bit
+ * here); 2: a scoring warp has met a bad block id (PKV_DEV_BAD_BLOCK).  In each
+ * case selected (int32 [num_selected], num_selected < 100) receives -1.
+ */
+int pkv_test_select_timeout(int what, uint64_t limit_ns, int32_t *selected, int num_selected,
+                            uint32_t *device_status, void *stream);
+
 /* Number of kernels the last successful pkv_paged_attention_decode call on
  * this host thread enqueued (1 = single pass, 2 = partition pass + reduce). */
 int pkv_last_decode_launches(void);

@@ -36,7 +36,7 @@ __all__ = [
     "set_decode_engine", "last_decode_engine", "kv_cache_usage", "KvCacheUsage", "swap_blocks",
     "SWAP_OUT", "SWAP_IN", "BlockPool",
     "DEV_BAD_BLOCK", "DEV_BAD_SLOT", "DEV_TIMEOUT", "DEV_BAD_CONTEXT_LEN", "DEV_DRAIN_TIMEOUT",
-    "HEADER_PATH", "bounded_wait_hook",
+    "HEADER_PATH", "bounded_wait_hook", "select_timeout_hook",
     "append_cache_q8", "summarize_blocks", "select_blocks", "paged_attention_decode_q8",
     "paged_attention_decode_selected", "paged_attention_list_workspace_bytes", "q8_scales",
     "select_blocks_workspace_bytes",
@@ -151,6 +151,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     L.pkv_decode_set_engine.argtypes = [i32]
     L.pkv_decode_set_engine.restype = i32
     L.pkv_test_bounded_wait.argtypes = [ctypes.c_uint64, ctypes.c_uint64, vp, vp]
+    L.pkv_test_select_timeout.argtypes = [i32, ctypes.c_uint64, vp, i32, vp, vp]
+    L.pkv_test_select_timeout.restype = i32
     L.pkv_test_bounded_wait.restype = i32
     if path is None:
         _lib = L
@@ -504,6 +506,17 @@ def bounded_wait_hook(device_status: torch.Tensor, limit_ns: int, max_polls: int
     _need_cuda(device_status)
     _check(load_library().pkv_test_bounded_wait(int(limit_ns), int(max_polls), _ptr(device_status),
                                                 _stream(stream)), "pkv_test_bounded_wait")
+
+
+def select_timeout_hook(what: int, selected: torch.Tensor, device_status: torch.Tensor, limit_ns: int,
+                        stream=None) -> None:
+    """Test hook: what a selection makes of a wait that gave up (see
+    pkv_test_select_timeout); selected: int32 [K], K < 100."""
+    _need_cuda(selected, device_status)
+    if selected.dtype != torch.int32:
+        raise ValueError("selected must be int32")
+    _check(load_library().pkv_test_select_timeout(int(what), int(limit_ns), _ptr(selected), selected.numel(),
+                                                  _ptr(device_status), _stream(stream)), "pkv_test_select_timeout")
 
 
 def reshape_and_cache(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,

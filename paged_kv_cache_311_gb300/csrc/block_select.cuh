@@ -338,7 +338,10 @@ __device__ __forceinline__ int row_blocks(const SelectParams &p, int L, bool tel
     return (L + p.block_size - 1) / p.block_size;
 }
 
+// What a scoring warp gives in place of its S: one of its blocks' ids is
+// outside the pool; a copy timed out (and was reported).
 constexpr float kBadChunk = -1.f;
+constexpr float kLateChunk = -2.f;
 
 // Shared memory of a scoring CTA of NW warps with rings of S tiles: the
 // weights [part][2 D] in the summaries' type -- three parts of -Q- (minima) and
@@ -364,8 +367,7 @@ __device__ __forceinline__ void bulk_load(void *dst_smem, const void *src, uint3
 
 // Keys of blocks [b0, b0 + p.chunk) of row (seq, kvh) into keys[0 ..], by a CTA
 // of NW warps.  Returns each warp's S (in units of the weights' scale), or
-// kBadChunk if one of its blocks' ids is outside the pool or a copy timed out;
-// nothing is scored in a row that is selected whole.  n receives the row's
+// kBadChunk or kLateChunk; nothing is scored in a row that is selected whole.  n receives the row's
 // number of blocks, weight (unless null) the weights of exact scores;
 // before_stores() runs before the first store.
 template <typename T, int D, int NW, int ST, typename Before>
@@ -489,7 +491,7 @@ __device__ __forceinline__ float score_blocks(const SelectParams &p, ScoreShared
                     drain_wait(&bar[u % ST], (uint32_t)((u / ST) & 1), p.status);
                 if (lane == 0)
                     report(p.status, PKV_DEV_TIMEOUT);
-                return kBadChunk;
+                return __any_sync(0xffffffffu, bad) ? kBadChunk : kLateChunk;
             }
             const uint32_t base = smem_u32(sw->ring[warp][st]) + row;
             float s[8][4], b[4] = {0.f, 0.f, 0.f, 0.f};
@@ -546,24 +548,26 @@ __device__ __forceinline__ void select_row(const SelectParams &p, SelectShared *
     const int32_t *table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
     // the chunks' bounds, a lane each: NaN and infinity order above numbers
     float S;
-    bool bad = false;
+    bool bad = false, late = false;
     {
         uint32_t most = 0;
         for (int c = lane; c < p.bounds; c += 32) {
             const float x = bounds[c];
             bad |= x == kBadChunk;
+            late |= x == kLateChunk;
             most = max(most, __float_as_uint(x) & 0x7fffffffu);
         }
         bad = __any_sync(0xffffffffu, bad);
+        late = __any_sync(0xffffffffu, late);
         S = __uint_as_float(__reduce_max_sync(0xffffffffu, most));
         S = !(S <= 3.0e38f) ? INFINITY : S;
     }
     int32_t *out = p.selected + ((int64_t)seq * p.num_kv_heads + kvh) * K;
-    if (bad || n <= K) {
+    if (bad || late || n <= K) {
         // a refused row selects nothing; a short one selects everything
         if (bad && tid == 0)
             report(p.status, PKV_DEV_BAD_BLOCK);
-        const int have = bad ? 0 : n;
+        const int have = bad || late ? 0 : n;
         for (int i = tid; i < K; i += NT)
             out[i] = i < have ? i : -1;
         return;
@@ -846,6 +850,22 @@ select_rows_kernel(const __grid_constant__ SelectParams p)
     }
     __syncthreads();
     select_row<T, D, NT>(p, sh, key, in, pend, p.ws_bound + row * p.bounds, seq, kvh, n);
+}
+
+// Test hook: what select_row makes of a scoring warp that gave up (what 1) or
+// met a bad id (2), on one CTA and a row of 100 blocks.
+__global__ void __launch_bounds__(kSelectThreads)
+select_timeout_test_kernel(const __grid_constant__ SelectParams p, int what)
+{
+    __shared__ SelectShared sh;
+    __shared__ float bounds[2];
+    if (threadIdx.x == 0) {
+        bounds[0] = 1.f;
+        bounds[1] = what == 1 ? kLateChunk : kBadChunk;
+    }
+    __syncthreads();
+    // the row is refused: no key, bit or table is looked at
+    select_row<__half, 64, kSelectThreads>(p, &sh, nullptr, nullptr, nullptr, bounds, 0, 0, 100);
 }
 
 }  // namespace pkv
