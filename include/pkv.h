@@ -650,7 +650,8 @@ int pkv_test_bounded_wait(uint64_t limit_ns, uint64_t max_polls, uint32_t *devic
 /*
  * Test hook of pkv_select_blocks' waits, as above: runs, on one CTA, what the
  * selection of a row of 100 blocks does after a wait gave up (limit_ns: 1 ..
- * 2e9).  what 1: a scoring warp has given up (and has reported it: no bit
+ * 2e9).  what 0: the scores never come, and only some threads notice (both
+ * timeout bits); 1: a scoring warp has given up (and has reported it: no bit
  * here); 2: a scoring warp has met a bad block id (PKV_DEV_BAD_BLOCK).  In each
  * case selected (int32 [num_selected], num_selected < 100) receives -1.
  */

@@ -190,7 +190,7 @@ extern "C" int pkv_select_blocks(int32_t *selected, const void *q, int q_dtype, 
 extern "C" int pkv_test_select_timeout(int what, uint64_t limit_ns, int32_t *selected, int num_selected,
                                        uint32_t *device_status, void *stream)
 {
-    if (what < 1 || what > 2 || limit_ns == 0 || limit_ns > kWaitLimitNs || !selected || num_selected <= 0 ||
+    if (what < 0 || what > 2 || limit_ns == 0 || limit_ns > kWaitLimitNs || !selected || num_selected <= 0 ||
         num_selected >= 100 || !device_status || !aligned(selected, 4) || !aligned(device_status, 4))
         return PKV_EINVAL;
     SelectParams p = {};
@@ -199,6 +199,6 @@ extern "C" int pkv_test_select_timeout(int what, uint64_t limit_ns, int32_t *sel
     p.num_selected = num_selected;
     p.num_seqs = p.num_kv_heads = 1;
     p.bounds = 2;
-    select_timeout_test_kernel<<<1, kSelectThreads, 0, static_cast<cudaStream_t>(stream)>>>(p, what);
+    select_timeout_test_kernel<<<1, kSelectThreads, 0, static_cast<cudaStream_t>(stream)>>>(p, what, limit_ns);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }

@@ -343,6 +343,21 @@ __device__ __forceinline__ int row_blocks(const SelectParams &p, int L, bool tel
 constexpr float kBadChunk = -1.f;
 constexpr float kLateChunk = -2.f;
 
+// Whether the wait on `bar` ended for all of the CTA's threads (`mine`: for
+// this one).  If it did not, thread 0 reports that and sees the copies off,
+// whoever gave up.  All threads call it.
+__device__ __forceinline__ bool cta_waited(bool mine, uint64_t *bar, uint32_t parity, uint32_t *status,
+                                           uint64_t limit_ns = kWaitLimitNs)
+{
+    if (__syncthreads_and(mine))
+        return true;
+    if (threadIdx.x == 0) {
+        report(status, PKV_DEV_TIMEOUT);
+        drain_wait(bar, parity, status, limit_ns);
+    }
+    return false;
+}
+
 // Shared memory of a scoring CTA of NW warps with rings of S tiles: the
 // weights [part][2 D] in the summaries' type -- three parts of -Q- (minima) and
 // Q+ (maxima), and a bound of their magnitude -- and the rings.
@@ -838,34 +853,34 @@ select_rows_kernel(const __grid_constant__ SelectParams p)
     const float scale = weight_scale<NT / 32>(big, sh->scan);
     if (tid < D)
         exact_weights<D>(sh->weight, x, scale);
-    if (n > p.num_selected) {
-        if (!mbar_wait_bounded(&sh->bar, 0)) {
-            if (tid == 0) {
-                report(p.status, PKV_DEV_TIMEOUT);
-                drain_wait(&sh->bar, 0, p.status);
-            }
-            n = 0;   // selects nothing
-        }
-        n = __syncthreads_and(n != 0) ? n : 0;
-    }
+    if (n > p.num_selected && !cta_waited(mbar_wait_bounded(&sh->bar, 0), &sh->bar, 0, p.status))
+        n = 0;   // selects nothing
     __syncthreads();
     select_row<T, D, NT>(p, sh, key, in, pend, p.ws_bound + row * p.bounds, seq, kvh, n);
 }
 
-// Test hook: what select_row makes of a scoring warp that gave up (what 1) or
-// met a bad id (2), on one CTA and a row of 100 blocks.
+// Test hook: what select_rows_kernel and select_row make of waits that gave
+// up, on one CTA and a row of 100 blocks.  what 0: the keys' copy never comes,
+// and thread 0 alone sees its wait end (on the barrier's other parity); 1: a
+// scoring warp gave up; 2: a scoring warp met a bad id.
 __global__ void __launch_bounds__(kSelectThreads)
-select_timeout_test_kernel(const __grid_constant__ SelectParams p, int what)
+select_timeout_test_kernel(const __grid_constant__ SelectParams p, int what, uint64_t limit_ns)
 {
     __shared__ SelectShared sh;
     __shared__ float bounds[2];
     if (threadIdx.x == 0) {
+        mbar_init(&sh.bar, 1);
+        fence_mbar_init();
         bounds[0] = 1.f;
-        bounds[1] = what == 1 ? kLateChunk : kBadChunk;
+        bounds[1] = what == 0 ? 1.f : what == 1 ? kLateChunk : kBadChunk;
     }
     __syncthreads();
-    // the row is refused: no key, bit or table is looked at
-    select_row<__half, 64, kSelectThreads>(p, &sh, nullptr, nullptr, nullptr, bounds, 0, 0, 100);
+    int n = 100;
+    if (what == 0 && !cta_waited(mbar_wait_bounded(&sh.bar, threadIdx.x == 0 ? 1 : 0, limit_ns), &sh.bar, 0, p.status, limit_ns))
+        n = 0;
+    __syncthreads();
+    // the row is refused or empty: no key, bit or table is looked at
+    select_row<__half, 64, kSelectThreads>(p, &sh, nullptr, nullptr, nullptr, bounds, 0, 0, n);
 }
 
 }  // namespace pkv
