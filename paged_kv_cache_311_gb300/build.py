@@ -88,10 +88,12 @@ def build(extra_flags=(), out_path: str | None = None, verbose_ptxas: bool = Fal
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         module = ex.submit(build_torch_module, os.path.join(os.path.dirname(out), "_pkv_torch.so"))
         objs = list(ex.map(compile_one, SOURCES))
-        module.result()
     tmp = f"{out}.{os.getpid()}.tmp"
     subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, out)
+    # the library needs nothing of torch's headers: it is there even where the
+    # module's compilation failed, which is reported now
+    module.result()
     return out
 
 
