@@ -124,9 +124,10 @@ int ensure_smem_attr(const void *func, int bytes, unsigned long long *done_mask)
     if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
         cudaSuccess)
         return PKV_ECUDA;
-    // every library kernel asks for the largest shared-memory carveout, so
-    // that consecutive launches of them never wait for an L1 / shared
-    // memory reconfiguration of the SMs
+    // the kernels that come here ask for the largest shared-memory carveout,
+    // so that consecutive launches of them never wait for an L1 / shared
+    // memory reconfiguration of the SMs.  (append_cache_q8 and
+    // summarize_blocks do not: their loads live on L1, see q8_cache.cu.)
     if (cudaFuncSetAttribute(func, cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared) != cudaSuccess)
         return PKV_ECUDA;
