@@ -515,10 +515,14 @@ int pkv_summarize_blocks(const void *k_cache, int cache_dtype, const float *k_sc
  * keep_last, and of the others those with the highest score
  *     sum over the kv head's query heads g, sum_d max(q_gd lo_d, q_gd hi_d),
  * an upper bound on the sum of the heads' largest q . k in the block (lo, hi:
- * the block's summary).  The selection is that of the exact scores, whatever
- * the rounding of intermediate sums; equal scores go to the lower block.  A
- * NaN or an infinity in a block's summary makes its score +infinity, one in a
- * head's q those of all blocks of its group.  (For a softmax scale > 0.)
+ * the block's summary; for lo <= hi).  Two blocks come out in the order of
+ * their exact scores if those differ by more than 2^-41 of the larger sum of
+ * its terms' magnitudes, sum_d |weight_d| (|lo_d| + |hi_d|); closer ones may
+ * come out either way, the same in every call.  (Where terms are smaller than
+ * about 2^-90, as far as fp32's subnormal numbers reach.)  Blocks with the
+ * same summary tie, and of them the lower one goes first.  A NaN or an
+ * infinity in a block's summary makes its score +infinity, one in a head's q
+ * those of all blocks of its group.  (For a softmax scale > 0.)
  *
  *   selected     int32 [num_seqs, num_kv_heads, num_selected] (written):
  *                logical block numbers in ascending order; all blocks, then

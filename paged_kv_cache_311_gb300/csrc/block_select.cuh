@@ -36,7 +36,9 @@
 // (see kScoreErr).  select_row finds the m-th largest score T; scores above
 // T + 2 eps are in, those below T - 2 eps are out, and only if what lies
 // between does not fit are those blocks (a few) scored again in pairs of fp32
-// numbers (48 bits) and selected by (score, then lowest block).
+// numbers and selected by (score, then lowest block).  Pairs hold 48 bits: some
+// 20 operations, each off by a few 2^-47 of its operands, leave a score
+// within 2^-42 of the sum of its terms' magnitudes.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -83,7 +85,10 @@ constexpr int kScoreTiles = 8;
 // (taken as) at one unit in its last place, 2^-23.  Eight chains of two steps
 // each: 2 x 17 x 2^-23 of what the chain adds up.  Joining the chains and the
 // three parts takes 5 roundings of 2^-24, the weights another 4 and the edges
-// T +- 2 eps two.  Together 40 x 2^-23; 44 are taken.
+// T +- 2 eps two.  Together 40 x 2^-23; 44 are taken.  How many bits the tensor
+// cores keep of a sum is not documented: one unit of 2^-23 per product is what
+// this rests on.  Measured on sums made to lose all that a cut can take: 8 x
+// 2^-23 of the terms at head_dim 128, 4 x 2^-23 at 64 (a cut at 2^-25).
 //
 // Three parts of a weight w leave out at most 2^-24 |w| in bfloat16 (one of
 // the four above).  In f16 they leave out 2^-33 |w|, but not less than half of
