@@ -491,7 +491,11 @@ size_t pkv_paged_attention_list_workspace_bytes(int num_seqs, int num_heads, int
  * smallest and the largest value over the rows the block holds now.  Called
  * after pkv_reshape_and_cache or pkv_append_cache_q8 with the same tables,
  * lengths and query_start; it reads the rows from the cache, so it may be
- * repeated, and a block copied with its summary stays right.
+ * repeated, and a block copied with its summary stays right.  To copy or swap
+ * blocks, pass the summaries to pkv_copy_blocks / pkv_swap_blocks too (block_bytes
+ * num_kv_heads * 2 * head_dim * element size; two layers' arrays in the places
+ * of K and V, or one in both): a block moved without its summary is selected
+ * by what its new place held.
  *
  *   k_cache      [num_blocks, num_kv_heads, block_size, head_dim] of
  *                cache_dtype: PKV_F16, PKV_BF16, or PKV_E4M3 with k_scales

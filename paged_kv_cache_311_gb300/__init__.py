@@ -1,10 +1,11 @@
 """paged_kv_cache_311_gb300 -- GB300-native paged KV-cache decode attention.
 
-A thin ctypes binding over ``libpkv.so`` (C ABI in ``include/pkv.h``).  Every
-step of the path runs in the library's CUDA kernels; this module only turns
-torch tensors into pointers, sizes and the current CUDA stream.  torch is
-used for device memory and streams, nothing else.  There is no CPU fallback:
-calling into the library without a built ``libpkv.so`` raises.
+A thin binding over ``libpkv.so`` (C ABI in ``include/pkv.h``): ctypes, and for
+the calls on 8-bit caches and selected blocks an extension module that checks
+tensors natively.  Every step of the path runs in the library's CUDA kernels;
+this package only turns torch tensors into pointers, sizes and CUDA streams.
+torch is used for device memory and streams, nothing else.  There is no CPU
+fallback: calling into the library without a built ``libpkv.so`` raises.
 
 Operations (PagedAttention: Efficient LLM Serving with vLLM, "The
 PagedAttention Algorithm" and "Advanced Features"):
