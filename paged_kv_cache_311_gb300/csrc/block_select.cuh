@@ -26,8 +26,8 @@
 //     and some none).
 //
 // What bounds it: 16 x 8 rows of 1024 to 2048 blocks (101 MB of summaries, 15 us
-// at the HBM's rate) take 30 us, some 23 for the scores -- what any read of
-// 100 MB takes in one launch -- and 7 for the second launch, whose code runs
+// at the HBM's rate) take 29.5 to 32 us, some 23 for the scores -- a plain load
+// kernel takes 21.5 for as much -- and 8 for the second launch, whose code runs
 // once.  4 x 8 rows of 128 to 512 blocks take 8 us, latencies throughout.
 //
 // Exactness.  Which blocks are selected is a set of whole numbers, so it must

@@ -33,9 +33,11 @@
 // has to fit a 16-bit range together with it.
 //
 // What bounds it: HBM.  Sixteen q8 contexts of 16K to 32K tokens (808 MB) take
-// 135 us, 6.0 TB/s or 89 % of a copy's rate (93 % while the SMs have work);
-// 64 of 128 to 2048 tokens with 32 kv heads 89 to 100 us (96 to 85 %); 128
-// blocks of 16 tokens of a 16-bit cache for 32 x 8 rows 44 us (91 %).  One
+// 134 to 139 us, 6.0 TB/s or 90 to 87 % of a copy's rate (93 % while the SMs have
+// work); 64 of 128 to 2048 tokens with 32 kv heads 91 to 102 us (94 to 84 %);
+// 128 blocks of 16 tokens of a 16-bit cache for 32 x 8 rows 43.5 us (93 %).  Over
+// the 8-bit cache those rows take 29 us (70 %): too few warps for the chain of
+// dependent instructions that each runs per tile.  One
 // request of 700 tokens takes 5.6 us, a launch and the latencies of length and
 // table, tile, products and merge.
 #pragma once
