@@ -461,7 +461,9 @@ int pkv_append_cache_q8(const void *key, const void *value, int dtype, void *k_c
  * head_dim 64 or 128; block_size 8, 16 or 32; num_heads / num_kv_heads 1 to 8;
  * num_seqs and num_kv_heads up to 65,535.  Device errors as for
  * pkv_paged_attention_decode: the rows they concern are zero.
- * Scores, softmax sums and accumulators are fp32.  The softmax weights enter
+ * Scores, softmax sums and accumulators are fp32.  A bfloat16 q is multiplied
+ * in f16, each head's scaled by a power of two: elements below 2^-28 of the
+ * head's largest are off by up to 2^-39 of it.  The softmax weights enter
  * the product with V in two 16-bit parts, whatever out_dtype is: each is off by
  * at most 2^-22 of itself and 2^-32 of the row's largest weight (2^-16 of
  * itself over a bfloat16 cache).
@@ -501,8 +503,9 @@ size_t pkv_paged_attention_list_workspace_bytes(int num_seqs, int num_heads, int
  *                cache_dtype: PKV_F16, PKV_BF16, or PKV_E4M3 with k_scales
  *                (NULL otherwise)
  *   summaries    [num_blocks, num_kv_heads, 2, head_dim] of summary_dtype:
- *                the cache's type, PKV_BF16 for an e4m3 cache; row 0 the
- *                minima, row 1 the maxima.  A NaN key makes both NaN.
+ *                the cache's type, PKV_BF16 for an e4m3 cache (which holds
+ *                its values down to 2^-133, and rounds smaller ones); row 0
+ *                the minima, row 1 the maxima.  A NaN key makes both NaN.
  *   num_tokens   host bound of query_start[num_seqs]
  * Other arguments, device errors and shapes as for pkv_append_cache_q8.
  */

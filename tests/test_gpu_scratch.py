@@ -63,3 +63,32 @@ def test_memory_that_another_stream_gave_back_is_not_used(raw):
         torch.cuda.synchronize()
         assert int(total) == nbytes, name
         assert torch.equal(got, want), name
+
+
+def test_the_default_stream_by_number_and_from_another_one():
+    """stream=0 while another stream is current."""
+    for name, call, like, nbytes in calls():
+        want, got = torch.zeros_like(like), torch.zeros_like(like)
+        call(want, None)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(torch.cuda.Stream()):
+            call(got, 0)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), name
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_captured_call_allocates_for_itself(raw):
+    """No workspace, the capturing stream named: the graph keeps its own."""
+    for name, call, like, nbytes in calls():
+        want, got = torch.zeros_like(like), torch.zeros_like(like)
+        call(want, None)
+        torch.cuda.synchronize()
+        graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=s):
+            call(got, s.cuda_stream if raw else s)
+        got.zero_()
+        block = torch.full((nbytes,), 255, dtype=torch.uint8, device=DEV)   # not what the graph writes into
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and bool((block == 255).all()), name

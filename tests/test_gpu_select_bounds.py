@@ -139,3 +139,33 @@ def test_scores_close_to_each_other(path, t):
     for K in (1, 7, 45, 50, 55, 90):
         got, want = select(q, sums, tables, np.array([n * bs], np.int32), bs, K, 0, 0)
         np.testing.assert_array_equal(got, want)
+
+
+@pytest.mark.parametrize("path", list(BLOCKS))
+@pytest.mark.parametrize("qt,st", [("f16", "bf16"), ("bf16", "f16")])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -14, 2.0 ** 13])
+def test_queries_and_summaries_of_different_types(path, qt, st, size):
+    """What an 8-bit cache (bfloat16 summaries) of an f16 model gives, and the other way round."""
+    n, bs, D = BLOCKS[path], 8, 64
+    rng = np.random.RandomState(n)
+    tables, NB = S.make_tables(rng, [n, n // 2])
+    sums = torch.from_numpy(np.sort(rng.randn(NB, 2, 2, D), axis=2)).to(S.DT[st])
+    q = torch.from_numpy(rng.randn(2, 10, D) * size).to(S.DT[qt])
+    for K in (3, 20):
+        got, want = select(q, sums, tables, np.array([n * bs, n // 2 * bs - 3], np.int32), bs, K, 1, 1)
+        np.testing.assert_array_equal(got, want)
+
+
+@pytest.mark.parametrize("alike", [False, True])
+def test_the_longest_contexts(alike):
+    """40,960 blocks, the most that a row may have; all alike: every one of them in doubt."""
+    n, bs, D = 40960, 8, 64
+    rng = np.random.RandomState(3)
+    tables, NB = S.make_tables(rng, [n, 100])
+    sums = torch.from_numpy(np.sort(rng.randn(NB, 1, 2, D), axis=2)).bfloat16()
+    if alike:
+        sums[:] = sums[0].clone()
+    q = torch.from_numpy(rng.randn(2, 4, D)).bfloat16()
+    for K in (1, 300, 40959):
+        got, want = select(q, sums, tables, np.array([n * bs, 100 * bs], np.int32), bs, K, 0, 1)
+        np.testing.assert_array_equal(got, want)
