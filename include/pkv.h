@@ -585,6 +585,105 @@ int pkv_paged_attention_decode_selected(void *out, int out_dtype, const void *q,
                                         void *stream);
 
 /*
+ * reshape_and_cache_q4 -- write each new token's key/value rows into its slot
+ * of a cache of 4-bit codes.  (The pages keep the cache in the model's type; at
+ * 4.5 bits a number decode attention reads little more than a quarter of it.)
+ *
+ * The cache.  k_cache, v_cache: [num_blocks, num_kv_heads, block_size *
+ * (D / 2 + D / 16)] bytes, D = head_dim; the bytes of one block and kv head are
+ * a record.  A group is the 64 neighbouring dimensions 64 j .. 64 j + 63 of a
+ * row (a token's D numbers of one kv head); it has a scale s and a minimum m
+ * of the cache's type, which is that of the rows it is written from, and 64
+ * codes u of 4 bits.  Its numbers are s u + m.
+ *   - Codes: row r is D / 8 little-endian words of 32 bits, word w at byte
+ *     a = r D / 2 + 4 w of the record before pieces are exchanged; word
+ *     (D / 64) i + j holds dimensions 64 j + 8 i + n, n = 0 .. 7, in bits 4 n ..
+ *     4 n + 3.  16-byte pieces are exchanged within lines of 128 bytes: what
+ *     would be at byte a is at a ^ 16 x, with x = (a / 128) % 8 for D = 128 and
+ *     x = {0, 4, 2, 6}[(a / 128) % 4] for D = 64.
+ *   - Pairs: (s, m) of row r, group j at byte block_size D / 2 + r D / 16 + 4 j.
+ * The call, for each group x of a row (fp32 arithmetic, halves to even):
+ *     m = min x,  s = (max x / 2 - m / 2) / 7.5, rounded to fp32 and to the type
+ *     (0 if below 2^-126),  u = min(15, round((x / 2 - m / 2) * (2 / s))), 0 for
+ *     s = 0; the product is taken to 16 binary places before it is rounded.
+ * A group with a NaN or an infinity stands for NaNs.  Rows of other slots keep
+ * their bytes.
+ *
+ *   key, value   num_tokens rows [num_kv_heads, head_dim] of dtype (PKV_F16 or
+ *                PKV_BF16; PKV_F32: PKV_EUNSUPPORTED), 16-byte aligned
+ *   key_stride, value_stride  elements from one token's rows to the next's: at
+ *                least num_kv_heads * head_dim, a multiple of 16 bytes (not
+ *                looked at for one token)
+ *   slot_mapping int64 [num_tokens], as for pkv_reshape_and_cache
+ * head_dim 64 or 128, block_size 8, 16 or 32, num_kv_heads up to 65,535.  Two
+ * tokens with the same slot in one call: undefined.  pkv_copy_blocks and
+ * pkv_swap_blocks move blocks as of any cache (block_bytes num_kv_heads *
+ * block_size * (D / 2 + D / 16)).
+ */
+int pkv_reshape_and_cache_q4(const void *key, int64_t key_stride, const void *value,
+                             int64_t value_stride, int dtype, void *k_cache, void *v_cache,
+                             const int64_t *slot_mapping, int num_tokens, int num_kv_heads,
+                             int head_dim, int block_size, int64_t num_blocks,
+                             uint32_t *device_status, void *stream);
+
+/*
+ * gather_cache_q4 -- the rows at the slots of slot_mapping as numbers: what the
+ * prefill of a prompt needs of a prefix that is cached (see
+ * pkv_block_pool_allocate_prompt).
+ *
+ *   key, value   num_tokens rows [num_kv_heads, head_dim] of out_dtype (written;
+ *                16-byte aligned; strides as above): dtype, or PKV_F32
+ *   dtype        the cache's type: what it was written from
+ * A number is s u + m, exact and then rounded once to out_dtype (infinite where
+ * that is past the type's largest number, which only groups that reach it can
+ * give).  A negative slot: its rows of key and value keep their bytes; a slot
+ * past the pool: the same, and PKV_DEV_BAD_SLOT.  Slots may repeat.  Shapes and
+ * errors as above.
+ */
+int pkv_gather_cache_q4(void *key, int64_t key_stride, void *value, int64_t value_stride,
+                        int out_dtype, const void *k_cache, const void *v_cache, int dtype,
+                        const int64_t *slot_mapping, int num_tokens, int num_kv_heads, int head_dim,
+                        int block_size, int64_t num_blocks, uint32_t *device_status, void *stream);
+
+/*
+ * paged_attention_decode_q4 -- pkv_paged_attention_decode over a cache that
+ * pkv_reshape_and_cache_q4 wrote:
+ *     out[s,h,:] = sum_i softmax_i(scale * q[s,h,:] . k_i) * v_i
+ * over the numbers that the cache stands for.  L = 0 gives a zero row.
+ *
+ *   q          num_seqs rows [num_heads, head_dim] of q_dtype (PKV_F16 or
+ *              PKV_BF16: the cache's type), 16-byte aligned
+ *   q_stride   elements from one sequence's rows to the next's: at least
+ *              num_heads * head_dim, a multiple of 8 (not looked at for one
+ *              sequence)
+ *   out        [num_seqs, num_heads, head_dim] of out_dtype (any), 16-byte aligned
+ *   max_context_len  host bound of context_lens (at most max_blocks_per_seq *
+ *              block_size)
+ *   partition_size  0 = automatic; else tokens per partition of the context,
+ *              a multiple of 32 and of block_size (512 blocks at most, unless
+ *              the whole context is shorter: PKV_EUNSUPPORTED)
+ *   workspace  at least pkv_paged_attention_q4_workspace_bytes(...) bytes,
+ *              16-byte aligned (may be NULL where that is 0)
+ * head_dim 64 or 128; block_size 8, 16 or 32; num_heads / num_kv_heads 1 to 8;
+ * num_seqs and num_kv_heads up to 65,535.  Device errors as for
+ * pkv_paged_attention_decode: the rows they concern are zero.
+ */
+int pkv_paged_attention_decode_q4(void *out, int out_dtype, const void *q, int64_t q_stride,
+                                  int q_dtype, const void *k_cache, const void *v_cache,
+                                  const int32_t *block_tables, int max_blocks_per_seq,
+                                  const int32_t *context_lens, int num_seqs, int num_heads,
+                                  int num_kv_heads, int head_dim, int block_size,
+                                  int64_t num_blocks, int max_context_len, float scale,
+                                  int partition_size, void *workspace, size_t workspace_bytes,
+                                  uint32_t *device_status, void *stream);
+
+/* Bytes of workspace of pkv_paged_attention_decode_q4 on the current device; 0
+ * if none is needed or on invalid sizes. */
+size_t pkv_paged_attention_q4_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads,
+                                              int head_dim, int block_size, int max_context_len,
+                                              int partition_size);
+
+/*
  * paged_attention_decode_static -- the same attention as
  * pkv_paged_attention_decode, for callers that cannot allocate device
  * memory.  (The pages have no counterpart; this is a convenience of this

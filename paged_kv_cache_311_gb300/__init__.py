@@ -1,7 +1,7 @@
 """paged_kv_cache_311_gb300 -- GB300-native paged KV-cache decode attention.
 
 A thin binding over ``libpkv.so`` (C ABI in ``include/pkv.h``): ctypes, and for
-the calls on 8-bit caches and selected blocks an extension module that checks
+the calls on 8-bit and 4-bit caches and selected blocks an extension module that checks
 tensors natively.  Every step of the path runs in the library's CUDA kernels;
 this package only turns torch tensors into pointers, sizes and CUDA streams.
 torch is used for device memory and streams, nothing else.  There is no CPU
@@ -12,12 +12,15 @@ PagedAttention Algorithm" and "Advanced Features"):
   paged_attention_decode  single-query attention over a block-table-mapped cache
   reshape_and_cache       scatter of new tokens' K/V into their slots
   copy_blocks             copy-on-write copy of shared blocks
-and, for caches that are held in 8 bits or read in part:
+and, for caches that are held in 8 or 4 bits or read in part:
   append_cache_q8                  new tokens' K/V into e4m3 blocks with scales
   paged_attention_decode_q8        attention over such a cache
   summarize_blocks                 the range of each block's keys
   select_blocks                    the blocks that bound says matter to a query
   paged_attention_decode_selected  attention over the selected blocks
+  reshape_and_cache_q4             new tokens' K/V into a cache of 4-bit codes
+  gather_cache_q4                  rows of such a cache back as numbers
+  paged_attention_decode_q4        attention over such a cache
 """
 from __future__ import annotations
 
@@ -40,7 +43,8 @@ __all__ = [
     "HEADER_PATH", "bounded_wait_hook", "select_timeout_hook",
     "append_cache_q8", "summarize_blocks", "select_blocks", "paged_attention_decode_q8",
     "paged_attention_decode_selected", "paged_attention_list_workspace_bytes", "q8_scales",
-    "select_blocks_workspace_bytes",
+    "select_blocks_workspace_bytes", "q4_cache", "reshape_and_cache_q4", "gather_cache_q4",
+    "paged_attention_decode_q4", "paged_attention_q4_workspace_bytes",
 ]
 
 HEADER_PATH = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
@@ -143,6 +147,15 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                                       vp, i32, i32, i32, i32, i32, i32, i64, i32, f32,
                                                       i32, vp, u64, vp, vp]
     L.pkv_paged_attention_decode_selected.restype = i32
+    L.pkv_reshape_and_cache_q4.argtypes = [vp, i64, vp, i64, i32, vp, vp, vp, i32, i32, i32, i32, i64, vp, vp]
+    L.pkv_reshape_and_cache_q4.restype = i32
+    L.pkv_gather_cache_q4.argtypes = [vp, i64, vp, i64, i32, vp, vp, i32, vp, i32, i32, i32, i32, i64, vp, vp]
+    L.pkv_gather_cache_q4.restype = i32
+    L.pkv_paged_attention_decode_q4.argtypes = [vp, i32, vp, i64, i32, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32,
+                                                i64, i32, f32, i32, vp, u64, vp, vp]
+    L.pkv_paged_attention_decode_q4.restype = i32
+    L.pkv_paged_attention_q4_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+    L.pkv_paged_attention_q4_workspace_bytes.restype = u64
     L.pkv_status_string.argtypes = [i32]
     L.pkv_status_string.restype = ctypes.c_char_p
     L.pkv_last_decode_launches.argtypes = []
@@ -609,7 +622,8 @@ def q8_scales(num_blocks: int, num_kv_heads: int, device=None) -> torch.Tensor:
 # The functions that the extension module calls, in its order.
 _BOUND = ("pkv_append_cache_q8", "pkv_summarize_blocks", "pkv_select_blocks", "pkv_select_blocks_workspace_bytes",
           "pkv_paged_attention_decode_q8", "pkv_paged_attention_decode_selected",
-          "pkv_paged_attention_list_workspace_bytes")
+          "pkv_paged_attention_list_workspace_bytes", "pkv_reshape_and_cache_q4", "pkv_gather_cache_q4",
+          "pkv_paged_attention_decode_q4", "pkv_paged_attention_q4_workspace_bytes")
 _module = None
 
 
@@ -751,4 +765,80 @@ def paged_attention_decode_selected(out: torch.Tensor, q: torch.Tensor, k_cache:
                             None, partition_size, _scratch(rc, q, stream), device_status, stream)
     if rc:
         raise PkvError(rc, "pkv_paged_attention_decode_selected")
+    return out
+
+
+# ------------------------------------------------------- caches held in 4 bits
+
+
+def q4_cache(num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int, device=None) -> torch.Tensor:
+    """A zeroed 4-bit K or V cache: uint8 [num_blocks, num_kv_heads, block_size,
+    head_dim / 2 + head_dim / 16].  A block's bytes of one kv head are one record
+    (codes of its rows, then their scales and minima); copy_blocks and
+    swap_blocks move a block like any other."""
+    if head_dim % 64:
+        raise ValueError("head_dim must be a multiple of 64")
+    return torch.zeros(num_blocks, num_kv_heads, block_size, head_dim // 2 + head_dim // 16, dtype=torch.uint8,
+                       device=device)
+
+
+def reshape_and_cache_q4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         slot_mapping: torch.Tensor, *, device_status: Optional[torch.Tensor] = None,
+                         stream=None) -> None:
+    """As reshape_and_cache, into a 4-bit cache: token t's rows go to slot
+    slot_mapping[t] (int64; negative: padding), each group of 64 dimensions with
+    a scale and a minimum of its own (see pkv_reshape_and_cache_q4).
+
+    key, value: [T, Hk, D] of float16 or bfloat16, which is the cache's type from
+    then on; their first dimension may have any stride (a slice of a fused
+    projection's output).  k_cache, v_cache: as q4_cache makes them."""
+    rc = (_module or _native()).write_q4(key, value, k_cache, v_cache, slot_mapping, device_status, stream)
+    if rc:
+        raise PkvError(rc, "pkv_reshape_and_cache_q4")
+
+
+def gather_cache_q4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    slot_mapping: torch.Tensor, *, dtype: Optional[torch.dtype] = None,
+                    device_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """key[t], value[t] = the numbers that the rows at slot slot_mapping[t] of a
+    4-bit cache stand for (a negative slot leaves its rows as they are): what a
+    prompt's prefill needs of a prefix that is cached.
+
+    key, value: [T, Hk, D], written; their first dimension may have any stride
+    that keeps rows apart.  Of the cache's type (what it was written from), or
+    float32 with dtype naming that type."""
+    if dtype is not None and dtype not in _DTYPE:
+        raise ValueError("dtype must be float16 or bfloat16")
+    rc = (_module or _native()).gather_q4(key, value, k_cache, v_cache, slot_mapping, None if dtype is None else _DTYPE[dtype],
+                                          device_status, stream)
+    if rc:
+        raise PkvError(rc, "pkv_gather_cache_q4")
+
+
+def paged_attention_q4_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
+                                       max_context_len: int, partition_size: int = 0) -> int:
+    """Workspace bytes of paged_attention_decode_q4 on the current device (0: none)."""
+    return int(load_library().pkv_paged_attention_q4_workspace_bytes(
+        num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len, partition_size))
+
+
+def paged_attention_decode_q4(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                              block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float, *,
+                              max_context_len: Optional[int] = None, partition_size: int = 0,
+                              workspace: Optional[torch.Tensor] = None,
+                              device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """As paged_attention_decode, over a 4-bit cache that reshape_and_cache_q4 wrote.
+
+    q: [B, H, D] of the cache's type (float16 or bfloat16: what it was written
+    from); its first dimension may have any stride.  out: [B, H, D], any floating
+    dtype.  max_context_len: host bound of context_lens (what the table can hold
+    if omitted).  workspace: paged_attention_q4_workspace_bytes, allocated here if
+    needed and not given."""
+    rc = (_module or _native()).decode_q4(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,
+                                          partition_size, workspace, device_status, stream)
+    if rc > 0:
+        rc = _module.decode_q4(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,
+                               partition_size, _scratch(rc, q, stream), device_status, stream)
+    if rc:
+        raise PkvError(rc, "pkv_paged_attention_decode_q4")
     return out

@@ -1,6 +1,6 @@
-// pkv_torch.cpp -- the Python side of the 8-bit cache's and the block
-// selection's calls: takes torch tensors, checks them, calls the C functions of
-// libpkv.so.  A decode step makes these calls once per layer; checked and
+// pkv_torch.cpp -- the Python side of the 8-bit and 4-bit caches' and the
+// block selection's calls: takes torch tensors, checks them, calls the C
+// functions of libpkv.so.  A decode step makes these calls once per layer; checked and
 // converted in Python they cost 6 us each, more than most of their kernels.
 //
 // The module does not link to libpkv.so: bind() receives the addresses of the
@@ -21,7 +21,10 @@
 namespace {
 
 // The bound functions, in the order of the names that the package passes.
-enum { kAppend, kSummarize, kSelect, kSelectBytes, kDecodeQ8, kDecodeSelected, kListBytes, kFunctions };
+enum {
+    kAppend, kSummarize, kSelect, kSelectBytes, kDecodeQ8, kDecodeSelected, kListBytes,
+    kWriteQ4, kGatherQ4, kDecodeQ4, kQ4Bytes, kFunctions
+};
 void *g_function[kFunctions];
 
 using T = const at::Tensor *;
@@ -44,7 +47,8 @@ struct Call {
     }
 
     // Tensor argument i: contiguous, on the CUDA device of the first one.
-    T tensor(int i, const char *name, bool optional = false)
+    // `rows`: of three dimensions, of which the first may have any stride.
+    T tensor(int i, const char *name, bool optional = false, bool rows = false)
     {
         PyObject *o = args[i];
         if (!ok || (optional && o == Py_None))
@@ -55,8 +59,12 @@ struct Call {
             return nullptr;
         }
         T t = &THPVariable_Unpack(o);
-        if (!t->is_cuda() || !t->is_contiguous()) {
-            PyErr_Format(PyExc_ValueError, "%s must be a contiguous CUDA tensor", name);
+        const bool laid_out = !rows ? t->is_contiguous()
+                              : t->dim() == 3 && (t->numel() == 0 || ((t->size(2) == 1 || t->stride(2) == 1) &&
+                                                                      (t->size(1) == 1 || t->stride(1) == t->size(2))));
+        if (!t->is_cuda() || !laid_out) {
+            PyErr_Format(PyExc_ValueError, rows ? "%s must be a CUDA tensor of three dimensions, contiguous but for the first"
+                                                : "%s must be a contiguous CUDA tensor", name);
             ok = false;
             return nullptr;
         }
@@ -178,6 +186,9 @@ bool floating(T t) { return dtype(t) >= 0 && dtype(t) != PKV_E4M3; }
 
 void *address(T t) { return t ? t->data_ptr() : nullptr; }
 template <typename P> P *as(T t) { return static_cast<P *>(address(t)); }
+
+// Elements from one row [H, D] of t to the next.
+int64_t row_stride(T t) { return t->size(0) > 1 ? t->stride(0) : t->size(1) * t->size(2); }
 
 // Makes the tensors' device current while a call runs.
 struct Device {
@@ -437,12 +448,138 @@ PyObject *decode(PyObject *, PyObject *const *args, Py_ssize_t nargs)
     });
 }
 
+// What the 4-bit cache's calls ask of their caches: uint8 [NB, Hk, bs, D / 2 + D / 16].
+void q4_caches(Call &c, T k, T v, int64_t Hk, int64_t D)
+{
+    if (!c.ok)
+        return;
+    if (k->scalar_type() != at::kByte || v->scalar_type() != at::kByte)
+        c.value_error("k_cache and v_cache must be uint8");
+    else if (k->dim() != 4 || v->sizes() != k->sizes() || k->size(1) != Hk || D % 16 || k->size(3) != D / 2 + D / 16)
+        c.value_error("k_cache and v_cache must be [NB, Hk, bs, D / 2 + D / 16]");
+}
+
+void slots(Call &c, T mapping, int64_t tokens)
+{
+    if (c.ok && (mapping->scalar_type() != at::kLong || mapping->dim() != 1 || mapping->size(0) != tokens))
+        c.value_error("slot_mapping must be int64 [T]");
+}
+
+// write_q4(key, value, k_cache, v_cache, slot_mapping, device_status, stream)
+PyObject *write_q4(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    if (!arguments(nargs, 7))
+        return nullptr;
+    return guarded([&]() -> PyObject * {
+        Call c(args);
+        T key = c.tensor(0, "key", false, true), value = c.tensor(1, "value", false, true);
+        T k = c.tensor(2, "k_cache"), v = c.tensor(3, "v_cache"), at = c.tensor(4, "slot_mapping");
+        uint32_t *status = c.status(5);
+        if (!c.ok)
+            return nullptr;
+        const int64_t tokens = key->size(0), Hk = key->size(1), D = key->size(2);
+        if (value->sizes() != key->sizes())
+            c.value_error("shape mismatch");
+        else if (!floating(key) || value->scalar_type() != key->scalar_type())
+            c.value_error("key and value must share a floating dtype");
+        q4_caches(c, k, v, Hk, D);
+        slots(c, at, tokens);
+        void *stream = c.stream(6);
+        const int n[3] = {c.narrow(tokens), c.narrow(Hk), c.narrow(D)};
+        const int bs = c.ok ? c.narrow(k->size(2)) : 0;
+        if (!c.ok)
+            return nullptr;
+        const Device device(c.index);
+        return PyLong_FromLong(reinterpret_cast<decltype(&pkv_reshape_and_cache_q4)>(g_function[kWriteQ4])(
+            address(key), row_stride(key), address(value), row_stride(value), dtype(key), address(k), address(v), as<int64_t>(at), n[0],
+            n[1], n[2], bs, k->size(0), status, stream));
+    });
+}
+
+// gather_q4(key, value, k_cache, v_cache, slot_mapping, cache's pkv_dtype or
+//           None: key's, device_status, stream)
+PyObject *gather_q4(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    if (!arguments(nargs, 8))
+        return nullptr;
+    return guarded([&]() -> PyObject * {
+        Call c(args);
+        T key = c.tensor(0, "key", false, true), value = c.tensor(1, "value", false, true);
+        T k = c.tensor(2, "k_cache"), v = c.tensor(3, "v_cache"), at = c.tensor(4, "slot_mapping");
+        uint32_t *status = c.status(6);
+        if (!c.ok)
+            return nullptr;
+        const int64_t tokens = key->size(0), Hk = key->size(1), D = key->size(2);
+        if (value->sizes() != key->sizes())
+            c.value_error("shape mismatch");
+        else if (!floating(key) || value->scalar_type() != key->scalar_type())
+            c.value_error("key and value must share a floating dtype");
+        q4_caches(c, k, v, Hk, D);
+        slots(c, at, tokens);
+        const int kind = !c.ok ? 0 : args[5] == Py_None ? dtype(key) : c.narrow(c.integer(5));
+        void *stream = c.stream(7);
+        const int n[3] = {c.narrow(tokens), c.narrow(Hk), c.narrow(D)};
+        const int bs = c.ok ? c.narrow(k->size(2)) : 0;
+        if (!c.ok)
+            return nullptr;
+        const Device device(c.index);
+        return PyLong_FromLong(reinterpret_cast<decltype(&pkv_gather_cache_q4)>(g_function[kGatherQ4])(
+            address(key), row_stride(key), address(value), row_stride(value), dtype(key), address(k), address(v), kind,
+            as<int64_t>(at), n[0], n[1], n[2], bs, k->size(0), status, stream));
+    });
+}
+
+// decode_q4(out, q, k_cache, v_cache, block_tables, context_lens, scale,
+//           max_context_len or None, partition_size, workspace, device_status,
+//           stream)
+PyObject *decode_q4(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    if (!arguments(nargs, 12))
+        return nullptr;
+    return guarded([&]() -> PyObject * {
+        Call c(args);
+        T out = c.tensor(0, "out"), q = c.tensor(1, "q", false, true), k = c.tensor(2, "k_cache"), v = c.tensor(3, "v_cache");
+        T bt = c.tensor(4, "block_tables"), cl = c.tensor(5, "context_lens");
+        const double scale = c.real(6);
+        const int64_t partition = c.integer(8);
+        Workspace ws(c, 9);
+        uint32_t *status = c.status(10);
+        if (!c.ok || !c.dims(k, 4, "shape mismatch"))
+            return nullptr;
+        const int64_t B = q->size(0), H = q->size(1), D = q->size(2), NB = k->size(0), Hk = k->size(1), bs = k->size(2);
+        if (out->sizes() != q->sizes())
+            c.value_error("shape mismatch");
+        else if (!floating(out) || !floating(q))
+            c.value_error("q and out must be floating");
+        q4_caches(c, k, v, Hk, D);
+        const int MB = c.tables(bt, cl, B);
+        const int64_t most = args[7] == Py_None ? (int64_t)MB * c.narrow(bs) : c.integer(7);
+        void *stream = c.stream(11);
+        const int n[7] = {c.narrow(B), c.narrow(H), c.narrow(Hk), c.narrow(D), c.narrow(bs), c.narrow(most), c.narrow(partition)};
+        if (!c.ok)
+            return nullptr;
+        const Device device(c.index);
+        if (!ws.given) {
+            const size_t need = reinterpret_cast<decltype(&pkv_paged_attention_q4_workspace_bytes)>(g_function[kQ4Bytes])(
+                n[0], n[1], n[2], n[3], n[4], n[5], n[6]);
+            if (need)
+                return PyLong_FromSize_t(need);
+        }
+        return PyLong_FromLong(reinterpret_cast<decltype(&pkv_paged_attention_decode_q4)>(g_function[kDecodeQ4])(
+            address(out), dtype(out), address(q), row_stride(q), dtype(q), address(k), address(v), as<int32_t>(bt), MB,
+            as<int32_t>(cl), n[0], n[1], n[2], n[3], n[4], NB, n[5], (float)scale, n[6], ws.at, ws.bytes, status, stream));
+    });
+}
+
 PyMethodDef g_methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append)), METH_FASTCALL, nullptr},
     {"summarize", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(summarize)), METH_FASTCALL, nullptr},
     {"select", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(select)), METH_FASTCALL, nullptr},
     {"decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode)), METH_FASTCALL, nullptr},
+    {"write_q4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(write_q4)), METH_FASTCALL, nullptr},
+    {"gather_q4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gather_q4)), METH_FASTCALL, nullptr},
+    {"decode_q4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode_q4)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_pkv_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
