@@ -375,16 +375,6 @@ struct alignas(16) ScoreShared {
     uint32_t big[NW];
 };
 
-// Untiled bulk copy global -> shared with mbarrier byte accounting; addresses
-// and size in multiples of 16 bytes.
-__device__ __forceinline__ void bulk_load(void *dst_smem, const void *src, uint32_t bytes, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst_smem)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
 // Keys of blocks [b0, b0 + p.chunk) of row (seq, kvh) into keys[0 ..], by a CTA
 // of NW warps.  Returns each warp's S (in units of the weights' scale), or
 // kBadChunk or kLateChunk; nothing is scored in a row that is selected whole.  n receives the row's

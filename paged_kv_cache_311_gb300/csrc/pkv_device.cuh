@@ -142,6 +142,16 @@ __device__ __forceinline__ void tma_load_5d(void *dst_smem, const CUtensorMap *m
         : "memory");
 }
 
+// Untiled bulk copy global -> shared with mbarrier byte accounting; addresses
+// and size in multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(void *dst_smem, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst_smem)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
 // 4-byte asynchronous copy global -> shared (no register staging); complete
 // the thread's copies with cp_async_wait_all before reading them.
 __device__ __forceinline__ void cp_async4(void *dst_smem, const void *src)

@@ -4,34 +4,54 @@
 
 #include <cmath>
 
-#include "pkv_host.cuh"
+#include "list_host.cuh"
 #include "q4_attention.cuh"
 
 namespace pkv {
 namespace {
 
-bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
 template <typename T, int D, int BS>
-int run_q4(const Q4Params &p, int num_seqs, cudaStream_t stream)
+int run_q4(const Q4Params &p, cudaStream_t stream)
 {
-    return launch_pdl(q4_attention_kernel<T, D, BS>, dim3(p.num_kv_heads, num_seqs), dim3(kQ4Warps * 32), 0, stream, p);
+    using C = Q4Cfg<D, BS>;
+    static unsigned long long done = 0;
+    auto kern = q4_attention_kernel<T, D, BS>;
+    const int rc = ensure_smem_attr(reinterpret_cast<const void *>(kern), C::SMEM_BYTES, &done);
+    if (rc)
+        return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.list.np, (unsigned)p.list.num_kv_heads, (unsigned)p.list.num_seqs);
+    cfg.blockDim = dim3(kListThreads);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.list.np;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.list.cluster ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess)
+        return PKV_ECUDA;
+    return p.list.np > 1 && !p.list.cluster ? launch_list_merge<D>(p.list, stream) : PKV_OK;
 }
 
 template <typename T, int D>
-int run_q4_block(const Q4Params &p, int num_seqs, int bs, cudaStream_t s)
+int run_q4_block(const Q4Params &p, int bs, cudaStream_t s)
 {
     switch (bs) {
-    case 8: return run_q4<T, D, 8>(p, num_seqs, s);
-    case 16: return run_q4<T, D, 16>(p, num_seqs, s);
-    default: return run_q4<T, D, 32>(p, num_seqs, s);
+    case 8: return run_q4<T, D, 8>(p, s);
+    case 16: return run_q4<T, D, 16>(p, s);
+    default: return run_q4<T, D, 32>(p, s);
     }
 }
 
 template <typename T>
-int run_q4_type(const Q4Params &p, int num_seqs, int head_dim, int bs, cudaStream_t s)
+int run_q4_type(const Q4Params &p, int head_dim, int bs, cudaStream_t s)
 {
-    return head_dim == 64 ? run_q4_block<T, 64>(p, num_seqs, bs, s) : run_q4_block<T, 128>(p, num_seqs, bs, s);
+    return head_dim == 64 ? run_q4_block<T, 64>(p, bs, s) : run_q4_block<T, 128>(p, bs, s);
 }
 
 }  // namespace
@@ -41,7 +61,19 @@ using namespace pkv;
 
 extern "C" {
 
-size_t pkv_paged_attention_q4_workspace_bytes(int, int, int, int, int, int, int) { return 0; }
+size_t pkv_paged_attention_q4_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                              int max_context_len, int partition_size)
+{
+    if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || block_size > 32 ||
+        max_context_len <= 0 || partition_size < 0 || partition_size % block_size)
+        return 0;
+    const ListCut cut = list_cut((long long)num_seqs * num_kv_heads, ((long long)max_context_len + block_size - 1) / block_size,
+                                 block_size, partition_size);
+    if (cut.np <= 1 || cut.cluster)
+        return 0;
+    ListLayout lay;
+    return list_layout(num_seqs, num_heads, cut.np, head_dim, &lay) ? lay.total : 0;
+}
 
 int pkv_paged_attention_decode_q4(void *out, int out_dtype, const void *q, int64_t q_stride, int q_dtype,
                                   const void *k_cache, const void *v_cache, const int32_t *block_tables,
@@ -50,8 +82,6 @@ int pkv_paged_attention_decode_q4(void *out, int out_dtype, const void *q, int64
                                   int max_context_len, float scale, int partition_size, void *workspace,
                                   size_t workspace_bytes, uint32_t *device_status, void *stream)
 {
-    (void)workspace;
-    (void)workspace_bytes;
     if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_dim <= 0 ||
         num_blocks <= 0 || num_blocks > INT32_MAX || max_blocks_per_seq <= 0 || block_size <= 0 ||
         max_context_len < 0 || partition_size < 0 || !std::isfinite(scale) ||
@@ -75,25 +105,45 @@ int pkv_paged_attention_decode_q4(void *out, int out_dtype, const void *q, int64
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
         !aligned(block_tables, 4) || !aligned(context_lens, 4))
         return PKV_EINVAL;
-    Q4Params p;
-    p.out = out;
-    p.q = q;
-    p.k_cache = static_cast<const uint8_t *>(k_cache);
-    p.v_cache = static_cast<const uint8_t *>(v_cache);
-    p.block_tables = block_tables;
-    p.context_lens = context_lens;
-    p.status = device_status;
-    p.num_blocks = num_blocks;
+
+    const long long blocks = max_context_len > 0 ? ((long long)max_context_len + block_size - 1) / block_size : 1;
+    const ListCut cut = list_cut((long long)num_seqs * num_kv_heads, blocks, block_size, partition_size);
+    if (cut.part > kListCap && blocks > kListCap)
+        return PKV_EUNSUPPORTED;
+    Q4Params p = {};
+    ListParams &l = p.list;
+    if (cut.np > 1 && !cut.cluster) {
+        ListLayout lay;
+        if (!list_layout(num_seqs, num_heads, cut.np, head_dim, &lay))
+            return PKV_EUNSUPPORTED;
+        if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 16))
+            return PKV_EWORKSPACE;
+        l.ws_ml = static_cast<float *>(workspace);
+        l.ws_acc = reinterpret_cast<float *>(static_cast<char *>(workspace) + lay.acc_off);
+    }
+    l.out = out;
+    l.q = q;
+    l.k_cache = static_cast<const uint8_t *>(k_cache);
+    l.v_cache = static_cast<const uint8_t *>(v_cache);
+    l.block_tables = block_tables;
+    l.context_lens = context_lens;
+    l.status = device_status;
+    l.num_blocks = num_blocks;
+    l.num_seqs = num_seqs;
+    l.num_kv_heads = num_kv_heads;
+    l.group = num_heads / num_kv_heads;
+    l.max_blocks_per_seq = max_blocks_per_seq;
+    l.max_context_len = max_context_len;
+    l.part_blocks = cut.part;
+    l.np = cut.np;
+    l.cluster = cut.cluster;
+    l.out_dtype = out_dtype;
+    l.q_dtype = q_dtype;
+    l.qscale = scale * 1.4426950408889634f;
     p.q_stride = q_stride;
-    p.num_kv_heads = num_kv_heads;
-    p.group = num_heads / num_kv_heads;
-    p.max_blocks_per_seq = max_blocks_per_seq;
-    p.max_context_len = max_context_len;
-    p.out_dtype = out_dtype;
-    p.qscale = scale * 1.4426950408889634f;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return q_dtype == PKV_F16 ? run_q4_type<__half>(p, num_seqs, head_dim, block_size, s)
-                              : run_q4_type<__nv_bfloat16>(p, num_seqs, head_dim, block_size, s);
+    return q_dtype == PKV_F16 ? run_q4_type<__half>(p, head_dim, block_size, s)
+                              : run_q4_type<__nv_bfloat16>(p, head_dim, block_size, s);
 }
 
 }  // extern "C"

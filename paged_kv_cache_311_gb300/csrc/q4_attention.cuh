@@ -1,7 +1,32 @@
 // q4_attention.cuh -- single-query attention over a 4-bit cache
 // (paged_attention_decode_q4):
 //   out[s, h] = sum_t softmax_t(scale * q[s, h] . k_t) * v_t,
-// a row's numbers s u + m for each group of 64 dimensions (see q4_cache.cuh).
+// a row's numbers s u + m for each group j of 64 dimensions (see q4_cache.cuh):
+//   q . k_t   = sum_j s_tj (q_j . u_tj) + m_tj sum(q_j)
+//   sum_t w_t v_t = sum_t (w_t s_tj) (u_tj - 8) + sum_t w_t (m_tj + 8 s_tj)
+// so that the products take whole numbers, and scales and minima join them in
+// fp32.
+//
+// The frame is that of list_attention.cuh: one CTA per (partition of the
+// context, kv head, sequence) with the kv head's G <= 8 query heads, partitions
+// merged by a cluster or through the workspace.  Each of four warps streams
+// records (bulk copies, one per block, codes with their scales) through a ring
+// of its own and takes them in tiles of 16 tokens: the tile's tokens are M of
+// S^T = K q^T, its dimensions M of O^T += V^T W^T, the query heads N of
+// warp-level MMAs (m16n8k16).
+//
+// Codes become matrix fragments without a conversion: a word's nibbles masked
+// in place are 16-bit numbers, two at a time.
+//   K: f16.  u in a half's lowest bits is the subnormal u 2^-24, in the next
+//      four u 2^-20: a mask is all it takes (five instructions for eight codes).
+//      The factors go into q (a sixteenth for the latter) and the scores.
+//   V: tokens are the products' inner axis, so two tokens' words are first
+//      paired half by half.  bfloat16: u in a mantissa's lowest bits is 128 + u;
+//      136 is subtracted, exactly.  The weights w_t s_tj can have any size,
+//      which f16 cannot hold; bfloat16 can, in two parts of together 16 bits.
+// The M axes' order is free: row 2 c + e + 8 f of a tile is its token
+// 4 c + 2 f + e (so that a thread's four tokens of V are neighbours), and a
+// thread's rows of V^T are the dimensions that its words hold.
 #pragma once
 
 #include "list_attention.cuh"
@@ -10,111 +35,485 @@
 namespace pkv {
 
 struct Q4Params {
-    void *out;
-    const void *q;
-    const uint8_t *k_cache;
-    const uint8_t *v_cache;
-    const int32_t *block_tables;
-    const int32_t *context_lens;
-    uint32_t *status;
-    int64_t num_blocks, q_stride;
-    int num_kv_heads, group, max_blocks_per_seq, max_context_len, out_dtype;
-    float qscale;                // softmax scale * log2(e)
+    ListParams list;             // without selected blocks and scales
+    int64_t q_stride;            // elements between two sequences' rows of q
 };
 
-constexpr int kQ4Warps = 4;
+constexpr int kQ4Ring = 49152;   // ring bytes of a CTA
+constexpr int kQ4Ctas = 4;       // CTAs per SM
 
-// One CTA per (kv head, sequence), a warp per token, D / 32 dimensions a lane.
-template <typename T, int D, int BS>
-__global__ void __launch_bounds__(kQ4Warps * 32)
-q4_attention_kernel(const __grid_constant__ Q4Params p)
-{
+template <int D, int BS> struct Q4Cfg {
     using R = Q4Row<D>;
-    constexpr int N = D / 32, GM = kListMaxGroup;
-    __shared__ float s_m[kQ4Warps][GM], s_l[kQ4Warps][GM], s_o[kQ4Warps][GM][D];
-    const int kvh = blockIdx.x, seq = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int d0 = lane * N, j = d0 / kQ4Group, i = d0 % kQ4Group / 8, shift = d0 % 8 * 4;
-    wait_for_stream();
-    const int L = p.context_lens[seq];
-    const int32_t *table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
-    bool bad = L < 0 || L > p.max_context_len;
-    if (bad) {
-        if (threadIdx.x == 0)
-            report(p.status, PKV_DEV_BAD_CONTEXT_LEN);
-    } else {
-        int wrong = 0;
-        for (int k = threadIdx.x; k < (L + BS - 1) / BS; k += kQ4Warps * 32)
-            wrong |= table[k] < 0 || table[k] >= p.num_blocks;
-        bad = __syncthreads_or(wrong);
-        if (bad && threadIdx.x == 0)
-            report(p.status, PKV_DEV_BAD_BLOCK);
-    }
-    float q[GM][N], o[GM][N], m[GM], l[GM];
+    static constexpr int TILE = 16;
+    static constexpr int REC = R::template record<BS>;
+    static constexpr int TOK = BS < TILE ? TILE : BS;          // tokens of a stage
+    static constexpr int RECS = TOK / BS;
+    static constexpr int STAGE_BYTES = 2 * RECS * REC;
+    static constexpr int S0 = kQ4Ring / (kListWarps * STAGE_BYTES);
+    static constexpr int S = S0 < 2 ? 2 : S0;
+    static constexpr int AWS = D + 4;                          // row stride of the merge scratch, in floats
+
+    static constexpr int RING = (kListWarps * S * STAGE_BYTES + 127) / 128 * 128;
+    // the warps' results and the CTA's, in the rings' memory once they are done with
+    static constexpr int OFF_RESULT = kListWarps * kListMaxGroup * (AWS + 2) * 4;
+    static constexpr int RESULT_END = OFF_RESULT + kListMaxGroup * (D + 2) * 4;
+    static constexpr int OFF_PHYS = RING > RESULT_END ? RING : RESULT_END;
+    static constexpr int OFF_BAR = OFF_PHYS + kListCap * 4;
+    static constexpr int OFF_FLAG = OFF_BAR + kListWarps * S * 8;
+    static constexpr int SMEM_BYTES = OFF_FLAG + 32 + 1024;    // slack for the alignment to 1024
+    static_assert(REC % 16 == 0 && OFF_RESULT % 16 == 0 && OFF_PHYS % 16 == 0, "alignment");
+};
+
+// One warp's state.  Lane (g, c) = (lane / 4, lane % 4).
+template <typename T, int D, int BS> struct Q4Engine {
+    using C = Q4Cfg<D, BS>;
+    using R = Q4Row<D>;
+    static constexpr int NG = R::GROUPS;
+
+    uint32_t qf[NG][4][2];   // q^T B-fragments of head g: group, step
+    float fs[2];             // heads 2c, 2c + 1: score of s (q . u)
+    float fm[NG][2];         //                   score of m
+    float o[NG][4][4];       // O^T C-fragments: group, m-tile
+    float om[NG][2];         // this lane's tokens' sums of w (m + 8 s)
+    float m[2], lsum[2];     // heads 2c, 2c + 1
+    int kcode[2], kpair[2];  // byte offsets of this lane's tokens of K in a stage's records
+    int vcode[4];            // and of V
+    int g, c;
+
+    // Offset of the record of tile row t in a stage, and the row in it.
+    __device__ __forceinline__ static int rec_of(int t) { return BS < C::TILE ? t / BS * C::REC : 0; }
+
+    __device__ __forceinline__ void init(const Q4Params &a, int seq, int kvh, int lane)
+    {
+        const ListParams &p = a.list;
+        g = lane >> 2;
+        c = lane & 3;
 #pragma unroll
-    for (int g = 0; g < GM; ++g) {
-        m[g] = -INFINITY;
-        l[g] = 0.f;
+        for (int i = 0; i < 2; ++i) {
+            const int t = 4 * (g >> 1) + (g & 1) + 2 * i;
+            kcode[i] = rec_of(t) + R::word(t % BS, NG * 2 * c);
+            kpair[i] = rec_of(t) + R::template pair<BS>(t % BS, 0);
+        }
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            o[g][n] = 0.f;
-            q[g][n] = g < p.group ? to_float(static_cast<const T *>(p.q)[(int64_t)seq * p.q_stride + (kvh * p.group + g) * D + d0 + n]) * p.qscale : 0.f;
+        for (int i = 0; i < 4; ++i) {
+            const int t = 4 * c + i;
+            vcode[i] = rec_of(t) + R::word(t % BS, NG * g);
+        }
+        // q: dimensions 64 j + 16 c .. + 15 of head g, brought to f16 by a
+        // power of two that puts the head's largest magnitude in [2^14, 2^15):
+        // what f16 cannot hold is below 2^-35 of it
+        const bool live = g < p.group;
+        const T *qp = static_cast<const T *>(p.q) + (int64_t)seq * a.q_stride + (kvh * p.group + (live ? g : 0)) * D + 16 * c;
+        uint32_t w[NG][8];
+        float big = 0.f;
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4 v = live ? reinterpret_cast<const uint4 *>(qp + 64 * j)[i] : make_uint4(0, 0, 0, 0);
+                w[j][4 * i] = v.x;
+                w[j][4 * i + 1] = v.y;
+                w[j][4 * i + 2] = v.z;
+                w[j][4 * i + 3] = v.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 f = Unpack<T>::pair(w[j][i] & 0x7fff7fffu);
+                big = fmaxf(big, fmaxf(f.x, f.y));
+            }
+        }
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        int x = (int)(__float_as_uint(big) >> 23) - 127 - 14;
+        x = big < INFINITY ? max(x, -100) : 0;
+        const float down = __uint_as_float((uint32_t)(127 - x) << 23);
+        const float factor = p.qscale * __uint_as_float((uint32_t)(127 + x) << 23);
+        float sum[NG];
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            sum[j] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = Unpack<T>::pair(w[j][4 * e + i]);
+                    f[2 * i] = v.x * down;
+                    f[2 * i + 1] = v.y * down;
+                }
+                // a word's pairs (n, n + 4), of which odd n come times 16
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float up = n & 1 ? 0.0625f : 1.f;
+                    const uint32_t h = Mma<__half>::pack(f[n] * up, f[n + 4] * up);
+                    qf[j][2 * e + (n >> 1)][n & 1] = h;
+                    const float2 back = Unpack<__half>::pair(h);
+                    sum[j] += (back.x + back.y) / up;
+                }
+            }
+            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
+            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
+        }
+        // head h's sits in lanes 4 h ..
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float f = __shfl_sync(0xffffffffu, factor, 8 * c + 4 * i);
+            fs[i] = f * 16777216.f;
+            m[i] = -INFINITY;
+            lsum[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                fm[j][i] = f * __shfl_sync(0xffffffffu, sum[j], 8 * c + 4 * i);
+                om[j][i] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+                o[j][mt][0] = o[j][mt][1] = o[j][mt][2] = o[j][mt][3] = 0.f;
         }
     }
-    auto numbers = [&](const uint8_t *rec, int row, float (&x)[N]) {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(rec + R::word(row, R::GROUPS * i + j)) >> shift;
-        const float2 f = Unpack<T>::pair(*reinterpret_cast<const uint32_t *>(rec + R::template pair<BS>(row, j)));
+
+    __device__ __forceinline__ static uint32_t codes_k(uint32_t w, uint32_t mask) { return w & mask; }
+    // u - 8 of the lowest nibbles of two halves, in bfloat16
+    __device__ __forceinline__ static uint32_t codes_v(uint32_t w)
+    {
+        return as_word(__hsub2(as_pair<__nv_bfloat16>((w & 0x000f000fu) | 0x43004300u), __float2bfloat162_rn(136.f)));
+    }
+
+    // (scale, minimum) of each group of a row, from shared memory.
+    __device__ __forceinline__ static void pairs(uint32_t at, float (&s)[NG], float (&mn)[NG])
+    {
+        if constexpr (NG == 2) {
+            const uint2 v = lds64(at);
+            const float2 a = Unpack<T>::pair(v.x), b = Unpack<T>::pair(v.y);
+            s[0] = a.x;
+            mn[0] = a.y;
+            s[1] = b.x;
+            mn[1] = b.y;
+        } else {
+            const float2 a = Unpack<T>::pair(lds32(at));
+            s[0] = a.x;
+            mn[0] = a.y;
+        }
+    }
+
+    // 16 tokens whose records (or the 16 rows of one from row0 on) start at
+    // kbase and vbase; nvalid of them count.
+    __device__ __forceinline__ void tile(uint32_t kbase, uint32_t vbase, int row0, int nvalid)
+    {
+        const uint32_t code0 = row0 * R::CODES, pair0 = row0 * R::PAIRS;
+        float acc[NG][4];
+        {
+            uint32_t w[2][2 * NG];   // token, word
 #pragma unroll
-        for (int n = 0; n < N; ++n)
-            x[n] = fmaf((float)((w >> (4 * n)) & 15u), f.x, f.y);
-    };
-    for (int t = warp; !bad && t < L; t += kQ4Warps) {
-        const int64_t at = ((int64_t)table[t / BS] * p.num_kv_heads + kvh) * R::template record<BS>;
-        float k[N], v[N];
-        numbers(p.k_cache + at, t % BS, k);
-        numbers(p.v_cache + at, t % BS, v);
+            for (int i = 0; i < 2; ++i) {
+                if constexpr (NG == 2) {
+                    const uint4 v = lds128(kbase + code0 + kcode[i]);
+                    w[i][0] = v.x;
+                    w[i][1] = v.y;
+                    w[i][2] = v.z;
+                    w[i][3] = v.w;
+                } else {
+                    const uint2 v = lds64(kbase + code0 + kcode[i]);
+                    w[i][0] = v.x;
+                    w[i][1] = v.y;
+                }
+            }
 #pragma unroll
-        for (int g = 0; g < GM; ++g) {
-            if (g < p.group) {
-                float x = 0.f;
+            for (int j = 0; j < NG; ++j) {
+                acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
 #pragma unroll
-                for (int n = 0; n < N; ++n)
-                    x = fmaf(q[g][n], k[n], x);
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t u = w[0][NG * e + j], v = w[1][NG * e + j];
+                    const uint32_t a0[4] = {u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u};
+                    Mma<__half>::run(acc[j], a0, qf[j][2 * e][0], qf[j][2 * e][1]);
+                    const uint32_t a1[4] = {(u >> 8) & 0x000f000fu, (v >> 8) & 0x000f000fu, (u >> 8) & 0x00f000f0u, (v >> 8) & 0x00f000f0u};
+                    Mma<__half>::run(acc[j], a1, qf[j][2 * e + 1][0], qf[j][2 * e + 1][1]);
+                }
+            }
+        }
+
+        // Online softmax in the log2 domain, as in list_attention.cuh; this
+        // lane holds tokens t0 = 4 (g / 2) + g % 2 and t0 + 2 of heads 2c, 2c + 1.
+        constexpr float kSlack = 8.f;
+        const int t0 = 4 * (g >> 1) + (g & 1);
+        float x[2][2], p[2][2];
+        bool over = false;
 #pragma unroll
-                for (int w = 16; w; w >>= 1)
-                    x += __shfl_xor_sync(0xffffffffu, x, w);
-                const float mn = fmaxf(m[g], x), ref = reference_of(mn);
-                const float f = exp2f(m[g] - ref), e = exp2f(x - ref);
-                m[g] = mn;
-                l[g] = l[g] * f + e;
+        for (int i = 0; i < 2; ++i) {
+            float s[NG], mn[NG];
+            pairs(kbase + pair0 + kpair[i], s, mn);
 #pragma unroll
-                for (int n = 0; n < N; ++n)
-                    o[g][n] = fmaf(o[g][n], f, e * v[n]);
+            for (int h = 0; h < 2; ++h) {
+                float dot = s[0] * acc[0][2 * i + h], low = mn[0] * fm[0][h];
+                if constexpr (NG == 2) {
+                    dot = fmaf(s[1], acc[1][2 * i + h], dot);
+                    low = fmaf(mn[1], fm[1][h], low);
+                }
+                x[i][h] = t0 + 2 * i < nvalid ? fmaf(fs[h], dot, low) : -INFINITY;
+                over |= x[i][h] > m[h] + kSlack;
+            }
+        }
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float tm = fmaxf(x[0][h], x[1][h]);
+                tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 4));
+                tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 8));
+                tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
+                const float top = fmaxf(m[h], tm);
+                const float alpha = ex2_fast(m[h] - reference_of(top));
+                lsum[h] *= alpha;
+                m[h] = top;
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    om[j][h] *= alpha;
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt) {
+                        o[j][mt][h] *= alpha;
+                        o[j][mt][2 + h] *= alpha;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float ref = reference_of(m[h]);
+            p[0][h] = ex2_fast(x[0][h] - ref);
+            p[1][h] = ex2_fast(x[1][h] - ref);
+            lsum[h] += p[0][h] + p[1][h];
+        }
+
+        // The weights times the scales, two bfloat16 parts of each, as
+        // B-fragments; the weights times the minima in fp32.
+        uint32_t hi[NG][2], lo[NG][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float s[NG], mn[NG];
+            pairs(vbase + pair0 + kpair[i], s, mn);
+            if (nvalid < C::TILE && t0 + 2 * i >= nvalid) {
+                // no token: what is there may be anything
+#pragma unroll
+                for (int j = 0; j < NG; ++j)
+                    s[j] = mn[j] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                const float mid = fmaf(8.f, s[j], mn[j]);
+                om[j][0] = fmaf(p[i][0], mid, om[j][0]);
+                om[j][1] = fmaf(p[i][1], mid, om[j][1]);
+                const float a = p[i][0] * s[j], b = p[i][1] * s[j];
+                const uint32_t h = Mma<__nv_bfloat16>::pack(a, b);
+                const float2 f = Unpack<__nv_bfloat16>::pair(h);
+                hi[j][i] = movmatrix_trans(h);
+                lo[j][i] = movmatrix_trans(Mma<__nv_bfloat16>::pack(a - f.x, b - f.y));
+            }
+        }
+        uint32_t w[4][NG];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (NG == 2) {
+                const uint2 v = lds64(vbase + code0 + vcode[i]);
+                w[i][0] = v.x;
+                w[i][1] = v.y;
+            } else {
+                w[i][0] = lds32(vbase + code0 + vcode[i]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t u = __byte_perm(w[0][j], w[1][j], e ? 0x7632 : 0x5410);
+                const uint32_t v = __byte_perm(w[2][j], w[3][j], e ? 0x7632 : 0x5410);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t a[4] = {codes_v(u >> (8 * k)), codes_v(u >> (8 * k + 4)), codes_v(v >> (8 * k)), codes_v(v >> (8 * k + 4))};
+                    Mma<__nv_bfloat16>::run(o[j][2 * e + k], a, hi[j][0], hi[j][1]);
+                    Mma<__nv_bfloat16>::run(o[j][2 * e + k], a, lo[j][0], lo[j][1]);
+                }
             }
         }
     }
+
+    // This warp's (max, sum, sums of values) of the heads below `group` into
+    // the merge scratch.
+    __device__ __forceinline__ void finish(float *mw, float *lw, float *aw, int warp, int group)
+    {
 #pragma unroll
-    for (int g = 0; g < GM; ++g) {
-        if (lane == 0) {
-            s_m[warp][g] = m[g];
-            s_l[warp][g] = l[g];
+        for (int h = 0; h < 2; ++h) {
+            float l = lsum[h], add[NG];
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                add[j] = om[j][h];
+                add[j] += __shfl_xor_sync(0xffffffffu, add[j], 4);
+                add[j] += __shfl_xor_sync(0xffffffffu, add[j], 8);
+                add[j] += __shfl_xor_sync(0xffffffffu, add[j], 16);
+            }
+            const int row = 2 * c + h;
+            if (row < group) {
+                if (g == 0) {
+                    mw[warp * kListMaxGroup + row] = m[h];
+                    lw[warp * kListMaxGroup + row] = l;
+                }
+                float *dst = aw + (warp * kListMaxGroup + row) * C::AWS + 8 * g;
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt)
+                        *reinterpret_cast<float2 *>(dst + 64 * j + 2 * mt) = make_float2(o[j][mt][h] + add[j], o[j][mt][2 + h] + add[j]);
+                }
+            }
         }
+    }
+};
+
+// Grid (partition, kv head, sequence).
+template <typename T, int D, int BS>
+__global__ void __launch_bounds__(kListThreads, kQ4Ctas)
+q4_attention_kernel(const __grid_constant__ Q4Params a)
+{
+    using C = Q4Cfg<D, BS>;
+    constexpr int S = C::S, NW = kListWarps;
+    const ListParams &p = a.list;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = aligned_smem(smem_raw);
+    int32_t *phys = reinterpret_cast<int32_t *>(smem + C::OFF_PHYS);
+    const int part = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + warp * S;
+    uint32_t *flag = reinterpret_cast<uint32_t *>(smem + C::OFF_FLAG);
+    int *warp_tokens = reinterpret_cast<int *>(smem + C::OFF_FLAG + 16);
+    if (lane == 0) {
+        for (int s = 0; s < S; ++s)
+            mbar_init(&bars[s], 1);
+        fence_mbar_init();
+    }
+    if (threadIdx.x == 0)
+        *flag = 0;
+    wait_for_stream();
+    const int L = p.context_lens[seq];
+    const int e0 = part * p.part_blocks;
+    ListEntries<BS> entries;
+    entries.load(p, seq, kvh, e0);
+    ListResult<D> *res = reinterpret_cast<ListResult<D> *>(smem + C::OFF_RESULT);
+    int tokens = 0;
+    if (L < 0 || L > p.max_context_len) {
+        if (part == 0 && kvh == 0 && threadIdx.x == 0)
+            report(p.status, PKV_DEV_BAD_CONTEXT_LEN);
+        tokens = -1;
+    } else if ((int64_t)e0 * BS < L) {
+        tokens = entries.resolve(p, phys, e0, L);
+        const int most = __reduce_max_sync(0xffffffffu, tokens);
+        if (lane == 0)
+            warp_tokens[warp] = most;
+        if (__syncthreads_or(tokens < 0)) {
+            if (threadIdx.x == 0)
+                report(p.status, PKV_DEV_BAD_BLOCK);
+            tokens = -1;
+        } else {
 #pragma unroll
-        for (int n = 0; n < N; ++n)
-            s_o[warp][g][d0 + n] = o[g][n];
+            for (int w = 0; w < NW; ++w)
+                tokens = max(tokens, warp_tokens[w]);
+        }
+    }
+    if (tokens <= 0) {
+        if (threadIdx.x < kListMaxGroup) {
+            res->m[threadIdx.x] = -INFINITY;
+            res->l[threadIdx.x] = tokens < 0 ? -1.f : 0.f;
+        }
+        __syncthreads();
+        write_result<D>(p, res, seq, kvh, part);
+        return;
+    }
+
+    // ---- this warp's stages: warp, warp + NW, ...
+    const int nstages = (tokens + C::TOK - 1) / C::TOK;
+    const int my_n = warp < nstages ? (nstages - 1 - warp) / NW + 1 : 0;
+    uint8_t *stages = smem + warp * S * C::STAGE_BYTES;
+    auto issue = [&](int i, int st) {
+        const int t0 = (warp + i * NW) * C::TOK;
+        uint8_t *kd = stages + st * C::STAGE_BYTES, *vd = kd + C::RECS * C::REC;
+        const int n = min(C::RECS, (tokens - t0 + BS - 1) / BS);
+        mbar_arrive_expect_tx(&bars[st], (uint32_t)(n * 2 * C::REC));
+        for (int b = 0; b < n; ++b) {
+            const int64_t at = ((int64_t)phys[t0 / BS + b] * p.num_kv_heads + kvh) * C::REC;
+            bulk_load(kd + b * C::REC, p.k_cache + at, C::REC, &bars[st]);
+            bulk_load(vd + b * C::REC, p.v_cache + at, C::REC, &bars[st]);
+        }
+    };
+    if (lane == 0) {
+        for (int i = 0; i < min(my_n, S); ++i)
+            issue(i, i);
+    }
+    Q4Engine<T, D, BS> eng;
+    eng.init(a, seq, kvh, lane);
+
+    int failed_at = -1;
+    for (int i = 0; i < my_n; ++i) {
+        const int st = i % S;
+        // the warp gives up as one: its products and shuffles need every lane
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[st], (uint32_t)((i / S) & 1)))) {
+            failed_at = i;
+            break;
+        }
+        const int t0 = (warp + i * NW) * C::TOK;
+        const uint32_t kbase = smem_u32(stages + st * C::STAGE_BYTES);
+#pragma unroll 1
+        for (int row0 = 0; row0 < C::TOK && t0 + row0 < tokens; row0 += C::TILE)
+            eng.tile(kbase, kbase + C::RECS * C::REC, row0, tokens - t0 - row0);
+        __syncwarp();
+        if (lane == 0 && i + S < my_n) {
+            fence_proxy_async_smem();
+            issue(i + S, st);
+        }
+    }
+    if (failed_at >= 0) {
+        // no CTA leaves with loads in flight
+        for (int i = failed_at; i < min(my_n, failed_at + S); ++i)
+            drain_wait(&bars[i % S], (uint32_t)((i / S) & 1), p.status);
+        if (lane == 0) {
+            report(p.status, PKV_DEV_TIMEOUT);
+            atomicOr(flag, 1u);
+        }
+    }
+
+    // ---- the warps' parts, through the rings' memory
+    __syncthreads();
+    const bool failed = *reinterpret_cast<volatile uint32_t *>(flag) != 0;
+    float *mw = reinterpret_cast<float *>(smem);
+    float *lw = mw + NW * kListMaxGroup;
+    float *aw = lw + NW * kListMaxGroup;
+    eng.finish(mw, lw, aw, warp, p.group);
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.group * D; i += kListThreads) {
+        const int r = i / D, d = i % D;
+        float Mx = -INFINITY, num = 0.f, den = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+            Mx = fmaxf(Mx, mw[w * kListMaxGroup + r]);
+        const float ref = reference_of(Mx);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float f = exp2f(mw[w * kListMaxGroup + r] - ref);   // 0 for a warp without tokens; NaN sums stay
+            num += f * aw[(w * kListMaxGroup + r) * C::AWS + d];
+            den += f * lw[w * kListMaxGroup + r];
+        }
+        res->acc[r][d] = num;
+        if (d == 0) {
+            res->m[r] = Mx;
+            res->l[r] = failed ? -1.f : den;
+        }
     }
     __syncthreads();
-    for (int k = threadIdx.x; k < p.group * D; k += kQ4Warps * 32) {
-        const int g = k / D, d = k % D;
-        float mx = -INFINITY, num = 0.f, den = 0.f;
-        for (int w = 0; w < kQ4Warps; ++w)
-            mx = fmaxf(mx, s_m[w][g]);
-        for (int w = 0; w < kQ4Warps; ++w) {
-            const float f = exp2f(s_m[w][g] - reference_of(mx));
-            num += f * s_o[w][g][d];
-            den += f * s_l[w][g];
-        }
-        store_out(p.out, p.out_dtype, ((int64_t)seq * p.num_kv_heads * p.group + kvh * p.group + g) * D + d, den == 0.f ? 0.f : num / den);
-    }
+    write_result<D>(p, res, seq, kvh, part);
+    if (p.np > 1 && !p.cluster)
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 }  // namespace pkv
