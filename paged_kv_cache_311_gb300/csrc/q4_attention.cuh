@@ -3,7 +3,7 @@
 //   out[s, h] = sum_t softmax_t(scale * q[s, h] . k_t) * v_t,
 // a row's numbers s u + m for each group j of 64 dimensions (see q4_cache.cuh):
 //   q . k_t   = sum_j s_tj (q_j . u_tj) + m_tj sum(q_j)
-//   sum_t w_t v_t = sum_t (w_t s_tj) (u_tj - 8) + sum_t w_t (m_tj + 8 s_tj)
+//   sum_t w_t v_t = sum_t (w_t s_tj) u_tj + sum_t w_t m_tj
 // so that the products take whole numbers, and scales and minima join them in
 // fp32.
 //
@@ -11,19 +11,23 @@
 // context, kv head, sequence) with the kv head's G <= 8 query heads, partitions
 // merged by a cluster or through the workspace.  Each of four warps streams
 // records (bulk copies, one per block, codes with their scales) through a ring
-// of its own and takes them in tiles of 16 tokens: the tile's tokens are M of
+// of its own, 32 tokens at a time, and takes them in two tiles of 16 tokens: a tile's tokens are M of
 // S^T = K q^T, its dimensions M of O^T += V^T W^T, the query heads N of
 // warp-level MMAs (m16n8k16).
 //
-// Codes become matrix fragments without a conversion: a word's nibbles masked
-// in place are 16-bit numbers, two at a time.
-//   K: f16.  u in a half's lowest bits is the subnormal u 2^-24, in the next
-//      four u 2^-20: a mask is all it takes (five instructions for eight codes).
-//      The factors go into q (a sixteenth for the latter) and the scores.
-//   V: tokens are the products' inner axis, so two tokens' words are first
-//      paired half by half.  bfloat16: u in a mantissa's lowest bits is 128 + u;
-//      136 is subtracted, exactly.  The weights w_t s_tj can have any size,
-//      which f16 cannot hold; bfloat16 can, in two parts of together 16 bits.
+// Codes become f16 matrix fragments without a conversion: a word's nibbles
+// masked in place are numbers, two at a time.  u in a half's lowest four bits is
+// the subnormal u 2^-24, in the next four u 2^-20: a mask is all it takes (five
+// instructions for eight codes of K; V's tokens are the products' inner axis, so
+// two tokens' words are first paired half by half: six).  The factors go into q
+// (a sixteenth for the latter) and the scores, and into the outputs.
+//
+// A weight w_t s_tj enters the product with V in two f16 parts: off by 2^-22 of
+// itself, or 2^-32 of the largest of its head so far.  That needs the largest
+// below 2^16 whatever the scales are, so the softmax's reference is not a head's
+// largest score alone: weights are 2^(x - m) with m such that the largest
+// 2^(x - m) s, not the largest 2^(x - m), is near 2^7.
+//
 // The M axes' order is free: row 2 c + e + 8 f of a tile is its token
 // 4 c + 2 f + e (so that a thread's four tokens of V are neighbours), and a
 // thread's rows of V^T are the dimensions that its words hold.
@@ -39,15 +43,18 @@ struct Q4Params {
     int64_t q_stride;            // elements between two sequences' rows of q
 };
 
-constexpr int kQ4Ring = 49152;   // ring bytes of a CTA
-constexpr int kQ4Ctas = 4;       // CTAs per SM
+constexpr int kQ4Ring = 57344;   // ring bytes of a CTA at most
+constexpr int kQ4Ctas = 3;       // CTAs per SM
 
 template <int D, int BS> struct Q4Cfg {
     using R = Q4Row<D>;
-    static constexpr int TILE = 16;
+    static constexpr int TILE = 16, TILES = 2;
     static constexpr int REC = R::template record<BS>;
-    static constexpr int TOK = BS < TILE ? TILE : BS;          // tokens of a stage
+    static constexpr int TOK = TILES * TILE;                   // tokens of a stage
     static constexpr int RECS = TOK / BS;
+    // from a tile's codes and pairs to the next's
+    static constexpr int NEXT_CODE = BS > TILE ? TILE * R::CODES : TILE / BS * REC;
+    static constexpr int NEXT_PAIR = BS > TILE ? TILE * R::PAIRS : TILE / BS * REC;
     static constexpr int STAGE_BYTES = 2 * RECS * REC;
     static constexpr int S0 = kQ4Ring / (kListWarps * STAGE_BYTES);
     static constexpr int S = S0 < 2 ? 2 : S0;
@@ -58,7 +65,8 @@ template <int D, int BS> struct Q4Cfg {
     static constexpr int OFF_RESULT = kListWarps * kListMaxGroup * (AWS + 2) * 4;
     static constexpr int RESULT_END = OFF_RESULT + kListMaxGroup * (D + 2) * 4;
     static constexpr int OFF_PHYS = RING > RESULT_END ? RING : RESULT_END;
-    static constexpr int OFF_BAR = OFF_PHYS + kListCap * 4;
+    static constexpr int OFF_AT = OFF_PHYS + kListCap * 4;
+    static constexpr int OFF_BAR = OFF_AT + kListCap * 8;
     static constexpr int OFF_FLAG = OFF_BAR + kListWarps * S * 8;
     static constexpr int SMEM_BYTES = OFF_FLAG + 32 + 1024;    // slack for the alignment to 1024
     static_assert(REC % 16 == 0 && OFF_RESULT % 16 == 0 && OFF_PHYS % 16 == 0, "alignment");
@@ -69,13 +77,16 @@ template <typename T, int D, int BS> struct Q4Engine {
     using C = Q4Cfg<D, BS>;
     using R = Q4Row<D>;
     static constexpr int NG = R::GROUPS;
+    static constexpr float kMost = 32768.f;      // of a weight times its scale
+    static constexpr float kLift = 7.f;          // log2 of the largest one where the reference is set
+    static constexpr float kLeast = 0x1p-100f;   // smaller scales count as this: weights stay below 2^115
 
     uint32_t qf[NG][4][2];   // q^T B-fragments of head g: group, step
     float fs[2];             // heads 2c, 2c + 1: score of s (q . u)
     float fm[NG][2];         //                   score of m
     float o[NG][4][4];       // O^T C-fragments: group, m-tile
-    float om[NG][2];         // this lane's tokens' sums of w (m + 8 s)
-    float m[2], lsum[2];     // heads 2c, 2c + 1
+    float om[NG][2];         // this lane's tokens' sums of w m
+    float m[2], lsum[2];     // heads 2c, 2c + 1: weights' reference and sum
     int kcode[2], kpair[2];  // byte offsets of this lane's tokens of K in a stage's records
     int vcode[4];            // and of V
     int g, c;
@@ -175,13 +186,6 @@ template <typename T, int D, int BS> struct Q4Engine {
         }
     }
 
-    __device__ __forceinline__ static uint32_t codes_k(uint32_t w, uint32_t mask) { return w & mask; }
-    // u - 8 of the lowest nibbles of two halves, in bfloat16
-    __device__ __forceinline__ static uint32_t codes_v(uint32_t w)
-    {
-        return as_word(__hsub2(as_pair<__nv_bfloat16>((w & 0x000f000fu) | 0x43004300u), __float2bfloat162_rn(136.f)));
-    }
-
     // (scale, minimum) of each group of a row, from shared memory.
     __device__ __forceinline__ static void pairs(uint32_t at, float (&s)[NG], float (&mn)[NG])
     {
@@ -199,74 +203,110 @@ template <typename T, int D, int BS> struct Q4Engine {
         }
     }
 
-    // 16 tokens whose records (or the 16 rows of one from row0 on) start at
-    // kbase and vbase; nvalid of them count.
-    __device__ __forceinline__ void tile(uint32_t kbase, uint32_t vbase, int row0, int nvalid)
+    // S^T of a tile.
+    __device__ __forceinline__ void scores(uint32_t kbase, int tile, float (&acc)[NG][4]) const
     {
-        const uint32_t code0 = row0 * R::CODES, pair0 = row0 * R::PAIRS;
-        float acc[NG][4];
-        {
-            uint32_t w[2][2 * NG];   // token, word
+        uint32_t w[2][2 * NG];   // token, word
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t at = kbase + kcode[i] + tile * C::NEXT_CODE;
+            if constexpr (NG == 2) {
+                const uint4 v = lds128(at);
+                w[i][0] = v.x;
+                w[i][1] = v.y;
+                w[i][2] = v.z;
+                w[i][3] = v.w;
+            } else {
+                const uint2 v = lds64(at);
+                w[i][0] = v.x;
+                w[i][1] = v.y;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t u = w[0][NG * e + j], v = w[1][NG * e + j];
+                const uint32_t a0[4] = {u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u};
+                Mma<__half>::run(acc[j], a0, qf[j][2 * e][0], qf[j][2 * e][1]);
+                const uint32_t a1[4] = {(u >> 8) & 0x000f000fu, (v >> 8) & 0x000f000fu, (u >> 8) & 0x00f000f0u, (v >> 8) & 0x00f000f0u};
+                Mma<__half>::run(acc[j], a1, qf[j][2 * e + 1][0], qf[j][2 * e + 1][1]);
+            }
+        }
+    }
+
+    // The 32 tokens of the stage whose records start at kbase and vbase;
+    // nvalid of them count.
+    __device__ __forceinline__ void step(uint32_t kbase, uint32_t vbase, int nvalid)
+    {
+        // Online softmax in the log2 domain; this lane holds tokens t0 = 4 (g /
+        // 2) + g % 2 and t0 + 2 of each tile, heads 2c, 2c + 1.  While no weight
+        // times its scale passes kMost, weights are taken against the head's
+        // reference m unchanged: no maximum across lanes, no rescaling.
+        constexpr int N = 2 * C::TILES;          // this lane's tokens
+        const int t0 = 4 * (g >> 1) + (g & 1);
+        float x[N][2], p[N][2], s[N][NG], mn[N][NG], top[N];
+        bool over = false;
+#pragma unroll
+        for (int tile = 0; tile < C::TILES; ++tile) {
+            float acc[NG][4];
+            scores(kbase, tile, acc);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if constexpr (NG == 2) {
-                    const uint4 v = lds128(kbase + code0 + kcode[i]);
-                    w[i][0] = v.x;
-                    w[i][1] = v.y;
-                    w[i][2] = v.z;
-                    w[i][3] = v.w;
-                } else {
-                    const uint2 v = lds64(kbase + code0 + kcode[i]);
-                    w[i][0] = v.x;
-                    w[i][1] = v.y;
+                const int n = 2 * tile + i;
+                pairs(kbase + kpair[i] + tile * C::NEXT_PAIR, s[n], mn[n]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float dot = s[n][0] * acc[0][2 * i + h], low = mn[n][0] * fm[0][h];
+                    if constexpr (NG == 2) {
+                        dot = fmaf(s[n][1], acc[1][2 * i + h], dot);
+                        low = fmaf(mn[n][1], fm[1][h], low);
+                    }
+                    x[n][h] = fmaf(fs[h], dot, low);
                 }
+                pairs(vbase + kpair[i] + tile * C::NEXT_PAIR, s[n], mn[n]);
             }
+        }
+        if (nvalid < C::TOK) {
+            // no token: what is there may be anything
 #pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+            for (int n = 0; n < N; ++n) {
+                if (t0 + 2 * (n & 1) + C::TILE * (n >> 1) >= nvalid) {
+                    x[n][0] = x[n][1] = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t u = w[0][NG * e + j], v = w[1][NG * e + j];
-                    const uint32_t a0[4] = {u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u};
-                    Mma<__half>::run(acc[j], a0, qf[j][2 * e][0], qf[j][2 * e][1]);
-                    const uint32_t a1[4] = {(u >> 8) & 0x000f000fu, (v >> 8) & 0x000f000fu, (u >> 8) & 0x00f000f0u, (v >> 8) & 0x00f000f0u};
-                    Mma<__half>::run(acc[j], a1, qf[j][2 * e + 1][0], qf[j][2 * e + 1][1]);
+                    for (int j = 0; j < NG; ++j)
+                        s[n][j] = mn[n][j] = 0.f;
                 }
             }
         }
-
-        // Online softmax in the log2 domain, as in list_attention.cuh; this
-        // lane holds tokens t0 = 4 (g / 2) + g % 2 and t0 + 2 of heads 2c, 2c + 1.
-        constexpr float kSlack = 8.f;
-        const int t0 = 4 * (g >> 1) + (g & 1);
-        float x[2][2], p[2][2];
-        bool over = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float s[NG], mn[NG];
-            pairs(kbase + pair0 + kpair[i], s, mn);
+        for (int n = 0; n < N; ++n) {
+            // minima of a size that makes the scales' part of the numbers one
+            // below fp32's last bit hold the weights down, too
+            top[n] = NG == 2 ? fmaxf(fmaxf(s[n][0], s[n][NG - 1]), 0x1p-24f * fmaxf(fabsf(mn[n][0]), fabsf(mn[n][NG - 1])))
+                             : fmaxf(s[n][0], 0x1p-24f * fabsf(mn[n][0]));
+            top[n] = fmaxf(top[n], kLeast);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float dot = s[0] * acc[0][2 * i + h], low = mn[0] * fm[0][h];
-                if constexpr (NG == 2) {
-                    dot = fmaf(s[1], acc[1][2 * i + h], dot);
-                    low = fmaf(mn[1], fm[1][h], low);
-                }
-                x[i][h] = t0 + 2 * i < nvalid ? fmaf(fs[h], dot, low) : -INFINITY;
-                over |= x[i][h] > m[h] + kSlack;
+                p[n][h] = ex2_fast(x[n][h] - m[h]);   // infinite before the first token
+                over |= p[n][h] * top[n] > kMost;
             }
         }
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float tm = fmaxf(x[0][h], x[1][h]);
-                tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 4));
-                tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 8));
-                tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
-                const float top = fmaxf(m[h], tm);
-                const float alpha = ex2_fast(m[h] - reference_of(top));
+                float t = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+                    t = fmaxf(t, x[n][h] + __log2f(top[n]) - kLift);
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                t = fmaxf(m[h], t);
+                const float ref = reference_of(t), alpha = ex2_fast(m[h] - ref);
+                m[h] = t;
                 lsum[h] *= alpha;
-                m[h] = top;
 #pragma unroll
                 for (int j = 0; j < NG; ++j) {
                     om[j][h] *= alpha;
@@ -276,63 +316,58 @@ template <typename T, int D, int BS> struct Q4Engine {
                         o[j][mt][2 + h] *= alpha;
                     }
                 }
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+                    p[n][h] = ex2_fast(x[n][h] - ref);
             }
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float ref = reference_of(m[h]);
-            p[0][h] = ex2_fast(x[0][h] - ref);
-            p[1][h] = ex2_fast(x[1][h] - ref);
-            lsum[h] += p[0][h] + p[1][h];
-        }
 
-        // The weights times the scales, two bfloat16 parts of each, as
-        // B-fragments; the weights times the minima in fp32.
-        uint32_t hi[NG][2], lo[NG][2];
+        // The weights' sums, their products with the minima in fp32, and with
+        // the scales in two f16 parts each, as B-fragments.
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float s[NG], mn[NG];
-            pairs(vbase + pair0 + kpair[i], s, mn);
-            if (nvalid < C::TILE && t0 + 2 * i >= nvalid) {
-                // no token: what is there may be anything
+        for (int tile = 0; tile < C::TILES; ++tile) {
+            uint32_t hi[NG][2], lo[NG][2];
 #pragma unroll
-                for (int j = 0; j < NG; ++j)
-                    s[j] = mn[j] = 0.f;
+            for (int i = 0; i < 2; ++i) {
+                const int n = 2 * tile + i;
+                lsum[0] += p[n][0];
+                lsum[1] += p[n][1];
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    om[j][0] = fmaf(p[n][0], mn[n][j], om[j][0]);
+                    om[j][1] = fmaf(p[n][1], mn[n][j], om[j][1]);
+                    const float a = p[n][0] * s[n][j], b = p[n][1] * s[n][j];
+                    const uint32_t h = Mma<__half>::pack(a, b);
+                    const float2 f = Unpack<__half>::pair(h);
+                    hi[j][i] = movmatrix_trans(h);
+                    lo[j][i] = movmatrix_trans(Mma<__half>::pack(a - f.x, b - f.y));
+                }
+            }
+            uint32_t w[4][NG];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t at = vbase + vcode[i] + tile * C::NEXT_CODE;
+                if constexpr (NG == 2) {
+                    const uint2 v = lds64(at);
+                    w[i][0] = v.x;
+                    w[i][1] = v.y;
+                } else {
+                    w[i][0] = lds32(at);
+                }
             }
 #pragma unroll
             for (int j = 0; j < NG; ++j) {
-                const float mid = fmaf(8.f, s[j], mn[j]);
-                om[j][0] = fmaf(p[i][0], mid, om[j][0]);
-                om[j][1] = fmaf(p[i][1], mid, om[j][1]);
-                const float a = p[i][0] * s[j], b = p[i][1] * s[j];
-                const uint32_t h = Mma<__nv_bfloat16>::pack(a, b);
-                const float2 f = Unpack<__nv_bfloat16>::pair(h);
-                hi[j][i] = movmatrix_trans(h);
-                lo[j][i] = movmatrix_trans(Mma<__nv_bfloat16>::pack(a - f.x, b - f.y));
-            }
-        }
-        uint32_t w[4][NG];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (NG == 2) {
-                const uint2 v = lds64(vbase + code0 + vcode[i]);
-                w[i][0] = v.x;
-                w[i][1] = v.y;
-            } else {
-                w[i][0] = lds32(vbase + code0 + vcode[i]);
-            }
-        }
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t u = __byte_perm(w[0][j], w[1][j], e ? 0x7632 : 0x5410);
+                    const uint32_t v = __byte_perm(w[2][j], w[3][j], e ? 0x7632 : 0x5410);
 #pragma unroll
-        for (int j = 0; j < NG; ++j) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t u = __byte_perm(w[0][j], w[1][j], e ? 0x7632 : 0x5410);
-                const uint32_t v = __byte_perm(w[2][j], w[3][j], e ? 0x7632 : 0x5410);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t a[4] = {codes_v(u >> (8 * k)), codes_v(u >> (8 * k + 4)), codes_v(v >> (8 * k)), codes_v(v >> (8 * k + 4))};
-                    Mma<__nv_bfloat16>::run(o[j][2 * e + k], a, hi[j][0], hi[j][1]);
-                    Mma<__nv_bfloat16>::run(o[j][2 * e + k], a, lo[j][0], lo[j][1]);
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t a[4] = {(u >> (8 * k)) & 0x000f000fu, (u >> (8 * k)) & 0x00f000f0u,
+                                               (v >> (8 * k)) & 0x000f000fu, (v >> (8 * k)) & 0x00f000f0u};
+                        Mma<__half>::run(o[j][2 * e + k], a, hi[j][0], hi[j][1]);
+                        Mma<__half>::run(o[j][2 * e + k], a, lo[j][0], lo[j][1]);
+                    }
                 }
             }
         }
@@ -366,7 +401,7 @@ template <typename T, int D, int BS> struct Q4Engine {
                 for (int j = 0; j < NG; ++j) {
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt)
-                        *reinterpret_cast<float2 *>(dst + 64 * j + 2 * mt) = make_float2(o[j][mt][h] + add[j], o[j][mt][2 + h] + add[j]);
+                        *reinterpret_cast<float2 *>(dst + 64 * j + 2 * mt) = make_float2(fmaf(o[j][mt][h], 16777216.f, add[j]), fmaf(o[j][mt][2 + h], 1048576.f, add[j]));
                 }
             }
         }
@@ -384,6 +419,7 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = aligned_smem(smem_raw);
     int32_t *phys = reinterpret_cast<int32_t *>(smem + C::OFF_PHYS);
+    int64_t *record = reinterpret_cast<int64_t *>(smem + C::OFF_AT);   // byte offsets of the partition's records
     const int part = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + warp * S;
@@ -432,6 +468,11 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
         return;
     }
 
+#pragma unroll 1
+    for (int k = threadIdx.x; k * BS < tokens; k += kListThreads)
+        record[k] = ((int64_t)phys[k] * p.num_kv_heads + kvh) * C::REC;
+    __syncthreads();
+
     // ---- this warp's stages: warp, warp + NW, ...
     const int nstages = (tokens + C::TOK - 1) / C::TOK;
     const int my_n = warp < nstages ? (nstages - 1 - warp) / NW + 1 : 0;
@@ -442,7 +483,7 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
         const int n = min(C::RECS, (tokens - t0 + BS - 1) / BS);
         mbar_arrive_expect_tx(&bars[st], (uint32_t)(n * 2 * C::REC));
         for (int b = 0; b < n; ++b) {
-            const int64_t at = ((int64_t)phys[t0 / BS + b] * p.num_kv_heads + kvh) * C::REC;
+            const int64_t at = record[t0 / BS + b];
             bulk_load(kd + b * C::REC, p.k_cache + at, C::REC, &bars[st]);
             bulk_load(vd + b * C::REC, p.v_cache + at, C::REC, &bars[st]);
         }
@@ -464,9 +505,7 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
         }
         const int t0 = (warp + i * NW) * C::TOK;
         const uint32_t kbase = smem_u32(stages + st * C::STAGE_BYTES);
-#pragma unroll 1
-        for (int row0 = 0; row0 < C::TOK && t0 + row0 < tokens; row0 += C::TILE)
-            eng.tile(kbase, kbase + C::RECS * C::REC, row0, tokens - t0 - row0);
+        eng.step(kbase, kbase + C::RECS * C::REC, tokens - t0);
         __syncwarp();
         if (lane == 0 && i + S < my_n) {
             fence_proxy_async_smem();

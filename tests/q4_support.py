@@ -139,10 +139,10 @@ def attention_reference(c, k=None, v=None):
             z = c["scale"] * (qq @ rows(k, h).T)
             p = np.exp(z - z.max(-1, keepdims=True))
             out[b, h * G:(h + 1) * G] = (p / p.sum(-1, keepdims=True)) @ rows(v, h)
-            # the largest sum of a score's terms (codes up to 15, minima), and of a value's (|u - 8| <= 8)
+            # the largest sum of a score's terms (codes up to 15, minima), and of a value's
             qa = np.abs(qq).reshape(G, -1, 64).sum(-1)
             score[b, h * G:(h + 1) * G] = abs(c["scale"]) * (qa @ (15 * rows(sk, h) + np.abs(rows(mk, h))).T).max(-1)
-            value[b, h * G:(h + 1) * G] = (8 * rows(sv, h) + np.abs(rows(mv, h) + 8 * rows(sv, h))).max()
+            value[b, h * G:(h + 1) * G] = (15 * rows(sv, h) + np.abs(rows(mv, h))).max()
     return out, score, value
 
 
@@ -154,12 +154,14 @@ def attention_tolerance(c, ref, score, value, out_dtype):
     so it is off by ds <= (D + 8) 2^-23 of its terms' sum; q brought to f16 by a
     power of two is off by at most 2^-35 of its head's largest, which times D
     terms is below one of those steps.  Every weight is then off by a factor
-    within e^(2 ds), by 2^-20 for the exponential and the division, and by 2^-17
-    as it enters the product with the codes in two bfloat16 parts; the sums over
-    L tokens are cut L + 16 times: each relative to sum_i w_i |v_i|'s terms.  A
-    16-bit output adds half a step of its own."""
+    within e^(2 ds), and by 2^-20 for the exponential, the division and the two
+    f16 parts in which it enters the product with the codes (2^-22, and 2^-32 of
+    the largest weight for each token, which L 2^-23 covers).  The sums over L
+    tokens are cut at most L + 16 times, each time by 2^-23 of what has been
+    summed: at most sum_i w_i (15 s + |m|), where codes and minima are summed
+    apart.  A 16-bit output adds half a step of its own."""
     L = np.asarray(c["lens"], float)[:, None]
-    rel = np.expm1(2 * (c["D"] + 8) * 2.0 ** -23 * score) + 2.0 ** -20 + 2.0 ** -17 + (L + 16) * 2.0 ** -23
+    rel = np.expm1(2 * (c["D"] + 8) * 2.0 ** -23 * score) + 2.0 ** -20 + (L + 16) * 2.0 ** -23
     tol = np.broadcast_to((rel * value)[..., None], ref.shape)
     if out_dtype != torch.float32:
         tiny = {torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134}[out_dtype]
