@@ -660,8 +660,7 @@ int pkv_gather_cache_q4(void *key, int64_t key_stride, void *value, int64_t valu
  *   max_context_len  host bound of context_lens (at most max_blocks_per_seq *
  *              block_size)
  *   partition_size  0 = automatic; else tokens per partition of the context,
- *              a multiple of 32 and of block_size (512 blocks at most, unless
- *              the whole context is shorter: PKV_EUNSUPPORTED)
+ *              a multiple of 32 and of block_size
  *   workspace  at least pkv_paged_attention_q4_workspace_bytes(...) bytes,
  *              16-byte aligned (may be NULL where that is 0)
  * head_dim 64 or 128; block_size 8, 16 or 32; num_heads / num_kv_heads 1 to 8;

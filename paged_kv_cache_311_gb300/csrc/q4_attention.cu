@@ -10,6 +10,51 @@
 namespace pkv {
 namespace {
 
+// How a call is cut: streamed into `shares`, or rows into `list.np` partitions.
+struct Q4Cut {
+    ListCut list;
+    int shares, part_units;
+};
+
+// Few rows are cut as lists of blocks are, each row a cluster of up to eight
+// CTAs; short rows (up to 1024 tokens) stay whole; other calls are streamed, the
+// only cut that goes by the contexts' own lengths.  (200 sequences of up to 512
+// tokens, 8 kv heads: whole 32.8 us, streamed 36.3; 33 of up to 4095, heads of
+// 64: 34.9 and 24.6; 64 of 128 to 2048, 32 kv heads: 87 and 90.)
+Q4Cut q4_cut(long long rows, long long max_context_len, int block_size, int partition_size)
+{
+    Q4Cut c{};
+    const long long blocks = max_context_len > 0 ? (max_context_len + block_size - 1) / block_size : 1;
+    c.list = list_cut(rows, blocks, block_size, partition_size);
+    if (partition_size > 0)
+        c.part_units = partition_size / kQ4Unit;
+    else if (!c.list.cluster && !(c.list.np == 1 && max_context_len <= 1024))
+        c.shares = kQ4Ctas * device_sm_count();
+    return c;
+}
+
+// The workspace of a cut; false if it passes 64 bits.
+struct Q4Layout {
+    ListLayout list;
+    size_t share_off, total;
+};
+bool q4_layout(const Q4Cut &c, uint64_t seqs, uint64_t heads, uint64_t kv_heads, uint64_t head_dim, Q4Layout *lay)
+{
+    *lay = Q4Layout{};
+    if (c.shares) {
+        // two parts of each share, of a group's heads, and where the share lies
+        if (!list_layout(2 * (uint64_t)c.shares, heads / kv_heads, 1, head_dim, &lay->list))
+            return false;
+        lay->share_off = (lay->list.total + 15) / 16 * 16;
+        lay->total = lay->share_off + c.shares * sizeof(Q4Share);
+        return true;
+    }
+    if (c.list.np > 1 && !c.list.cluster && !list_layout(seqs, heads, c.list.np, head_dim, &lay->list))
+        return false;
+    lay->total = lay->list.total;
+    return true;
+}
+
 template <typename T, int D, int BS>
 int run_q4(const Q4Params &p, cudaStream_t stream)
 {
@@ -20,7 +65,8 @@ int run_q4(const Q4Params &p, cudaStream_t stream)
     if (rc)
         return rc;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.list.np, (unsigned)p.list.num_kv_heads, (unsigned)p.list.num_seqs);
+    cfg.gridDim = p.shares ? dim3((unsigned)p.shares)
+                           : dim3((unsigned)p.list.np, (unsigned)p.list.num_kv_heads, (unsigned)p.list.num_seqs);
     cfg.blockDim = dim3(kListThreads);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = stream;
@@ -35,6 +81,11 @@ int run_q4(const Q4Params &p, cudaStream_t stream)
     cfg.numAttrs = p.list.cluster ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess)
         return PKV_ECUDA;
+    if (p.shares) {
+        static unsigned long long merge_done = 0;
+        const int rm = ensure_smem_attr(reinterpret_cast<const void *>(q4_merge_kernel<D>), 0, &merge_done);
+        return rm ? rm : launch_pdl(q4_merge_kernel<D>, dim3((unsigned)p.shares), dim3(kQ4MergeThreads), 0, stream, p);
+    }
     return p.list.np > 1 && !p.list.cluster ? launch_list_merge<D>(p.list, stream) : PKV_OK;
 }
 
@@ -64,15 +115,12 @@ extern "C" {
 size_t pkv_paged_attention_q4_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
                                               int max_context_len, int partition_size)
 {
-    if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || block_size > 32 ||
-        max_context_len <= 0 || partition_size < 0 || partition_size % block_size)
+    if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_dim <= 0 ||
+        block_size <= 0 || block_size > 32 || max_context_len < 0 || partition_size < 0 || partition_size % kQ4Unit)
         return 0;
-    const ListCut cut = list_cut((long long)num_seqs * num_kv_heads, ((long long)max_context_len + block_size - 1) / block_size,
-                                 block_size, partition_size);
-    if (cut.np <= 1 || cut.cluster)
-        return 0;
-    ListLayout lay;
-    return list_layout(num_seqs, num_heads, cut.np, head_dim, &lay) ? lay.total : 0;
+    Q4Layout lay;
+    const Q4Cut cut = q4_cut((long long)num_seqs * num_kv_heads, max_context_len, block_size, partition_size);
+    return q4_layout(cut, num_seqs, num_heads, num_kv_heads, head_dim, &lay) ? lay.total : 0;
 }
 
 int pkv_paged_attention_decode_q4(void *out, int out_dtype, const void *q, int64_t q_stride, int q_dtype,
@@ -106,21 +154,21 @@ int pkv_paged_attention_decode_q4(void *out, int out_dtype, const void *q, int64
         !aligned(block_tables, 4) || !aligned(context_lens, 4))
         return PKV_EINVAL;
 
-    const long long blocks = max_context_len > 0 ? ((long long)max_context_len + block_size - 1) / block_size : 1;
-    const ListCut cut = list_cut((long long)num_seqs * num_kv_heads, blocks, block_size, partition_size);
-    if (cut.part > kListCap && blocks > kListCap)
-        return PKV_EUNSUPPORTED;
+    const Q4Cut cut = q4_cut((long long)num_seqs * num_kv_heads, max_context_len, block_size, partition_size);
     Q4Params p = {};
     ListParams &l = p.list;
-    if (cut.np > 1 && !cut.cluster) {
-        ListLayout lay;
-        if (!list_layout(num_seqs, num_heads, cut.np, head_dim, &lay))
-            return PKV_EUNSUPPORTED;
+    Q4Layout lay;
+    if (!q4_layout(cut, num_seqs, num_heads, num_kv_heads, head_dim, &lay))
+        return PKV_EUNSUPPORTED;
+    if (lay.total) {
         if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 16))
             return PKV_EWORKSPACE;
         l.ws_ml = static_cast<float *>(workspace);
-        l.ws_acc = reinterpret_cast<float *>(static_cast<char *>(workspace) + lay.acc_off);
+        l.ws_acc = reinterpret_cast<float *>(static_cast<char *>(workspace) + lay.list.acc_off);
+        p.ws_share = reinterpret_cast<Q4Share *>(static_cast<char *>(workspace) + lay.share_off);
     }
+    p.shares = cut.shares;
+    p.part_units = cut.part_units;
     l.out = out;
     l.q = q;
     l.k_cache = static_cast<const uint8_t *>(k_cache);
@@ -134,9 +182,8 @@ int pkv_paged_attention_decode_q4(void *out, int out_dtype, const void *q, int64
     l.group = num_heads / num_kv_heads;
     l.max_blocks_per_seq = max_blocks_per_seq;
     l.max_context_len = max_context_len;
-    l.part_blocks = cut.part;
-    l.np = cut.np;
-    l.cluster = cut.cluster;
+    l.np = cut.list.np;
+    l.cluster = cut.list.cluster;
     l.out_dtype = out_dtype;
     l.q_dtype = q_dtype;
     l.qscale = scale * 1.4426950408889634f;

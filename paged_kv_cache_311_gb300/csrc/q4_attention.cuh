@@ -7,13 +7,17 @@
 // so that the products take whole numbers, and scales and minima join them in
 // fp32.
 //
-// The frame is that of list_attention.cuh: one CTA per (partition of the
-// context, kv head, sequence) with the kv head's G <= 8 query heads, partitions
-// merged by a cluster or through the workspace.  Each of four warps streams
-// records (bulk copies, one per block, codes with their scales) through a ring
-// of its own, 32 tokens at a time, and takes them in two tiles of 16 tokens: a tile's tokens are M of
-// S^T = K q^T, its dimensions M of O^T += V^T W^T, the query heads N of
-// warp-level MMAs (m16n8k16).
+// A CTA owns the G <= 8 query heads of a kv head.  Its four warps take the
+// tokens of a row (a sequence's kv head) 32 at a time in turn, each through a
+// ring of bulk copies of its own (one per block: codes with their scales), and
+// work on two tiles of 16: a tile's tokens are M of S^T = K q^T, its dimensions
+// M of O^T += V^T W^T, the query heads N of warp-level MMAs (m16n8k16).
+//
+// How the work is cut.  Either a CTA per row or per partition of one (merged by
+// a cluster or through the workspace, as in list_attention.cuh); or, "streamed",
+// as many CTAs as fit on the GPU at once, each of which takes an equal share of
+// all rows' tokens put one behind another.  A share's first and last row may be
+// parts, which q4_merge_kernel joins.  The rings run on over the rows' ends.
 //
 // Codes become f16 matrix fragments without a conversion: a word's nibbles
 // masked in place are numbers, two at a time.  u in a half's lowest four bits is
@@ -38,11 +42,26 @@
 
 namespace pkv {
 
+// Where a streamed CTA's share lies: units [lo, hi) of the stream, of which the
+// first is unit `unit` of the `units` of kv head `head` of sequence `seq`.
+struct Q4Share {
+    int64_t lo, hi;
+    int seq, head, unit, units;
+};
+
 struct Q4Params {
     ListParams list;             // without selected blocks and scales
     int64_t q_stride;            // elements between two sequences' rows of q
+    int shares;                  // streamed: CTAs; else 0
+    int part_units;              // tokens / 32 of a partition; 0: a row's, divided by list.np
+    Q4Share *ws_share;           // streamed: the shares, for the merge
 };
 
+constexpr int kQ4Unit = 32;      // tokens that a warp takes at a time
+// What a row's start and end cost a CTA, in units: shares are of equal cost.
+// (64 sequences of 128 to 2048 tokens, 32 kv heads: 90 us; with 4 units 100,
+// with none 119.)
+constexpr int kQ4RowCost = 8;
 constexpr int kQ4Ring = 57344;   // ring bytes of a CTA at most
 constexpr int kQ4Ctas = 3;       // CTAs per SM
 
@@ -50,27 +69,128 @@ template <int D, int BS> struct Q4Cfg {
     using R = Q4Row<D>;
     static constexpr int TILE = 16, TILES = 2;
     static constexpr int REC = R::template record<BS>;
-    static constexpr int TOK = TILES * TILE;                   // tokens of a stage
+    static constexpr int TOK = kQ4Unit;                        // tokens of a stage
     static constexpr int RECS = TOK / BS;
     // from a tile's codes and pairs to the next's
     static constexpr int NEXT_CODE = BS > TILE ? TILE * R::CODES : TILE / BS * REC;
     static constexpr int NEXT_PAIR = BS > TILE ? TILE * R::PAIRS : TILE / BS * REC;
     static constexpr int STAGE_BYTES = 2 * RECS * REC;
-    static constexpr int S0 = kQ4Ring / (kListWarps * STAGE_BYTES);
-    static constexpr int S = S0 < 2 ? 2 : S0;
-    static constexpr int AWS = D + 4;                          // row stride of the merge scratch, in floats
+    static constexpr int S = kQ4Ring / (kListWarps * STAGE_BYTES);
+    static constexpr int CHUNK = 128;                          // units whose blocks are looked up at a time
+    static constexpr int AWS = D + 4;                          // row stride of a warp's result, in floats
 
-    static constexpr int RING = (kListWarps * S * STAGE_BYTES + 127) / 128 * 128;
-    // the warps' results and the CTA's, in the rings' memory once they are done with
-    static constexpr int OFF_RESULT = kListWarps * kListMaxGroup * (AWS + 2) * 4;
-    static constexpr int RESULT_END = OFF_RESULT + kListMaxGroup * (D + 2) * 4;
-    static constexpr int OFF_PHYS = RING > RESULT_END ? RING : RESULT_END;
-    static constexpr int OFF_AT = OFF_PHYS + kListCap * 4;
-    static constexpr int OFF_BAR = OFF_AT + kListCap * 8;
+    static constexpr int OFF_AT = (kListWarps * S * STAGE_BYTES + 127) / 128 * 128;
+    // a warp's scales and minima of K in fp32 (and as many of V): all tokens' of
+    // the first group, then of the second
+    static constexpr int NUMBERS = R::GROUPS * TOK * 16;
+    static constexpr int OFF_NUM = OFF_AT + CHUNK * RECS * 8;
+    static constexpr int OFF_RESULT = OFF_NUM + kListWarps * 2 * NUMBERS;
+    static constexpr int OFF_ML = OFF_RESULT + kListMaxGroup * (D + 2) * 4;
+    static constexpr int OFF_BAD = OFF_ML + kListWarps * kListMaxGroup * 8;
+    static constexpr int OFF_BAR = OFF_BAD + CHUNK;
     static constexpr int OFF_FLAG = OFF_BAR + kListWarps * S * 8;
-    static constexpr int SMEM_BYTES = OFF_FLAG + 32 + 1024;    // slack for the alignment to 1024
-    static_assert(REC % 16 == 0 && OFF_RESULT % 16 == 0 && OFF_PHYS % 16 == 0, "alignment");
+    static constexpr int SMEM_BYTES = OFF_FLAG + 128 + 1024;   // slack for the alignment to 1024
+    static_assert(REC % 16 == 0 && STAGE_BYTES % 16 == 0 && OFF_RESULT % 16 == 0 && OFF_BAR % 8 == 0 && S >= 2, "alignment");
+    static_assert(kListMaxGroup * AWS * 4 <= STAGE_BYTES, "a warp's result fits the stage it took last");
 };
+
+// Units of a sequence; one of a refused length has none.
+__device__ __forceinline__ int q4_units(const ListParams &p, int seq)
+{
+    const int L = p.context_lens[seq];
+    return L < 0 || L > p.max_context_len ? 0 : (int)(((int64_t)L + kQ4Unit - 1) / kQ4Unit);
+}
+
+// Share i's place, by all threads of a CTA.  The stream is cut by cost, a row
+// costing its units and kQ4RowCost in front of them, at i / shares of the whole.
+// Each thread adds up a run of sequences; the runs that hold the share's two
+// ends are walked by their threads.
+__device__ __forceinline__ void q4_find_share(const ListParams &p, int shares, int i, Q4Share *share, int64_t *sums)
+{
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int run = (p.num_seqs + kListThreads - 1) / kListThreads;
+    const int s0 = min(p.num_seqs, t * run), s1 = min(p.num_seqs, s0 + run);
+    const int64_t Hk = p.num_kv_heads;
+    int64_t mine[2] = {0, 0};   // units of a head, cost of a head
+    for (int s = s0; s < s1; ++s) {
+        const int n = q4_units(p, s);
+        mine[0] += n;
+        mine[1] += n ? n + kQ4RowCost : 0;
+    }
+    int64_t upto[2] = {mine[0], mine[1]}, total = 0;
+#pragma unroll
+    for (int k = 1; k < 32; k *= 2) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const int64_t other = __shfl_up_sync(0xffffffffu, upto[w], k);
+            upto[w] += lane >= k ? other : 0;
+        }
+    }
+    if (lane == 31) {
+        sums[2 * warp] = upto[0];
+        sums[2 * warp + 1] = upto[1];
+    }
+    if (t == 0)
+        *share = Q4Share{};
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kListWarps; ++w) {
+        upto[0] += w < warp ? sums[2 * w] : 0;
+        upto[1] += w < warp ? sums[2 * w + 1] : 0;
+        total += sums[2 * w + 1];
+    }
+    total *= Hk;
+    int64_t each;
+    uint32_t rest;
+    if (total >> 32 == 0) {
+        each = (uint32_t)total / (uint32_t)shares;
+        rest = (uint32_t)total % (uint32_t)shares;
+    } else {
+        each = total / shares;
+        rest = (uint32_t)(total % shares);
+    }
+#pragma unroll 1
+    for (int end = 0; end < 2; ++end) {
+        const int64_t at = each * (i + end) + rest * (uint32_t)(i + end) / (uint32_t)shares;
+        int64_t cost = (upto[1] - mine[1]) * Hk, units = (upto[0] - mine[0]) * Hk;
+        if (cost <= at && at < upto[1] * Hk) {
+            int s = s0, n = q4_units(p, s);
+            for (int64_t c; at >= cost + (c = n ? (n + kQ4RowCost) * Hk : 0); n = q4_units(p, ++s)) {
+                cost += c;
+                units += n * Hk;
+            }
+            int head = 0;
+            for (int step = 1 << 15; step; step /= 2)   // (at - cost) / (n + kQ4RowCost), below 2^16
+                head += at - cost >= (int64_t)(head + step) * (n + kQ4RowCost) ? step : 0;
+            const int unit = max(0, (int)(at - cost - (int64_t)head * (n + kQ4RowCost)) - kQ4RowCost);
+            units += (int64_t)head * n + unit;
+            if (end == 0) {
+                share->seq = s;
+                share->head = head;
+                share->unit = unit;
+                share->units = n;
+                share->lo = units;
+            } else {
+                share->hi = units;
+            }
+        } else if (at == total && t == kListThreads - 1) {
+            share->hi = upto[0] * Hk;
+            if (end == 0)   // an empty stream
+                share->lo = upto[0] * Hk;
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+
+// D = A * B, m16n8k16, f16.
+__device__ __forceinline__ void q4_mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 
 // One warp's state.  Lane (g, c) = (lane / 4, lane % 4).
 template <typename T, int D, int BS> struct Q4Engine {
@@ -82,13 +202,15 @@ template <typename T, int D, int BS> struct Q4Engine {
     static constexpr float kLeast = 0x1p-100f;   // smaller scales count as this: weights stay below 2^115
 
     uint32_t qf[NG][4][2];   // q^T B-fragments of head g: group, step
-    float fs[2];             // heads 2c, 2c + 1: score of s (q . u)
-    float fm[NG][2];         //                   score of m
+    // a float2 is of heads 2c, 2c + 1
+    float2 fs;               // the softmax's factor, with the powers of two of q and u
+    float2 fm[NG];           // sum(q_j), in the same units as q . u
     float o[NG][4][4];       // O^T C-fragments: group, m-tile
-    float om[NG][2];         // this lane's tokens' sums of w m
-    float m[2], lsum[2];     // heads 2c, 2c + 1: weights' reference and sum
-    int kcode[2], kpair[2];  // byte offsets of this lane's tokens of K in a stage's records
-    int vcode[4];            // and of V
+    float2 om[NG];           // this lane's tokens' sums of w m
+    float2 m, lsum;          // weights' reference and sum
+    uint32_t nums;           // this warp's numbers in shared memory
+    int kcode[2], vcode[4];  // byte offsets of this lane's tokens of K and of V in a stage's records
+    int mine;                // of the pairs of the token that this lane makes numbers of
     int g, c;
 
     // Offset of the record of tile row t in a stage, and the row in it.
@@ -103,20 +225,21 @@ template <typename T, int D, int BS> struct Q4Engine {
         for (int i = 0; i < 2; ++i) {
             const int t = 4 * (g >> 1) + (g & 1) + 2 * i;
             kcode[i] = rec_of(t) + R::word(t % BS, NG * 2 * c);
-            kpair[i] = rec_of(t) + R::template pair<BS>(t % BS, 0);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = 4 * c + i;
             vcode[i] = rec_of(t) + R::word(t % BS, NG * g);
         }
+        mine = lane / BS * C::REC + R::template pair<BS>(lane % BS, 0);
         // q: dimensions 64 j + 16 c .. + 15 of head g, brought to f16 by a
         // power of two that puts the head's largest magnitude in [2^14, 2^15):
         // what f16 cannot hold is below 2^-35 of it
         const bool live = g < p.group;
         const T *qp = static_cast<const T *>(p.q) + (int64_t)seq * a.q_stride + (kvh * p.group + (live ? g : 0)) * D + 16 * c;
+        using V = typename Pair16<T>::V;
         uint32_t w[NG][8];
-        float big = 0.f;
+        V top = as_pair<T>(0u);
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
 #pragma unroll
@@ -128,13 +251,13 @@ template <typename T, int D, int BS> struct Q4Engine {
                 w[j][4 * i + 3] = v.w;
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 f = Unpack<T>::pair(w[j][i] & 0x7fff7fffu);
-                big = fmaxf(big, fmaxf(f.x, f.y));
-            }
+            for (int i = 0; i < 8; ++i)
+                top = __hmax2(top, __habs2(as_pair<T>(w[j][i])));   // NaN loses
         }
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        top = __hmax2(top, as_pair<T>(__shfl_xor_sync(0xffffffffu, as_word(top), 1)));
+        top = __hmax2(top, as_pair<T>(__shfl_xor_sync(0xffffffffu, as_word(top), 2)));
+        const float2 both = Unpack<T>::pair(as_word(top));
+        const float big = fmaxf(both.x, both.y);
         int x = (int)(__float_as_uint(big) >> 23) - 127 - 14;
         x = big < INFINITY ? max(x, -100) : 0;
         const float down = __uint_as_float((uint32_t)(127 - x) << 23);
@@ -142,42 +265,36 @@ template <typename T, int D, int BS> struct Q4Engine {
         float sum[NG];
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
-            sum[j] = 0.f;
+            float2 total = make_float2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float f[8];
+                float2 f[4];   // dimensions 2 i, 2 i + 1 of a word's eight
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 v = Unpack<T>::pair(w[j][4 * e + i]);
-                    f[2 * i] = v.x * down;
-                    f[2 * i + 1] = v.y * down;
+                    f[i] = fmul2(Unpack<T>::pair(w[j][4 * e + i]), make_float2(down, down));
+                    total = fadd2(total, f[i]);
                 }
                 // a word's pairs (n, n + 4), of which odd n come times 16
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const float up = n & 1 ? 0.0625f : 1.f;
-                    const uint32_t h = Mma<__half>::pack(f[n] * up, f[n + 4] * up);
-                    qf[j][2 * e + (n >> 1)][n & 1] = h;
-                    const float2 back = Unpack<__half>::pair(h);
-                    sum[j] += (back.x + back.y) / up;
+                for (int i = 0; i < 2; ++i) {
+                    qf[j][2 * e + i][0] = Mma<__half>::pack(f[i].x, f[i + 2].x);
+                    qf[j][2 * e + i][1] = Mma<__half>::pack(f[i].y * 0.0625f, f[i + 2].y * 0.0625f);
                 }
             }
+            sum[j] = total.x + total.y;
             sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
             sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
         }
         // head h's sits in lanes 4 h ..
+        auto heads = [&](float v) { return make_float2(__shfl_sync(0xffffffffu, v, 8 * c), __shfl_sync(0xffffffffu, v, 8 * c + 4)); };
+        fs = heads(factor * 16777216.f);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float f = __shfl_sync(0xffffffffu, factor, 8 * c + 4 * i);
-            fs[i] = f * 16777216.f;
-            m[i] = -INFINITY;
-            lsum[i] = 0.f;
-#pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                fm[j][i] = f * __shfl_sync(0xffffffffu, sum[j], 8 * c + 4 * i);
-                om[j][i] = 0.f;
-            }
+        for (int j = 0; j < NG; ++j) {
+            fm[j] = heads(sum[j] * 0x1p-24f);
+            om[j] = make_float2(0.f, 0.f);
         }
+        m = make_float2(-INFINITY, -INFINITY);
+        lsum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
 #pragma unroll
@@ -186,52 +303,218 @@ template <typename T, int D, int BS> struct Q4Engine {
         }
     }
 
-    // (scale, minimum) of each group of a row, from shared memory.
-    __device__ __forceinline__ static void pairs(uint32_t at, float (&s)[NG], float (&mn)[NG])
+    // Scales and minima of a step's tokens in fp32, each twice (the factors of
+    // two heads), where the warp's lanes find them: a lane makes a token's.
+    //  Returns the largest scale of V among all tokens, at least kLeast,
+    // with the minima that hold the weights down, too: those of a size that makes
+    // the scales' part of the numbers one below fp32's last bit.
+    __device__ __forceinline__ float numbers(uint32_t kbase, uint32_t vbase, int nvalid) const
     {
-        if constexpr (NG == 2) {
-            const uint2 v = lds64(at);
-            const float2 a = Unpack<T>::pair(v.x), b = Unpack<T>::pair(v.y);
-            s[0] = a.x;
-            mn[0] = a.y;
-            s[1] = b.x;
-            mn[1] = b.y;
-        } else {
-            const float2 a = Unpack<T>::pair(lds32(at));
-            s[0] = a.x;
-            mn[0] = a.y;
+        float top = kLeast;
+        const int lane = 4 * g + c;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                float2 f = Unpack<T>::pair(lds32((v ? vbase : kbase) + mine + 4 * j));
+                if (lane >= nvalid)
+                    f = make_float2(0.f, 0.f);   // no token: what is there may be anything
+                if (v)
+                    top = fmaxf(top, fmaxf(f.x, fabsf(f.y) * 0x1p-24f));
+                asm volatile("st.shared.v4.f32 [%0], {%1, %1, %2, %2};" ::"r"(nums + v * C::NUMBERS + (j * C::TOK + lane) * 16), "f"(f.x), "f"(f.y) : "memory");
+            }
         }
+        return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
     }
 
-    // S^T of a tile.
-    __device__ __forceinline__ void scores(uint32_t kbase, int tile, float (&acc)[NG][4]) const
+    // This lane holds tokens t0 = 4 (g / 2) + g % 2 and t0 + 2 of each tile.
+    static constexpr int N = 2 * C::TILES;
+    __device__ __forceinline__ int token(int n) const { return 4 * (g >> 1) + (g & 1) + 2 * (n & 1) + C::TILE * (n >> 1); }
+    // (s, s), (m, m) of token n, group j: K's (v = 0) or V's
+    __device__ __forceinline__ void number(int v, int j, int n, float2 &s, float2 &mn) const
     {
-        uint32_t w[2][2 * NG];   // token, word
+        const float4 f = lds128f(nums + v * C::NUMBERS + j * C::TOK * 16 + token(n) * 16);
+        s = make_float2(f.x, f.y);
+        mn = make_float2(f.z, f.w);
+    }
+
+    // Scores of the step whose records start at kbase, up to fs.  Products that
+    // add to the same sums stand apart: their latency is four others' time.
+    __device__ __forceinline__ void scores(uint32_t kbase, float2 (&x)[N]) const
+    {
+        uint32_t w[N][2 * NG];   // token, word
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t at = kbase + kcode[i] + tile * C::NEXT_CODE;
+        for (int n = 0; n < N; ++n) {
+            const uint32_t at = kbase + kcode[n & 1] + (n >> 1) * C::NEXT_CODE;
             if constexpr (NG == 2) {
                 const uint4 v = lds128(at);
-                w[i][0] = v.x;
-                w[i][1] = v.y;
-                w[i][2] = v.z;
-                w[i][3] = v.w;
+                w[n][0] = v.x;
+                w[n][1] = v.y;
+                w[n][2] = v.z;
+                w[n][3] = v.w;
             } else {
                 const uint2 v = lds64(at);
-                w[i][0] = v.x;
-                w[i][1] = v.y;
+                w[n][0] = v.x;
+                w[n][1] = v.y;
+            }
+        }
+        float acc[C::TILES][NG][4];
+#pragma unroll
+        for (int step = 0; step < 4; ++step) {
+#pragma unroll
+            for (int tile = 0; tile < C::TILES; ++tile) {
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    const int word = NG * (step >> 1) + j;
+                    uint32_t u = w[2 * tile][word], v = w[2 * tile + 1][word];
+                    if (step & 1) {
+                        u >>= 8;
+                        v >>= 8;
+                    }
+                    const uint32_t a[4] = {u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u};
+                    if (step == 0)
+                        q4_mma_first(acc[tile][j], a, qf[j][0][0], qf[j][0][1]);
+                    else
+                        Mma<__half>::run(acc[tile][j], a, qf[j][step][0], qf[j][step][1]);
+                }
             }
         }
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
-            acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t u = w[0][NG * e + j], v = w[1][NG * e + j];
-                const uint32_t a0[4] = {u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u};
-                Mma<__half>::run(acc[j], a0, qf[j][2 * e][0], qf[j][2 * e][1]);
-                const uint32_t a1[4] = {(u >> 8) & 0x000f000fu, (v >> 8) & 0x000f000fu, (u >> 8) & 0x00f000f0u, (v >> 8) & 0x00f000f0u};
-                Mma<__half>::run(acc[j], a1, qf[j][2 * e + 1][0], qf[j][2 * e + 1][1]);
+            for (int n = 0; n < N; ++n) {
+                float2 s, mn;
+                number(0, j, n, s, mn);
+                const float2 d = make_float2(acc[n >> 1][j][2 * (n & 1)], acc[n >> 1][j][2 * (n & 1) + 1]);
+                x[n] = j ? ffma2(s, d, x[n]) : fmul2(s, d);
+                x[n] = ffma2(mn, fm[j], x[n]);
+            }
+        }
+    }
+
+    // Weights of a step from its scores.  Online softmax in the log2 domain:
+    // while no weight times a scale can pass kMost, weights are taken against
+    // the head's reference m unchanged: no maximum across lanes, no rescaling.
+    __device__ __forceinline__ void weights(const float2 (&x)[N], float top, int nvalid, float2 (&p)[N])
+    {
+        float most = 0.f;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const float2 z = ffma2(x[n], fs, make_float2(-m.x, -m.y));   // infinite before the first token
+            p[n] = make_float2(ex2_fast(z.x), ex2_fast(z.y));
+        }
+        if (nvalid < C::TOK) {
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                if (token(n) >= nvalid)
+                    p[n] = make_float2(0.f, 0.f);
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            most = fmaxf(most, fmaxf(p[n].x, p[n].y));
+        if (!__any_sync(0xffffffffu, most * top > kMost))
+            return;
+        float2 t = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            float big = kLeast;
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                float2 s, mn;
+                number(1, j, n, s, mn);
+                big = fmaxf(big, fmaxf(s.x, fabsf(mn.x) * 0x1p-24f));
+            }
+            big = __log2f(big) - kLift;
+            if (token(n) < nvalid) {
+                t.x = fmaxf(t.x, fmaf(x[n].x, fs.x, big));
+                t.y = fmaxf(t.y, fmaf(x[n].y, fs.y, big));
+            }
+        }
+#pragma unroll
+        for (int k = 4; k < 32; k *= 2) {
+            t.x = fmaxf(t.x, __shfl_xor_sync(0xffffffffu, t.x, k));
+            t.y = fmaxf(t.y, __shfl_xor_sync(0xffffffffu, t.y, k));
+        }
+        t = make_float2(fmaxf(m.x, t.x), fmaxf(m.y, t.y));
+        const float2 ref = make_float2(reference_of(t.x), reference_of(t.y));
+        const float2 alpha = make_float2(ex2_fast(m.x - ref.x), ex2_fast(m.y - ref.y));
+        m = t;
+        lsum = fmul2(lsum, alpha);
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            om[j] = fmul2(om[j], alpha);
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+                o[j][mt][0] *= alpha.x;
+                o[j][mt][1] *= alpha.y;
+                o[j][mt][2] *= alpha.x;
+                o[j][mt][3] *= alpha.y;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const bool live = token(n) < nvalid;
+            p[n].x = live ? ex2_fast(fmaf(x[n].x, fs.x, -ref.x)) : 0.f;
+            p[n].y = live ? ex2_fast(fmaf(x[n].y, fs.y, -ref.y)) : 0.f;
+        }
+    }
+
+    // The weights' sums, their products with the minima in fp32, and with the
+    // codes of a tile of the step whose records start at vbase.
+    __device__ __forceinline__ void value_tile(uint32_t vbase, int tile, const float2 (&p)[N])
+    {
+        uint32_t hi[NG][2], lo[NG][2];   // weights times scales in two f16 parts, as B-fragments
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int n = 2 * tile + i;
+            lsum = fadd2(lsum, p[n]);
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                float2 s, mn;
+                number(1, j, n, s, mn);
+                om[j] = ffma2(p[n], mn, om[j]);
+                const float2 w = fmul2(p[n], s);
+                const uint32_t h = Mma<__half>::pack(w.x, w.y);
+                const float2 f = Unpack<__half>::pair(h);
+                const float2 rest = fadd2(w, make_float2(-f.x, -f.y));
+                hi[j][i] = movmatrix_trans(h);
+                lo[j][i] = movmatrix_trans(Mma<__half>::pack(rest.x, rest.y));
+            }
+        }
+        uint32_t w[4][NG];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t at = vbase + vcode[i] + tile * C::NEXT_CODE;
+            if constexpr (NG == 2) {
+                const uint2 v = lds64(at);
+                w[i][0] = v.x;
+                w[i][1] = v.y;
+            } else {
+                w[i][0] = lds32(at);
+            }
+        }
+        // four m-tiles at a time, so that the two parts' products, which add to
+        // the same sums, stand apart
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+            uint32_t a[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = NG == 2 ? i >> 1 : 0, e = NG == 2 ? q : i >> 1, k = i & 1;
+                const uint32_t u = __byte_perm(w[0][j], w[1][j], e ? 0x7632 : 0x5410) >> (8 * k);
+                const uint32_t v = __byte_perm(w[2][j], w[3][j], e ? 0x7632 : 0x5410) >> (8 * k);
+                a[i][0] = u & 0x000f000fu;
+                a[i][1] = u & 0x00f000f0u;
+                a[i][2] = v & 0x000f000fu;
+                a[i][3] = v & 0x00f000f0u;
+            }
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = NG == 2 ? i >> 1 : 0, e = NG == 2 ? q : i >> 1, k = i & 1;
+                    Mma<__half>::run(o[j][2 * e + k], a[i], part ? lo[j][0] : hi[j][0], part ? lo[j][1] : hi[j][1]);
+                }
             }
         }
     }
@@ -240,175 +523,60 @@ template <typename T, int D, int BS> struct Q4Engine {
     // nvalid of them count.
     __device__ __forceinline__ void step(uint32_t kbase, uint32_t vbase, int nvalid)
     {
-        // Online softmax in the log2 domain; this lane holds tokens t0 = 4 (g /
-        // 2) + g % 2 and t0 + 2 of each tile, heads 2c, 2c + 1.  While no weight
-        // times its scale passes kMost, weights are taken against the head's
-        // reference m unchanged: no maximum across lanes, no rescaling.
-        constexpr int N = 2 * C::TILES;          // this lane's tokens
-        const int t0 = 4 * (g >> 1) + (g & 1);
-        float x[N][2], p[N][2], s[N][NG], mn[N][NG], top[N];
-        bool over = false;
+        const float top = numbers(kbase, vbase, nvalid);
+        __syncwarp();
+        float2 x[N], p[N];
+        scores(kbase, x);
+        weights(x, top, nvalid, p);
 #pragma unroll
-        for (int tile = 0; tile < C::TILES; ++tile) {
-            float acc[NG][4];
-            scores(kbase, tile, acc);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int n = 2 * tile + i;
-                pairs(kbase + kpair[i] + tile * C::NEXT_PAIR, s[n], mn[n]);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float dot = s[n][0] * acc[0][2 * i + h], low = mn[n][0] * fm[0][h];
-                    if constexpr (NG == 2) {
-                        dot = fmaf(s[n][1], acc[1][2 * i + h], dot);
-                        low = fmaf(mn[n][1], fm[1][h], low);
-                    }
-                    x[n][h] = fmaf(fs[h], dot, low);
-                }
-                pairs(vbase + kpair[i] + tile * C::NEXT_PAIR, s[n], mn[n]);
-            }
-        }
-        if (nvalid < C::TOK) {
-            // no token: what is there may be anything
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                if (t0 + 2 * (n & 1) + C::TILE * (n >> 1) >= nvalid) {
-                    x[n][0] = x[n][1] = -INFINITY;
-#pragma unroll
-                    for (int j = 0; j < NG; ++j)
-                        s[n][j] = mn[n][j] = 0.f;
-                }
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            // minima of a size that makes the scales' part of the numbers one
-            // below fp32's last bit hold the weights down, too
-            top[n] = NG == 2 ? fmaxf(fmaxf(s[n][0], s[n][NG - 1]), 0x1p-24f * fmaxf(fabsf(mn[n][0]), fabsf(mn[n][NG - 1])))
-                             : fmaxf(s[n][0], 0x1p-24f * fabsf(mn[n][0]));
-            top[n] = fmaxf(top[n], kLeast);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                p[n][h] = ex2_fast(x[n][h] - m[h]);   // infinite before the first token
-                over |= p[n][h] * top[n] > kMost;
-            }
-        }
-        if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float t = -INFINITY;
-#pragma unroll
-                for (int n = 0; n < N; ++n)
-                    t = fmaxf(t, x[n][h] + __log2f(top[n]) - kLift);
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                t = fmaxf(m[h], t);
-                const float ref = reference_of(t), alpha = ex2_fast(m[h] - ref);
-                m[h] = t;
-                lsum[h] *= alpha;
-#pragma unroll
-                for (int j = 0; j < NG; ++j) {
-                    om[j][h] *= alpha;
-#pragma unroll
-                    for (int mt = 0; mt < 4; ++mt) {
-                        o[j][mt][h] *= alpha;
-                        o[j][mt][2 + h] *= alpha;
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < N; ++n)
-                    p[n][h] = ex2_fast(x[n][h] - ref);
-            }
-        }
-
-        // The weights' sums, their products with the minima in fp32, and with
-        // the scales in two f16 parts each, as B-fragments.
-#pragma unroll
-        for (int tile = 0; tile < C::TILES; ++tile) {
-            uint32_t hi[NG][2], lo[NG][2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int n = 2 * tile + i;
-                lsum[0] += p[n][0];
-                lsum[1] += p[n][1];
-#pragma unroll
-                for (int j = 0; j < NG; ++j) {
-                    om[j][0] = fmaf(p[n][0], mn[n][j], om[j][0]);
-                    om[j][1] = fmaf(p[n][1], mn[n][j], om[j][1]);
-                    const float a = p[n][0] * s[n][j], b = p[n][1] * s[n][j];
-                    const uint32_t h = Mma<__half>::pack(a, b);
-                    const float2 f = Unpack<__half>::pair(h);
-                    hi[j][i] = movmatrix_trans(h);
-                    lo[j][i] = movmatrix_trans(Mma<__half>::pack(a - f.x, b - f.y));
-                }
-            }
-            uint32_t w[4][NG];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t at = vbase + vcode[i] + tile * C::NEXT_CODE;
-                if constexpr (NG == 2) {
-                    const uint2 v = lds64(at);
-                    w[i][0] = v.x;
-                    w[i][1] = v.y;
-                } else {
-                    w[i][0] = lds32(at);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < NG; ++j) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t u = __byte_perm(w[0][j], w[1][j], e ? 0x7632 : 0x5410);
-                    const uint32_t v = __byte_perm(w[2][j], w[3][j], e ? 0x7632 : 0x5410);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t a[4] = {(u >> (8 * k)) & 0x000f000fu, (u >> (8 * k)) & 0x00f000f0u,
-                                               (v >> (8 * k)) & 0x000f000fu, (v >> (8 * k)) & 0x00f000f0u};
-                        Mma<__half>::run(o[j][2 * e + k], a, hi[j][0], hi[j][1]);
-                        Mma<__half>::run(o[j][2 * e + k], a, lo[j][0], lo[j][1]);
-                    }
-                }
-            }
-        }
+        for (int tile = 0; tile < C::TILES; ++tile)
+            value_tile(vbase, tile, p);
     }
 
-    // This warp's (max, sum, sums of values) of the heads below `group` into
-    // the merge scratch.
-    __device__ __forceinline__ void finish(float *mw, float *lw, float *aw, int warp, int group)
+    // This warp's reference, sum and sums of values of the heads below `group`:
+    // ml [kListMaxGroup][2], aw [kListMaxGroup][AWS].
+    __device__ __forceinline__ void finish(float2 *ml, float *aw, int group)
     {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            float l = lsum[h], add[NG];
+            float l = h ? lsum.y : lsum.x, add[NG];
             l += __shfl_xor_sync(0xffffffffu, l, 4);
             l += __shfl_xor_sync(0xffffffffu, l, 8);
             l += __shfl_xor_sync(0xffffffffu, l, 16);
 #pragma unroll
             for (int j = 0; j < NG; ++j) {
-                add[j] = om[j][h];
+                add[j] = h ? om[j].y : om[j].x;
                 add[j] += __shfl_xor_sync(0xffffffffu, add[j], 4);
                 add[j] += __shfl_xor_sync(0xffffffffu, add[j], 8);
                 add[j] += __shfl_xor_sync(0xffffffffu, add[j], 16);
             }
             const int row = 2 * c + h;
             if (row < group) {
-                if (g == 0) {
-                    mw[warp * kListMaxGroup + row] = m[h];
-                    lw[warp * kListMaxGroup + row] = l;
-                }
-                float *dst = aw + (warp * kListMaxGroup + row) * C::AWS + 8 * g;
+                if (g == 0)
+                    ml[row] = make_float2(h ? m.y : m.x, l);
+                float *dst = aw + row * C::AWS + 8 * g;
 #pragma unroll
                 for (int j = 0; j < NG; ++j) {
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt)
-                        *reinterpret_cast<float2 *>(dst + 64 * j + 2 * mt) = make_float2(fmaf(o[j][mt][h], 16777216.f, add[j]), fmaf(o[j][mt][2 + h], 1048576.f, add[j]));
+                        *reinterpret_cast<float2 *>(dst + 64 * j + 2 * mt) =
+                            make_float2(fmaf(o[j][mt][h], 16777216.f, add[j]), fmaf(o[j][mt][2 + h], 1048576.f, add[j]));
                 }
             }
         }
     }
 };
 
-// Grid (partition, kv head, sequence).
+// Zero rows for the heads of every kv head of a sequence.
+template <int D>
+__device__ __forceinline__ void q4_zero_rows(const ListParams &p, int seq)
+{
+    const int64_t heads = (int64_t)p.num_kv_heads * p.group;
+    for (int64_t i = (int64_t)threadIdx.x * 4; i < heads * D; i += kListThreads * 4)
+        store_out4(p.out, p.out_dtype, seq * heads * D + i, make_float4(0.f, 0.f, 0.f, 0.f));
+}
+
+// Grid: streamed (shares); else (partition, kv head, sequence).
 template <typename T, int D, int BS>
 __global__ void __launch_bounds__(kListThreads, kQ4Ctas)
 q4_attention_kernel(const __grid_constant__ Q4Params a)
@@ -418,13 +586,15 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
     const ListParams &p = a.list;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = aligned_smem(smem_raw);
-    int32_t *phys = reinterpret_cast<int32_t *>(smem + C::OFF_PHYS);
-    int64_t *record = reinterpret_cast<int64_t *>(smem + C::OFF_AT);   // byte offsets of the partition's records
-    const int part = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
+    int64_t *record = reinterpret_cast<int64_t *>(smem + C::OFF_AT);   // byte offsets in a cache; -1: none
+    ListResult<D> *res = reinterpret_cast<ListResult<D> *>(smem + C::OFF_RESULT);
+    float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
+    uint8_t *bad_row = smem + C::OFF_BAD;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + warp * S;
     uint32_t *flag = reinterpret_cast<uint32_t *>(smem + C::OFF_FLAG);
-    int *warp_tokens = reinterpret_cast<int *>(smem + C::OFF_FLAG + 16);
+    Q4Share *share = reinterpret_cast<Q4Share *>(smem + C::OFF_FLAG + 8);
+    int64_t *sums = reinterpret_cast<int64_t *>(smem + C::OFF_FLAG + 64);
     if (lane == 0) {
         for (int s = 0; s < S; ++s)
             mbar_init(&bars[s], 1);
@@ -433,126 +603,348 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
     if (threadIdx.x == 0)
         *flag = 0;
     wait_for_stream();
-    const int L = p.context_lens[seq];
-    const int e0 = part * p.part_blocks;
-    ListEntries<BS> entries;
-    entries.load(p, seq, kvh, e0);
-    ListResult<D> *res = reinterpret_cast<ListResult<D> *>(smem + C::OFF_RESULT);
-    int tokens = 0;
-    if (L < 0 || L > p.max_context_len) {
-        if (part == 0 && kvh == 0 && threadIdx.x == 0)
-            report(p.status, PKV_DEV_BAD_CONTEXT_LEN);
-        tokens = -1;
-    } else if ((int64_t)e0 * BS < L) {
-        tokens = entries.resolve(p, phys, e0, L);
-        const int most = __reduce_max_sync(0xffffffffu, tokens);
-        if (lane == 0)
-            warp_tokens[warp] = most;
-        if (__syncthreads_or(tokens < 0)) {
-            if (threadIdx.x == 0)
-                report(p.status, PKV_DEV_BAD_BLOCK);
-            tokens = -1;
-        } else {
-#pragma unroll
-            for (int w = 0; w < NW; ++w)
-                tokens = max(tokens, warp_tokens[w]);
+
+    // ---- the share: `left` units from unit `unit` of row (seq, head) on
+    int seq, head, unit, L;
+    int64_t left;
+    if (a.shares) {
+        for (int s = blockIdx.x; s < p.num_seqs; s += a.shares) {
+            const int len = p.context_lens[s];
+            if (len <= 0 || len > p.max_context_len) {
+                q4_zero_rows<D>(p, s);
+                if (len != 0 && threadIdx.x == 0)
+                    report(p.status, PKV_DEV_BAD_CONTEXT_LEN);
+            }
+        }
+        q4_find_share(p, a.shares, blockIdx.x, share, sums);
+        if (threadIdx.x == 0)
+            a.ws_share[blockIdx.x] = *share;
+        left = share->hi - share->lo;
+        if (left == 0) {
+            if (threadIdx.x < p.group)   // its part of the row that it lies in
+                *reinterpret_cast<float2 *>(p.ws_ml + ((int64_t)blockIdx.x * 2 * p.group + threadIdx.x) * 2) = make_float2(-INFINITY, 0.f);
+            return;
+        }
+        seq = share->seq;
+        head = share->head;
+        unit = share->unit;
+        L = p.context_lens[seq];
+    } else {
+        seq = blockIdx.z;
+        head = blockIdx.y;
+        L = p.context_lens[seq];
+        const int n = q4_units(p, seq);
+        const int part = a.part_units ? a.part_units : (n + p.np - 1) / p.np;
+        unit = (int)min((int64_t)n, (int64_t)part * blockIdx.x);
+        left = min(part, n - unit);
+        if (left == 0) {
+            const bool refused = L < 0 || L > p.max_context_len;
+            if (refused && blockIdx.x == 0 && head == 0 && threadIdx.x == 0)
+                report(p.status, PKV_DEV_BAD_CONTEXT_LEN);
+            if (threadIdx.x < kListMaxGroup) {
+                res->m[threadIdx.x] = -INFINITY;
+                res->l[threadIdx.x] = refused ? -1.f : 0.f;
+            }
+            __syncthreads();
+            write_result<D>(p, res, seq, head, blockIdx.x);
+            return;
         }
     }
-    if (tokens <= 0) {
-        if (threadIdx.x < kListMaxGroup) {
-            res->m[threadIdx.x] = -INFINITY;
-            res->l[threadIdx.x] = tokens < 0 ? -1.f : 0.f;
+
+    auto units_of = [](int len) { return (int)(((int64_t)len + kQ4Unit - 1) / kQ4Unit); };
+    // the row behind (s, h): the next head, or the next sequence that has units
+    auto next_row = [&](int &s, int &h, int &len) {
+        if (++h < p.num_kv_heads)
+            return;
+        h = 0;
+        do
+            len = p.context_lens[++s];
+        while (len <= 0 || len > p.max_context_len);
+    };
+
+    uint8_t *stages = smem + warp * S * C::STAGE_BYTES;
+    int stage = 0;              // the one that this warp takes next
+    uint32_t phase = 0;         // its barrier's
+    bool dead = false;          // a wait gave up
+    bool refused = false;       // the row has a bad block
+    bool whole = unit == 0;     // the row starts here
+    int rows = 0;               // rows finished
+    bool fresh = true;          // the engine has nothing of the row yet
+    Q4Engine<T, D, BS> eng;
+    eng.nums = smem_u32(smem + C::OFF_NUM + warp * 2 * C::NUMBERS);
+
+    while (left > 0) {
+        // ---- the blocks of the next units; -1 behind a row's last
+        int chunk = (int)min(left, (int64_t)C::CHUNK);
+        for (int k = threadIdx.x; k < chunk; k += kListThreads)
+            bad_row[k] = 0;
+        __syncthreads();
+        {
+            int s = seq, h = head, u = unit, len = L, row = 0;
+            bool bad = false;
+            for (int at = 0; at < chunk; ++row) {
+                const int n = min(units_of(len) - u, chunk - at);
+                const int32_t *table = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
+                for (int k = threadIdx.x; k < n * C::RECS; k += kListThreads) {
+                    const int64_t b = (int64_t)u * C::RECS + k;
+                    int64_t where = -1;
+                    if (b * BS < len) {
+                        int id = table[b];
+                        if (id < 0 || (int64_t)id >= p.num_blocks) {
+                            bad = true;
+                            bad_row[row] = 1;
+                            id = 0;   // a block that there is, for a result that is dropped
+                        }
+                        where = ((int64_t)id * p.num_kv_heads + h) * C::REC;
+                    }
+                    record[at * C::RECS + k] = where;
+                }
+                u += n;
+                if (at + n < chunk) {
+                    u = 0;
+                    next_row(s, h, len);
+                } else {
+                    // a row that goes on in the next chunk leaves a unit for
+                    // every warp there (whose memory takes the warp's result)
+                    const int64_t rest = min((int64_t)(units_of(len) - u), left - chunk);
+                    if (rest > 0 && rest < NW) {
+                        chunk = at > 0 ? at : chunk - NW;
+                        break;
+                    }
+                }
+                at += n;
+            }
+            if (bad)
+                report(p.status, PKV_DEV_BAD_BLOCK);
         }
         __syncthreads();
-        write_result<D>(p, res, seq, kvh, part);
-        return;
-    }
 
-#pragma unroll 1
-    for (int k = threadIdx.x; k * BS < tokens; k += kListThreads)
-        record[k] = ((int64_t)phys[k] * p.num_kv_heads + kvh) * C::REC;
-    __syncthreads();
-
-    // ---- this warp's stages: warp, warp + NW, ...
-    const int nstages = (tokens + C::TOK - 1) / C::TOK;
-    const int my_n = warp < nstages ? (nstages - 1 - warp) / NW + 1 : 0;
-    uint8_t *stages = smem + warp * S * C::STAGE_BYTES;
-    auto issue = [&](int i, int st) {
-        const int t0 = (warp + i * NW) * C::TOK;
-        uint8_t *kd = stages + st * C::STAGE_BYTES, *vd = kd + C::RECS * C::REC;
-        const int n = min(C::RECS, (tokens - t0 + BS - 1) / BS);
-        mbar_arrive_expect_tx(&bars[st], (uint32_t)(n * 2 * C::REC));
-        for (int b = 0; b < n; ++b) {
-            const int64_t at = record[t0 / BS + b];
-            bulk_load(kd + b * C::REC, p.k_cache + at, C::REC, &bars[st]);
-            bulk_load(vd + b * C::REC, p.v_cache + at, C::REC, &bars[st]);
-        }
-    };
-    if (lane == 0) {
-        for (int i = 0; i < min(my_n, S); ++i)
-            issue(i, i);
-    }
-    Q4Engine<T, D, BS> eng;
-    eng.init(a, seq, kvh, lane);
-
-    int failed_at = -1;
-    for (int i = 0; i < my_n; ++i) {
-        const int st = i % S;
-        // the warp gives up as one: its products and shuffles need every lane
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[st], (uint32_t)((i / S) & 1)))) {
-            failed_at = i;
-            break;
-        }
-        const int t0 = (warp + i * NW) * C::TOK;
-        const uint32_t kbase = smem_u32(stages + st * C::STAGE_BYTES);
-        eng.step(kbase, kbase + C::RECS * C::REC, tokens - t0);
-        __syncwarp();
-        if (lane == 0 && i + S < my_n) {
+        // ---- this warp's units of the chunk: warp, warp + NW, ...
+        // unit k into a stage
+        auto issue = [&](int k, int stage) {
+            const uint8_t *const kc = p.k_cache, *const vc = p.v_cache;
+            uint8_t *kd = stages + stage * C::STAGE_BYTES;
+            uint64_t *bar = &bars[stage];
+            int64_t at[C::RECS];
+            int n = 0;
+#pragma unroll
+            for (int b = 0; b < C::RECS; ++b) {
+                const uint2 v = lds64(smem_u32(record + k * C::RECS + b));
+                at[b] = (int64_t)((uint64_t)v.y << 32 | v.x);
+                n += at[b] >= 0;
+            }
+            mbar_arrive_expect_tx(bar, (uint32_t)(n * 2 * C::REC));
+#pragma unroll
+            for (int b = 0; b < C::RECS; ++b) {
+                if (at[b] >= 0) {
+                    bulk_load(kd + b * C::REC, kc + at[b], C::REC, bar);
+                    bulk_load(kd + (C::RECS + b) * C::REC, vc + at[b], C::REC, bar);
+                }
+            }
+        };
+        if (lane == 0 && !dead) {
             fence_proxy_async_smem();
-            issue(i + S, st);
+            for (int i = 0; i < S && warp + i * NW < chunk; ++i)
+                issue(warp + i * NW, (stage + i) % S);
         }
-    }
-    if (failed_at >= 0) {
-        // no CTA leaves with loads in flight
-        for (int i = failed_at; i < min(my_n, failed_at + S); ++i)
-            drain_wait(&bars[i % S], (uint32_t)((i / S) & 1), p.status);
-        if (lane == 0) {
-            report(p.status, PKV_DEV_TIMEOUT);
-            atomicOr(flag, 1u);
-        }
-    }
+        int k = warp, row = 0;
+        for (int at = 0; at < chunk; ++row) {
+            const int n = min(units_of(L) - unit, chunk - at);
+            const bool row_ends = unit + n == units_of(L), flush = row_ends || left == n;
+            int held = -1, held_stage = 0;   // the unit whose stage takes this warp's result
+            if (fresh) {
+                eng.init(a, seq, head, lane);
+                fresh = false;
+            }
+            if (k < at + n) {
+                const int last = k + (at + n - 1 - k) / NW * NW;
+                // units from here on are not followed into their stages by others, or not before the result is out
+                const int stop = min(flush ? last : last + 1, chunk - S * NW);
+                int valid = (int)min((int64_t)INT32_MAX, L - (int64_t)(unit + k - at) * kQ4Unit);
+                for (; k <= last && !dead; k += NW) {
+                    // the warp gives up as one: its products and shuffles need every lane
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[stage], phase))) {
+                        // no CTA leaves with loads in flight
+                        for (int i = 0; i < S && k + i * NW < chunk; ++i)
+                            drain_wait(&bars[(stage + i) % S], phase ^ (stage + i >= S), lane == 0 ? p.status : nullptr);
+                        if (lane == 0) {
+                            report(p.status, PKV_DEV_TIMEOUT);
+                            atomicOr(flag, 1u);
+                        }
+                        dead = true;
+                    } else {
+                        const uint32_t kbase = smem_u32(stages + stage * C::STAGE_BYTES);
+                        eng.step(kbase, kbase + C::RECS * C::REC, valid);
+                        valid -= NW * kQ4Unit;
+                        __syncwarp();
+                        if (lane == 0 && k < stop) {
+                            fence_proxy_async_smem();
+                            issue(k + S * NW, stage);
+                        }
+                        held_stage = stage;
+                        if (++stage == S) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                    }
+                }
+                k = last + NW;
+                if (flush && !dead)
+                    held = last;
+            }
+            refused |= bad_row[row] != 0;
+            at += n;
+            unit += n;
+            left -= n;
+            if (!flush)
+                continue;
 
-    // ---- the warps' parts, through the rings' memory
-    __syncthreads();
-    const bool failed = *reinterpret_cast<volatile uint32_t *>(flag) != 0;
-    float *mw = reinterpret_cast<float *>(smem);
-    float *lw = mw + NW * kListMaxGroup;
-    float *aw = lw + NW * kListMaxGroup;
-    eng.finish(mw, lw, aw, warp, p.group);
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.group * D; i += kListThreads) {
-        const int r = i / D, d = i % D;
-        float Mx = -INFINITY, num = 0.f, den = 0.f;
+            // ---- the warps' parts of the row, through the stages that they took last
+            if (held >= 0)
+                eng.finish(ml + warp * kListMaxGroup, reinterpret_cast<float *>(stages + held_stage * C::STAGE_BYTES), p.group);
+            else if (lane < kListMaxGroup)
+                ml[warp * kListMaxGroup + lane] = make_float2(-INFINITY, 0.f);
+            int *slot = reinterpret_cast<int *>(sums);
+            if (lane == 0)
+                slot[warp] = held_stage;
+            __syncthreads();
+            const bool drop = refused || *reinterpret_cast<volatile uint32_t *>(flag) != 0;
+            whole &= row_ends;
+            const int64_t head0 = ((int64_t)seq * p.num_kv_heads + head) * p.group;
+            const int64_t part0 = ((int64_t)blockIdx.x * 2 + (rows > 0)) * p.group;
+            for (int i = threadIdx.x; i < p.group * (D / 4); i += kListThreads) {
+                const int r = i / (D / 4), d = i % (D / 4) * 4;
+                float Mx = -INFINITY, den = 0.f;
+                float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+                float2 t[NW];
 #pragma unroll
-        for (int w = 0; w < NW; ++w)
-            Mx = fmaxf(Mx, mw[w * kListMaxGroup + r]);
-        const float ref = reference_of(Mx);
+                for (int w = 0; w < NW; ++w) {
+                    t[w] = ml[w * kListMaxGroup + r];
+                    Mx = fmaxf(Mx, t[w].x);
+                }
+                const float ref = reference_of(Mx);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float f = exp2f(mw[w * kListMaxGroup + r] - ref);   // 0 for a warp without tokens; NaN sums stay
-            num += f * aw[(w * kListMaxGroup + r) * C::AWS + d];
-            den += f * lw[w * kListMaxGroup + r];
-        }
-        res->acc[r][d] = num;
-        if (d == 0) {
-            res->m[r] = Mx;
-            res->l[r] = failed ? -1.f : den;
+                for (int w = 0; w < NW; ++w) {
+                    if (t[w].y != 0.f) {   // else the warp had no token; NaN sums stay
+                        const float f = ex2_fast(t[w].x - ref);
+                        const float4 x = *reinterpret_cast<const float4 *>(smem + (w * S + slot[w]) * C::STAGE_BYTES + (r * C::AWS + d) * 4);
+                        num.x = fmaf(f, x.x, num.x);
+                        num.y = fmaf(f, x.y, num.y);
+                        num.z = fmaf(f, x.z, num.z);
+                        num.w = fmaf(f, x.w, num.w);
+                        den = fmaf(f, t[w].y, den);
+                    }
+                }
+                if (!a.shares) {
+                    *reinterpret_cast<float4 *>(&res->acc[r][d]) = num;
+                    if (d == 0) {
+                        res->m[r] = Mx;
+                        res->l[r] = drop ? -1.f : den;
+                    }
+                } else if (whole) {
+                    const bool zero = drop || den == 0.f;
+                    const float inv = 1.f / den;
+                    store_out4(p.out, p.out_dtype, (head0 + r) * D + d,
+                               zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv));
+                } else {
+                    *reinterpret_cast<float4 *>(p.ws_acc + (part0 + r) * D + d) = num;
+                    if (d == 0)
+                        *reinterpret_cast<float2 *>(p.ws_ml + (part0 + r) * 2) = make_float2(Mx, drop ? -1.f : den);
+                }
+            }
+            __syncthreads();
+            if (left == 0)
+                break;
+            if (lane == 0 && held >= 0 && held + S * NW < chunk && !dead) {
+                fence_proxy_async_smem();
+                issue(held + S * NW, held_stage);
+            }
+            ++rows;
+            whole = true;
+            refused = false;
+            unit = 0;
+            fresh = true;
+            next_row(seq, head, L);
         }
     }
-    __syncthreads();
-    write_result<D>(p, res, seq, kvh, part);
-    if (p.np > 1 && !p.cluster)
+    if (!a.shares) {
+        write_result<D>(p, res, seq, head, blockIdx.x);
+        if (p.np > 1 && !p.cluster)
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    } else {
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
+}
+
+// Joins the parts of the rows that several shares hold: CTA i looks after the
+// row inside which share i is the first to begin, a thread after four
+// dimensions of a head.  A part of sum -1: the row is refused.
+constexpr int kQ4MergeThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kQ4MergeThreads)
+q4_merge_kernel(const __grid_constant__ Q4Params a)
+{
+    const ListParams &p = a.list;
+    const int i = blockIdx.x, r = threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Q4Share share = a.ws_share[i];
+    const int64_t row = share.lo - share.unit, before = a.ws_share[max(i - 1, 0)].lo;
+    if (share.unit == 0 || before > row)
+        return;
+    // the row's last share: the last one that starts before the row's end
+    int last = -1;
+    for (int k0 = 0; k0 < a.shares; k0 += kQ4MergeThreads) {
+        const int k = k0 + threadIdx.x;
+        last += __syncthreads_count(k < a.shares && a.ws_share[k].lo < row + share.units);
+    }
+    if (r >= p.group)
+        return;
+    float mx = -INFINITY, den = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool bad = false;
+    constexpr int U = 16;
+    for (int k0 = i - 1; k0 <= last; k0 += U) {
+        float2 t[U];
+        float4 x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = min(k0 + u, last);
+            // a share's second place holds the part of a row that is not its first
+            const int64_t at = ((int64_t)k * 2 + (k < i && before != row)) * p.group + r;
+            t[u] = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml) + at);
+            x[u] = __ldcg(reinterpret_cast<const float4 *>(p.ws_acc + at * D + d));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            t[u] = k0 + u <= last ? t[u] : make_float2(-INFINITY, 0.f);
+        float mn = mx;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            mn = fmaxf(mn, t[u].x);
+            bad |= t[u].y < 0.f;
+        }
+        const float ref = reference_of(mn), f0 = exp2f(mx - ref);
+        den *= f0;
+        num = make_float4(num.x * f0, num.y * f0, num.z * f0, num.w * f0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (t[u].y != 0.f) {
+                const float f = exp2f(t[u].x - ref);
+                den += f * t[u].y;
+                num.x += f * x[u].x;
+                num.y += f * x[u].y;
+                num.z += f * x[u].z;
+                num.w += f * x[u].w;
+            }
+        }
+        mx = mn;
+    }
+    const int64_t head = ((int64_t)share.seq * p.num_kv_heads + share.head) * p.group + r;
+    const bool zero = bad || den == 0.f;
+    const float inv = 1.f / den;
+    store_out4(p.out, p.out_dtype, head * D + d,
+               zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv));
 }
 
 }  // namespace pkv

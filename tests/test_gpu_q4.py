@@ -414,3 +414,63 @@ def test_run_together():
         for b, a in zip(back, (all_k[2], all_v[2])):
             assert torch.equal(b.cpu(), torch.from_numpy(S.numbers(*S.quantize(a.double().numpy(), DT[t]))).to(DT[t]))
         assert st.item() == 0
+
+
+def test_decode_shares_of_many_chunks():
+    """8.4M tokens over all rows: a share of the stream is longer than what a CTA looks up at once, and its chunks end in
+    the middle of rows.  Checked for some heads against 64-bit attention over the numbers read back."""
+    Hk, D, bs, L = 64, 64, 32, 131072 - 5
+    MB = -(-L // bs)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    table = torch.randperm(MB + 3, generator=g, device=DEV)[:MB].to(torch.int32)
+    k, v, st = cache(MB + 3, Hk, bs, D), cache(MB + 3, Hk, bs, D), status()
+    pos = torch.arange(L, device=DEV)
+    slots = table.long()[pos // bs] * bs + pos % bs
+    back = []
+    for c in (k, v):
+        x = torch.randn(L, Hk, D, generator=g, device=DEV).bfloat16()
+        pkv.reshape_and_cache_q4(x, x, c, c, slots, device_status=st)
+        y = torch.empty(L, Hk, D, device=DEV)
+        pkv.gather_cache_q4(y, y, c, c, slots, dtype=torch.bfloat16, device_status=st)
+        back.append(y)
+        del x
+    q = torch.randn(1, Hk, D, generator=g, device=DEV).bfloat16()
+    out = torch.empty(1, Hk, D, device=DEV)
+    pkv.paged_attention_decode_q4(out, q, k, v, table[None], torch.tensor([L], dtype=torch.int32, device=DEV), D ** -0.5, device_status=st)
+    assert st.item() == 0
+    for h in range(0, Hk, 7):
+        kk, vv = (b[:, h].double() for b in back)
+        want = torch.softmax(q[0, h].double() @ kk.T * D ** -0.5, -1) @ vv
+        # scores below 10 off by less than (D + 8) 2^-23 x 60; sums of 131,067 weights cut 2^-23 each: of numbers below 8
+        assert float((out[0, h].double() - want).abs().max()) < 8 * (2 * 72 * 60 + L) * 2.0 ** -23 / 8
+
+
+@pytest.mark.parametrize("lens", [(2600, 0, 33, 31, 700, 1, 32, 4000, 64, 0), tuple([5] * 300), tuple([200, 1] * 40), (1,) * 7 + (3000,)])
+def test_decode_ragged_rows_in_a_stream(lens):
+    """Rows that begin and end anywhere in the shares, sequences without tokens between them."""
+    for D, t, bs in ((64, "f16", 8), (128, "bf16", 16), (128, "f16", 32)):
+        c = S.q4_case(16, t=t, G=3, Hk=5, D=D, bs=bs, lens=lens)
+        got, st = run_decode(c, max_len=8192 if max(lens) < 8192 and c["tables"].shape[1] * bs >= 8192 else None)
+        assert st == 0
+        check(c, got)
+
+
+@pytest.mark.parametrize("what", ["block", "length"])
+def test_bad_data_in_a_stream(what):
+    """A refused sequence among many: its rows are zero, its neighbours in the same shares are not touched."""
+    lens = [300, 900, 40, 2000, 64, 1500] * 4
+    c = S.q4_case(17, t="bf16", G=4, Hk=7, lens=lens)
+    good = {k: (v.copy() if isinstance(v, np.ndarray) else v) for k, v in c.items()}
+    hurt = [3, 8, 23]
+    for s in hurt:
+        if what == "block":
+            c["tables"][s, 1] = c["NB"] + s
+        else:
+            c["lens"][s] = -s if s % 2 else 2001
+    got, st = run_decode(c, max_len=2000)
+    assert st == (pkv.DEV_BAD_BLOCK if what == "block" else pkv.DEV_BAD_CONTEXT_LEN)
+    assert (got[hurt] == 0).all()
+    ref, score, value = S.attention_reference(good)
+    tol = S.attention_tolerance(good, ref, score, value, torch.float32)
+    rest = [s for s in range(len(lens)) if s not in hurt]
+    assert (np.abs(got - ref)[rest] <= tol[rest]).all()
