@@ -33,20 +33,25 @@ int check_rows(const Q4RowsParams &p, int head_dim, int block_size, int elem_byt
     return PKV_OK;
 }
 
+// Tokens per CTA: what it takes at a time (its rows over the token's, at least
+// one token), then times two while that leaves 16 CTAs per SM.
 template <typename K>
 int launch(K kern, Q4RowsParams p, int rows_per_cta, cudaStream_t stream)
 {
     const int rows = 2 * p.num_kv_heads;
-    p.tokens_per_cta = rows >= rows_per_cta ? 1 : rows_per_cta / rows;
+    const int64_t y = ((int64_t)rows + rows_per_cta - 1) / rows_per_cta;
+    const int64_t enough = 16LL * device_sm_count();
+    p.tokens_per_cta = rows < rows_per_cta ? rows_per_cta / rows : 1;
+    while ((p.num_tokens / (2 * p.tokens_per_cta) + 1) * y > enough)
+        p.tokens_per_cta *= 2;
     const unsigned x = (unsigned)(((int64_t)p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta);
-    const int64_t y = ((int64_t)p.tokens_per_cta * rows + rows_per_cta - 1) / rows_per_cta;
     return launch_pdl(kern, dim3(x, (unsigned)y), dim3(kQ4Threads), 0, stream, p);
 }
 
 template <typename T, int D>
 int write_block(const Q4RowsParams &p, int bs, cudaStream_t s)
 {
-    constexpr int rows = kQ4Threads / (D / 16);
+    constexpr int rows = kQ4Threads / Q4Writer<T, D, 8>::LPR;
     switch (bs) {
     case 8: return launch(reshape_and_cache_q4_kernel<T, D, 8>, p, rows, s);
     case 16: return launch(reshape_and_cache_q4_kernel<T, D, 16>, p, rows, s);
@@ -57,7 +62,7 @@ int write_block(const Q4RowsParams &p, int bs, cudaStream_t s)
 template <typename T, typename O, int D>
 int gather_block(const Q4RowsParams &p, int bs, cudaStream_t s)
 {
-    constexpr int rows = kQ4Threads / (D / 8);
+    constexpr int rows = kQ4Threads / Q4Reader<T, O, D, 8>::LPR;
     switch (bs) {
     case 8: return launch(gather_cache_q4_kernel<T, O, D, 8>, p, rows, s);
     case 16: return launch(gather_cache_q4_kernel<T, O, D, 16>, p, rows, s);
