@@ -17,10 +17,10 @@ struct Q4Cut {
 };
 
 // Few rows are cut as lists of blocks are, each row a cluster of up to eight
-// CTAs; short rows (up to 1024 tokens) stay whole; other calls are streamed, the
-// only cut that goes by the contexts' own lengths.  (200 sequences of up to 512
-// tokens, 8 kv heads: whole 32.8 us, streamed 36.3; 33 of up to 4095, heads of
-// 64: 34.9 and 24.6; 64 of 128 to 2048, 32 kv heads: 87 and 90.)
+// CTAs; rows that fill the SMs and are at most 2048 tokens long stay whole; other
+// calls are streamed, the only cut that goes by the contexts' own lengths.  (30
+// sequences of 1500 tokens, 8 kv heads: whole 19.3 us, streamed 24.0; 64 of 128 to
+// 2048, 32 kv heads: 81.6 and 86.1; 33 of up to 4095, heads of 64: 33.5 and 24.0.)
 Q4Cut q4_cut(long long rows, long long max_context_len, int block_size, int partition_size)
 {
     Q4Cut c{};
@@ -28,7 +28,7 @@ Q4Cut q4_cut(long long rows, long long max_context_len, int block_size, int part
     c.list = list_cut(rows, blocks, block_size, partition_size);
     if (partition_size > 0)
         c.part_units = partition_size / kQ4Unit;
-    else if (!c.list.cluster && !(c.list.np == 1 && max_context_len <= 1024))
+    else if (!c.list.cluster && !(c.list.np == 1 && max_context_len <= 2048))
         c.shares = kQ4Ctas * device_sm_count();
     return c;
 }
@@ -55,12 +55,12 @@ bool q4_layout(const Q4Cut &c, uint64_t seqs, uint64_t heads, uint64_t kv_heads,
     return true;
 }
 
-template <typename T, int D, int BS>
+template <typename T, int D, int BS, bool TWICE>
 int run_q4(const Q4Params &p, cudaStream_t stream)
 {
     using C = Q4Cfg<D, BS>;
     static unsigned long long done = 0;
-    auto kern = q4_attention_kernel<T, D, BS>;
+    auto kern = q4_attention_kernel<T, D, BS, TWICE>;
     const int rc = ensure_smem_attr(reinterpret_cast<const void *>(kern), C::SMEM_BYTES, &done);
     if (rc)
         return rc;
@@ -89,13 +89,19 @@ int run_q4(const Q4Params &p, cudaStream_t stream)
     return p.list.np > 1 && !p.list.cluster ? launch_list_merge<D>(p.list, stream) : PKV_OK;
 }
 
+template <typename T, int D, int BS>
+int run_q4_group(const Q4Params &p, cudaStream_t s)
+{
+    return p.list.group <= 4 ? run_q4<T, D, BS, true>(p, s) : run_q4<T, D, BS, false>(p, s);
+}
+
 template <typename T, int D>
 int run_q4_block(const Q4Params &p, int bs, cudaStream_t s)
 {
     switch (bs) {
-    case 8: return run_q4<T, D, 8>(p, s);
-    case 16: return run_q4<T, D, 16>(p, s);
-    default: return run_q4<T, D, 32>(p, s);
+    case 8: return run_q4_group<T, D, 8>(p, s);
+    case 16: return run_q4_group<T, D, 16>(p, s);
+    default: return run_q4_group<T, D, 32>(p, s);
     }
 }
 

@@ -87,7 +87,8 @@ template <int D, int BS> struct Q4Cfg {
     static constexpr int OFF_RESULT = OFF_NUM + kListWarps * 2 * NUMBERS;
     static constexpr int OFF_ML = OFF_RESULT + kListMaxGroup * (D + 2) * 4;
     static constexpr int OFF_BAD = OFF_ML + kListWarps * kListMaxGroup * 8;
-    static constexpr int OFF_BAR = OFF_BAD + CHUNK;
+    static constexpr int OFF_IDS = OFF_BAD + CHUNK;
+    static constexpr int OFF_BAR = OFF_IDS + kListThreads * 4;
     static constexpr int OFF_FLAG = OFF_BAR + kListWarps * S * 8;
     static constexpr int SMEM_BYTES = OFF_FLAG + 128 + 1024;   // slack for the alignment to 1024
     static_assert(REC % 16 == 0 && STAGE_BYTES % 16 == 0 && OFF_RESULT % 16 == 0 && OFF_BAR % 8 == 0 && S >= 2, "alignment");
@@ -192,8 +193,19 @@ __device__ __forceinline__ void q4_mma_first(float (&d)[4], const uint32_t (&a)[
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// A wait that did not end at once: until the phase completes for every lane, or
+// one gives up.  Kept out of the loops that wait.
+__device__ __noinline__ bool q4_wait(uint64_t *bar, uint32_t phase)
+{
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, phase));
+}
+
 // One warp's state.  Lane (g, c) = (lane / 4, lane % 4).
-template <typename T, int D, int BS> struct Q4Engine {
+//
+// TWICE (groups of up to four heads): N's columns 4 .. 7 are heads 0 .. 3 once
+// more, with the weights' second parts where columns 0 .. 3 have the first, so
+// that one product takes both; their sums are added at the end.
+template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
     using C = Q4Cfg<D, BS>;
     using R = Q4Row<D>;
     static constexpr int NG = R::GROUPS;
@@ -211,6 +223,7 @@ template <typename T, int D, int BS> struct Q4Engine {
     uint32_t nums;           // this warp's numbers in shared memory
     int kcode[2], vcode[4];  // byte offsets of this lane's tokens of K and of V in a stage's records
     int mine;                // of the pairs of the token that this lane makes numbers of
+    float second;            // TWICE: -1 where this lane has the weights' second parts
     int g, c;
 
     // Offset of the record of tile row t in a stage, and the row in it.
@@ -235,8 +248,10 @@ template <typename T, int D, int BS> struct Q4Engine {
         // q: dimensions 64 j + 16 c .. + 15 of head g, brought to f16 by a
         // power of two that puts the head's largest magnitude in [2^14, 2^15):
         // what f16 cannot hold is below 2^-35 of it
-        const bool live = g < p.group;
-        const T *qp = static_cast<const T *>(p.q) + (int64_t)seq * a.q_stride + (kvh * p.group + (live ? g : 0)) * D + 16 * c;
+        const int head = TWICE ? g & 3 : g;
+        const bool live = head < p.group;
+        const T *qp = static_cast<const T *>(p.q) + (int64_t)seq * a.q_stride + ((int64_t)kvh * p.group + (live ? head : 0)) * D + 16 * c;
+        second = TWICE && c >= 2 ? -1.f : 0.f;
         using V = typename Pair16<T>::V;
         uint32_t w[NG][8];
         V top = as_pair<T>(0u);
@@ -316,9 +331,10 @@ template <typename T, int D, int BS> struct Q4Engine {
         for (int v = 0; v < 2; ++v) {
 #pragma unroll
             for (int j = 0; j < NG; ++j) {
-                float2 f = Unpack<T>::pair(lds32((v ? vbase : kbase) + mine + 4 * j));
-                if (lane >= nvalid)
-                    f = make_float2(0.f, 0.f);   // no token: what is there may be anything
+                uint32_t w = lds32((v ? vbase : kbase) + mine + 4 * j);
+                if (nvalid < C::TOK)
+                    w = lane < nvalid ? w : 0u;   // no token: what is there may be anything
+                const float2 f = Unpack<T>::pair(w);
                 if (v)
                     top = fmaxf(top, fmaxf(f.x, fabsf(f.y) * 0x1p-24f));
                 asm volatile("st.shared.v4.f32 [%0], {%1, %1, %2, %2};" ::"r"(nums + v * C::NUMBERS + (j * C::TOK + lane) * 16), "f"(f.x), "f"(f.y) : "memory");
@@ -476,9 +492,14 @@ template <typename T, int D, int BS> struct Q4Engine {
                 const float2 w = fmul2(p[n], s);
                 const uint32_t h = Mma<__half>::pack(w.x, w.y);
                 const float2 f = Unpack<__half>::pair(h);
-                const float2 rest = fadd2(w, make_float2(-f.x, -f.y));
-                hi[j][i] = movmatrix_trans(h);
-                lo[j][i] = movmatrix_trans(Mma<__half>::pack(rest.x, rest.y));
+                if constexpr (TWICE) {
+                    const float2 part = ffma2(f, make_float2(second, second), w);
+                    hi[j][i] = movmatrix_trans(Mma<__half>::pack(part.x, part.y));
+                } else {
+                    const float2 rest = fadd2(w, make_float2(-f.x, -f.y));
+                    hi[j][i] = movmatrix_trans(h);
+                    lo[j][i] = movmatrix_trans(Mma<__half>::pack(rest.x, rest.y));
+                }
             }
         }
         uint32_t w[4][NG];
@@ -509,7 +530,7 @@ template <typename T, int D, int BS> struct Q4Engine {
                 a[i][3] = v & 0x00f000f0u;
             }
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
+            for (int part = 0; part < (TWICE ? 1 : 2); ++part) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int j = NG == 2 ? i >> 1 : 0, e = NG == 2 ? q : i >> 1, k = i & 1;
@@ -551,8 +572,13 @@ template <typename T, int D, int BS> struct Q4Engine {
                 add[j] += __shfl_xor_sync(0xffffffffu, add[j], 16);
             }
             const int row = 2 * c + h;
-            if (row < group) {
-                if (g == 0)
+            if ((TWICE ? row & 3 : row) < group) {
+                if (TWICE && c >= 2) {
+#pragma unroll
+                    for (int j = 0; j < NG; ++j)
+                        add[j] = 0.f;
+                }
+                if (g == 0 && (!TWICE || c < 2))
                     ml[row] = make_float2(h ? m.y : m.x, l);
                 float *dst = aw + row * C::AWS + 8 * g;
 #pragma unroll
@@ -577,7 +603,7 @@ __device__ __forceinline__ void q4_zero_rows(const ListParams &p, int seq)
 }
 
 // Grid: streamed (shares); else (partition, kv head, sequence).
-template <typename T, int D, int BS>
+template <typename T, int D, int BS, bool TWICE>
 __global__ void __launch_bounds__(kListThreads, kQ4Ctas)
 q4_attention_kernel(const __grid_constant__ Q4Params a)
 {
@@ -603,6 +629,11 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
     if (threadIdx.x == 0)
         *flag = 0;
     wait_for_stream();
+    // a table that the CTA's threads hold leaves memory together with the length
+    int32_t *ids = reinterpret_cast<int32_t *>(smem + C::OFF_IDS);
+    const bool early = !a.shares && p.max_context_len <= kListThreads * BS;
+    if (early && threadIdx.x * BS < p.max_context_len)
+        ids[threadIdx.x] = p.block_tables[(int64_t)blockIdx.z * p.max_blocks_per_seq + threadIdx.x];
 
     // ---- the share: `left` units from unit `unit` of row (seq, head) on
     int seq, head, unit, L;
@@ -670,7 +701,7 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
     bool whole = unit == 0;     // the row starts here
     int rows = 0;               // rows finished
     bool fresh = true;          // the engine has nothing of the row yet
-    Q4Engine<T, D, BS> eng;
+    Q4Engine<T, D, BS, TWICE> eng;
     eng.nums = smem_u32(smem + C::OFF_NUM + warp * 2 * C::NUMBERS);
 
     while (left > 0) {
@@ -689,7 +720,7 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
                     const int64_t b = (int64_t)u * C::RECS + k;
                     int64_t where = -1;
                     if (b * BS < len) {
-                        int id = table[b];
+                        int id = early ? ids[b] : table[b];
                         if (id < 0 || (int64_t)id >= p.num_blocks) {
                             bad = true;
                             bad_row[row] = 1;
@@ -763,7 +794,7 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
                 int valid = (int)min((int64_t)INT32_MAX, L - (int64_t)(unit + k - at) * kQ4Unit);
                 for (; k <= last && !dead; k += NW) {
                     // the warp gives up as one: its products and shuffles need every lane
-                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[stage], phase))) {
+                    if (!__all_sync(0xffffffffu, mbar_try_wait(&bars[stage], phase)) && !q4_wait(&bars[stage], phase)) {
                         // no CTA leaves with loads in flight
                         for (int i = 0; i < S && k + i * NW < chunk; ++i)
                             drain_wait(&bars[(stage + i) % S], phase ^ (stage + i >= S), lane == 0 ? p.status : nullptr);
@@ -827,7 +858,12 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
                 for (int w = 0; w < NW; ++w) {
                     if (t[w].y != 0.f) {   // else the warp had no token; NaN sums stay
                         const float f = ex2_fast(t[w].x - ref);
-                        const float4 x = *reinterpret_cast<const float4 *>(smem + (w * S + slot[w]) * C::STAGE_BYTES + (r * C::AWS + d) * 4);
+                        const float *aw = reinterpret_cast<const float *>(smem + (w * S + slot[w]) * C::STAGE_BYTES) + r * C::AWS + d;
+                        float4 x = *reinterpret_cast<const float4 *>(aw);
+                        if constexpr (TWICE) {
+                            const float4 y = *reinterpret_cast<const float4 *>(aw + 4 * C::AWS);
+                            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                        }
                         num.x = fmaf(f, x.x, num.x);
                         num.y = fmaf(f, x.y, num.y);
                         num.z = fmaf(f, x.z, num.z);

@@ -41,7 +41,7 @@ int launch(K kern, Q4RowsParams p, int rows_per_cta, cudaStream_t stream)
     const int rows = 2 * p.num_kv_heads;
     const int64_t y = ((int64_t)rows + rows_per_cta - 1) / rows_per_cta;
     const int64_t enough = 16LL * device_sm_count();
-    p.tokens_per_cta = rows < rows_per_cta ? rows_per_cta / rows : 1;
+    p.step = p.tokens_per_cta = rows < rows_per_cta ? rows_per_cta / rows : 1;
     while ((p.num_tokens / (2 * p.tokens_per_cta) + 1) * y > enough)
         p.tokens_per_cta *= 2;
     const unsigned x = (unsigned)(((int64_t)p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta);
@@ -92,7 +92,7 @@ Q4RowsParams rows_params(const void *key, int64_t key_stride, const void *value,
     p.num_blocks = num_blocks;
     p.num_tokens = num_tokens;
     p.num_kv_heads = num_kv_heads;
-    p.tokens_per_cta = 1;
+    p.tokens_per_cta = p.step = 1;
     return p;
 }
 

@@ -61,40 +61,32 @@ struct Q4RowsParams {
     int64_t num_blocks;
     int num_tokens, num_kv_heads;
     int tokens_per_cta;
+    int step;                     // tokens whose rows a CTA takes at a time
 };
 
 constexpr int kQ4Threads = 256;
 
 // Which rows a thread of a CTA works on, LANES threads to a row: always the same
-// row (K's heads, then V's) of tokens first, first + step, ... below end.  Where
-// a token has fewer rows than a CTA takes at a time, the CTA takes several
-// tokens; where it has more, blockIdx.y tells the rows.
+// row (K's heads, then V's) of `left` tokens first, first + step, ...  Where a
+// token has fewer rows than a CTA takes at a time, the CTA takes several tokens
+// (`step`); where it has more, blockIdx.y tells the rows.
 template <int LANES> struct Q4Rows {
     static constexpr int AT_ONCE = kQ4Threads / LANES;
-    int head, step;
-    int64_t first, end;
+    int head, step, left;
+    int64_t first;
     bool is_v;
-    __device__ __forceinline__ explicit Q4Rows(const Q4RowsParams &p)
+    __device__ __forceinline__ explicit Q4Rows(const Q4RowsParams &p) : step(p.step)
     {
         const int rows = 2 * p.num_kv_heads, mine = threadIdx.x / LANES;
-        int row = mine, token = 0;
-        step = 1;
-        if (rows < AT_ONCE) {
-            step = AT_ONCE / rows;
-            token = mine / rows;
-            row = mine - token * rows;
-        } else {
-            row += blockIdx.y * AT_ONCE;
-        }
+        const int token = step > 1 ? mine / rows : 0;
+        const int row = step > 1 ? mine - token * rows : mine + (int)blockIdx.y * AT_ONCE;
         is_v = row >= p.num_kv_heads;
         head = is_v ? row - p.num_kv_heads : row;
         const int64_t t0 = (int64_t)blockIdx.x * p.tokens_per_cta;
         first = t0 + token;
-        end = min(t0 + p.tokens_per_cta, (int64_t)p.num_tokens);
-        if (row >= rows || token >= step)
-            first = end;    // no row of its own
+        const int here = (int)min((int64_t)p.tokens_per_cta, p.num_tokens - t0) - token;
+        left = row < rows && token < step && here > 0 ? (step > 1 ? (here + step - 1) / step : here) : 0;
     }
-    __device__ __forceinline__ int left() const { return first < end ? (int)((end - first + step - 1) / step) : 0; }
 };
 
 // A slot's record: `base` is the first block's record of the head, blocks are
@@ -235,7 +227,7 @@ reshape_and_cache_q4_kernel(const __grid_constant__ Q4RowsParams p)
     const int64_t stride = mine.is_v ? p.value_stride : p.key_stride, step = stride * mine.step;
     const T *src = static_cast<const T *>(mine.is_v ? p.value : p.key) + mine.first * stride + mine.head * D + 16 * l;
     const int64_t *at = p.slot_mapping + mine.first;
-    int left = mine.left();
+    int left = mine.left;
     wait_for_stream();
     for (; __all_sync(0xffffffffu, left >= U); left -= U) {
         uint4 x[U][2];
@@ -358,30 +350,29 @@ gather_cache_q4_kernel(const __grid_constant__ Q4RowsParams p)
     const int64_t stride = mine.is_v ? p.value_stride : p.key_stride, step = stride * mine.step;
     O *dst = static_cast<O *>(const_cast<void *>(mine.is_v ? p.value : p.key)) + mine.first * stride + mine.head * D + 8 * reader.i;
     const int64_t *at = p.slot_mapping + mine.first;
-    int left = mine.left();
+    int left = mine.left;
     wait_for_stream();
-    for (; left >= U; left -= U) {
+    auto batch = [&](auto all) {
         int64_t slot[U];
         typename G::Row r[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            slot[u] = *at;
-            at += mine.step;
-        }
+        for (int u = 0; u < U; ++u)
+            slot[u] = decltype(all)::value || u < left ? at[(int64_t)u * mine.step] : -1;
 #pragma unroll
         for (int u = 0; u < U; ++u)
             r[u] = reader.read(slot[u]);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            G::write(r[u], dst);
-            dst += step;
-        }
-    }
-    for (; left > 0; --left) {
+        for (int u = 0; u < U; ++u)
+            G::write(r[u], dst + u * step);
+        at += U * (int64_t)mine.step;
+        dst += U * step;
+    };
+    for (; left >= U; left -= U)
+        batch(std::true_type{});
+    if (left > 1)
+        batch(std::false_type{});
+    else if (left == 1)
         G::write(reader.read(*at), dst);
-        at += mine.step;
-        dst += step;
-    }
 }
 
 }  // namespace pkv
