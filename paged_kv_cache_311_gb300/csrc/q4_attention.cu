@@ -84,7 +84,12 @@ int run_q4(const Q4Params &p, cudaStream_t stream)
     if (p.shares) {
         static unsigned long long merge_done = 0;
         const int rm = ensure_smem_attr(reinterpret_cast<const void *>(q4_merge_kernel<D>), 0, &merge_done);
-        return rm ? rm : launch_pdl(q4_merge_kernel<D>, dim3((unsigned)p.shares), dim3(kQ4MergeThreads), 0, stream, p);
+        if (rm)
+            return rm;
+        // at least a thread for each four dimensions of a group's heads
+        const bool many = p.shares >= 8LL * p.list.num_seqs * p.list.num_kv_heads;
+        const int threads = many ? kQ4MergeThreads : p.list.group * (D / 4) <= 128 ? 128 : 256;
+        return launch_pdl(q4_merge_kernel<D>, dim3((unsigned)p.shares), dim3(threads), 0, stream, p);
     }
     return p.list.np > 1 && !p.list.cluster ? launch_list_merge<D>(p.list, stream) : PKV_OK;
 }

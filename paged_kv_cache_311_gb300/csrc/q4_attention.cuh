@@ -914,15 +914,25 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
 
 // Joins the parts of the rows that several shares hold: CTA i looks after the
 // row inside which share i is the first to begin, a thread after four
-// dimensions of a head.  A part of sum -1: the row is refused.
-constexpr int kQ4MergeThreads = 256;
+// dimensions of a head in every `ways`th part.  A part of sum -1: the row is
+// refused.  CTAs are large where rows have many parts (one context of 128K tokens,
+// 57 parts a row: 41.4 us against 43.5) and small where many of them have two (33
+// sequences, heads of 64: 25.9 against 29.1).
+constexpr int kQ4MergeThreads = 512;   // at most
 
 template <int D>
 __global__ void __launch_bounds__(kQ4MergeThreads)
 q4_merge_kernel(const __grid_constant__ Q4Params a)
 {
+    struct Part {
+        float m, l;   // l of -1: refused
+        float4 sums;
+    };
+    __shared__ Part parts[kQ4MergeThreads];
     const ListParams &p = a.list;
-    const int i = blockIdx.x, r = threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
+    const int items = p.group * (D / 4), ways = (int)blockDim.x / items;
+    const int way = threadIdx.x / items, item = threadIdx.x - way * items;
+    const int i = blockIdx.x, r = item / (D / 4), d = item % (D / 4) * 4;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Q4Share share = a.ws_share[i];
     const int64_t row = share.lo - share.unit, before = a.ws_share[max(i - 1, 0)].lo;
@@ -930,33 +940,39 @@ q4_merge_kernel(const __grid_constant__ Q4Params a)
         return;
     // the row's last share: the last one that starts before the row's end
     int last = -1;
-    for (int k0 = 0; k0 < a.shares; k0 += kQ4MergeThreads) {
+    for (int k0 = 0; k0 < a.shares; k0 += (int)blockDim.x) {
         const int k = k0 + threadIdx.x;
         last += __syncthreads_count(k < a.shares && a.ws_share[k].lo < row + share.units);
     }
-    if (r >= p.group)
-        return;
     float mx = -INFINITY, den = 0.f;
     float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
     bool bad = false;
-    constexpr int U = 16;
-    for (int k0 = i - 1; k0 <= last; k0 += U) {
+    auto join = [&](const float2 &t, const float4 &x, float ref) {
+        if (t.y != 0.f) {
+            const float f = exp2f(t.x - ref);
+            den += f * t.y;
+            num.x += f * x.x;
+            num.y += f * x.y;
+            num.z += f * x.z;
+            num.w += f * x.w;
+        }
+    };
+    constexpr int U = 8;
+    for (int k0 = i - 1 + way; way < ways && k0 <= last; k0 += U * ways) {
         float2 t[U];
         float4 x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k = min(k0 + u, last);
+            const int k = min(k0 + u * ways, last);
             // a share's second place holds the part of a row that is not its first
             const int64_t at = ((int64_t)k * 2 + (k < i && before != row)) * p.group + r;
             t[u] = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml) + at);
             x[u] = __ldcg(reinterpret_cast<const float4 *>(p.ws_acc + at * D + d));
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            t[u] = k0 + u <= last ? t[u] : make_float2(-INFINITY, 0.f);
         float mn = mx;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            t[u] = k0 + u * ways <= last ? t[u] : make_float2(-INFINITY, 0.f);
             mn = fmaxf(mn, t[u].x);
             bad |= t[u].y < 0.f;
         }
@@ -964,17 +980,25 @@ q4_merge_kernel(const __grid_constant__ Q4Params a)
         den *= f0;
         num = make_float4(num.x * f0, num.y * f0, num.z * f0, num.w * f0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (t[u].y != 0.f) {
-                const float f = exp2f(t[u].x - ref);
-                den += f * t[u].y;
-                num.x += f * x[u].x;
-                num.y += f * x[u].y;
-                num.z += f * x[u].z;
-                num.w += f * x[u].w;
-            }
-        }
+        for (int u = 0; u < U; ++u)
+            join(t[u], x[u], ref);
         mx = mn;
+    }
+    parts[threadIdx.x] = Part{mx, bad ? -1.f : den, num};
+    __syncthreads();
+    if (way > 0)
+        return;
+    float M = -INFINITY;
+    for (int w = 0; w < ways; ++w) {
+        M = fmaxf(M, parts[w * items + item].m);
+        bad |= parts[w * items + item].l < 0.f;
+    }
+    const float ref = reference_of(M);
+    den = 0.f;
+    num = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 0; w < ways; ++w) {
+        const Part &x = parts[w * items + item];
+        join(make_float2(x.m, x.l), x.sums, ref);
     }
     const int64_t head = ((int64_t)share.seq * p.num_kv_heads + share.head) * p.group + r;
     const bool zero = bad || den == 0.f;
