@@ -62,7 +62,7 @@ constexpr int kQ4Unit = 32;      // tokens that a warp takes at a time
 // (64 sequences of 128 to 2048 tokens, 32 kv heads: 90 us; with 4 units 100,
 // with none 119.)
 constexpr int kQ4RowCost = 8;
-constexpr int kQ4Ring = 57344;   // ring bytes of a CTA at most
+constexpr int kQ4Ring = 40960;   // ring bytes of a CTA at most
 constexpr int kQ4Ctas = 3;       // CTAs per SM
 
 template <int D, int BS> struct Q4Cfg {
@@ -224,6 +224,8 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
     int kcode[2], vcode[4];  // byte offsets of this lane's tokens of K and of V in a stage's records
     int mine;                // of the pairs of the token that this lane makes numbers of
     float second;            // TWICE: -1 where this lane has the weights' second parts
+    uint32_t steps;          // taken of the row
+    uint32_t flip;           // ~0 in steps that take V's codes from 15
     int g, c;
 
     // Offset of the record of tile row t in a stage, and the row in it.
@@ -252,6 +254,7 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
         const bool live = head < p.group;
         const T *qp = static_cast<const T *>(p.q) + (int64_t)seq * a.q_stride + ((int64_t)kvh * p.group + (live ? head : 0)) * D + 16 * c;
         second = TWICE && c >= 2 ? -1.f : 0.f;
+        steps = 0;
         using V = typename Pair16<T>::V;
         uint32_t w[NG][8];
         V top = as_pair<T>(0u);
@@ -323,6 +326,14 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
     //  Returns the largest scale of V among all tokens, at least kLeast,
     // with the minima that hold the weights down, too: those of a size that makes
     // the scales' part of the numbers one below fp32's last bit.
+    //
+    // V's codes are not negative: their sums would grow while the minima's take
+    // most of them away again, and tensor cores cut what they add towards zero,
+    // which tells in outputs that are means of many numbers.  So half the steps
+    // (flip: of four, the second and third) take s u + m as (m + 15 s) + (-s)
+    // (15 - u): the sums stay as small as one step's, and of either sign in turn.
+    // (Means over 60,000 tokens are then off by 2.6e-5 of their size; where each
+    // step only started from zero and was added rounded to nearest, by 2.0e-4.)
     __device__ __forceinline__ float numbers(uint32_t kbase, uint32_t vbase, int nvalid) const
     {
         float top = kLeast;
@@ -334,9 +345,13 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
                 uint32_t w = lds32((v ? vbase : kbase) + mine + 4 * j);
                 if (nvalid < C::TOK)
                     w = lane < nvalid ? w : 0u;   // no token: what is there may be anything
-                const float2 f = Unpack<T>::pair(w);
+                float2 f = Unpack<T>::pair(w);
                 if (v)
                     top = fmaxf(top, fmaxf(f.x, fabsf(f.y) * 0x1p-24f));
+                if (v) {
+                    f.y = fmaf(flip ? 15.f : 0.f, f.x, f.y);
+                    f.x = __uint_as_float(__float_as_uint(f.x) ^ (flip & 0x80000000u));
+                }
                 asm volatile("st.shared.v4.f32 [%0], {%1, %1, %2, %2};" ::"r"(nums + v * C::NUMBERS + (j * C::TOK + lane) * 16), "f"(f.x), "f"(f.y) : "memory");
             }
         }
@@ -438,7 +453,7 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
             for (int j = 0; j < NG; ++j) {
                 float2 s, mn;
                 number(1, j, n, s, mn);
-                big = fmaxf(big, fmaxf(s.x, fabsf(mn.x) * 0x1p-24f));
+                big = fmaxf(big, fmaxf(fabsf(s.x), fabsf(mn.x) * 0x1p-24f));
             }
             big = __log2f(big) - kLift;
             if (token(n) < nvalid) {
@@ -475,11 +490,20 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
         }
     }
 
+    // (w ^ flip) & mask, one instruction
+    __device__ __forceinline__ uint32_t codes(uint32_t w, uint32_t mask) const
+    {
+        uint32_t d;
+        asm("lop3.b32 %0, %1, %2, %3, 0x28;" : "=r"(d) : "r"(w), "r"(flip), "r"(mask));
+        return d;
+    }
+
     // The weights' sums, their products with the minima in fp32, and with the
     // codes of a tile of the step whose records start at vbase.
     __device__ __forceinline__ void value_tile(uint32_t vbase, int tile, const float2 (&p)[N])
     {
-        uint32_t hi[NG][2], lo[NG][2];   // weights times scales in two f16 parts, as B-fragments
+        constexpr int PARTS = TWICE ? 1 : 2;
+        uint32_t part[PARTS][NG][2];   // weights times scales, as B-fragments
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int n = 2 * tile + i;
@@ -493,12 +517,12 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
                 const uint32_t h = Mma<__half>::pack(w.x, w.y);
                 const float2 f = Unpack<__half>::pair(h);
                 if constexpr (TWICE) {
-                    const float2 part = ffma2(f, make_float2(second, second), w);
-                    hi[j][i] = movmatrix_trans(Mma<__half>::pack(part.x, part.y));
+                    const float2 mine = ffma2(f, make_float2(second, second), w);
+                    part[0][j][i] = movmatrix_trans(Mma<__half>::pack(mine.x, mine.y));
                 } else {
                     const float2 rest = fadd2(w, make_float2(-f.x, -f.y));
-                    hi[j][i] = movmatrix_trans(h);
-                    lo[j][i] = movmatrix_trans(Mma<__half>::pack(rest.x, rest.y));
+                    part[0][j][i] = movmatrix_trans(h);
+                    part[PARTS - 1][j][i] = movmatrix_trans(Mma<__half>::pack(rest.x, rest.y));
                 }
             }
         }
@@ -514,27 +538,26 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
                 w[i][0] = lds32(at);
             }
         }
-        // four m-tiles at a time, so that the two parts' products, which add to
-        // the same sums, stand apart
 #pragma unroll
-        for (int q = 0; q < NG; ++q) {
-            uint32_t a[4][4];
+        for (int j = 0; j < NG; ++j) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = NG == 2 ? i >> 1 : 0, e = NG == 2 ? q : i >> 1, k = i & 1;
-                const uint32_t u = __byte_perm(w[0][j], w[1][j], e ? 0x7632 : 0x5410) >> (8 * k);
-                const uint32_t v = __byte_perm(w[2][j], w[3][j], e ? 0x7632 : 0x5410) >> (8 * k);
-                a[i][0] = u & 0x000f000fu;
-                a[i][1] = u & 0x00f000f0u;
-                a[i][2] = v & 0x000f000fu;
-                a[i][3] = v & 0x00f000f0u;
-            }
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t u = __byte_perm(w[0][j], w[1][j], e ? 0x7632 : 0x5410);
+                const uint32_t v = __byte_perm(w[2][j], w[3][j], e ? 0x7632 : 0x5410);
+                uint32_t a[2][4];
 #pragma unroll
-            for (int part = 0; part < (TWICE ? 1 : 2); ++part) {
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t uk = u >> (8 * k), vk = v >> (8 * k);
+                    a[k][0] = codes(uk, 0x000f000fu);
+                    a[k][1] = codes(uk, 0x00f000f0u);
+                    a[k][2] = codes(vk, 0x000f000fu);
+                    a[k][3] = codes(vk, 0x00f000f0u);
+                }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = NG == 2 ? i >> 1 : 0, e = NG == 2 ? q : i >> 1, k = i & 1;
-                    Mma<__half>::run(o[j][2 * e + k], a[i], part ? lo[j][0] : hi[j][0], part ? lo[j][1] : hi[j][1]);
+                for (int i = 0; i < PARTS; ++i) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        Mma<__half>::run(o[j][2 * e + k], a[k], part[i][j][0], part[i][j][1]);
                 }
             }
         }
@@ -544,6 +567,7 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
     // nvalid of them count.
     __device__ __forceinline__ void step(uint32_t kbase, uint32_t vbase, int nvalid)
     {
+        flip = 0u - ((steps + 1) >> 1 & 1u);
         const float top = numbers(kbase, vbase, nvalid);
         __syncwarp();
         float2 x[N], p[N];
@@ -552,6 +576,7 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
 #pragma unroll
         for (int tile = 0; tile < C::TILES; ++tile)
             value_tile(vbase, tile, p);
+        ++steps;
     }
 
     // This warp's reference, sum and sums of values of the heads below `group`:

@@ -41,10 +41,12 @@ int launch(K kern, Q4RowsParams p, int rows_per_cta, cudaStream_t stream)
     const int rows = 2 * p.num_kv_heads;
     const int64_t y = ((int64_t)rows + rows_per_cta - 1) / rows_per_cta;
     const int64_t enough = 16LL * device_sm_count();
-    p.step = p.tokens_per_cta = rows < rows_per_cta ? rows_per_cta / rows : 1;
-    while ((p.num_tokens / (2 * p.tokens_per_cta) + 1) * y > enough)
-        p.tokens_per_cta *= 2;
-    const unsigned x = (unsigned)(((int64_t)p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta);
+    p.step = rows < rows_per_cta ? rows_per_cta / rows : 1;
+    int64_t tokens = p.step;
+    while (tokens < p.num_tokens && (p.num_tokens / (2 * tokens) + 1) * y > enough)
+        tokens *= 2;
+    p.tokens_per_cta = (int)(tokens < p.num_tokens ? tokens : p.num_tokens);
+    const unsigned x = (unsigned)((p.num_tokens + (int64_t)p.tokens_per_cta - 1) / p.tokens_per_cta);
     return launch_pdl(kern, dim3(x, (unsigned)y), dim3(kQ4Threads), 0, stream, p);
 }
 

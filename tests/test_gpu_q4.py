@@ -474,3 +474,41 @@ def test_bad_data_in_a_stream(what):
     tol = S.attention_tolerance(good, ref, score, value, torch.float32)
     rest = [s for s in range(len(lens)) if s not in hurt]
     assert (np.abs(got - ref)[rest] <= tol[rest]).all()
+
+
+@pytest.mark.parametrize("t,D,bs,Hk,T", [("f16", 128, 16, 3, 20011), ("bf16", 64, 8, 5, 30011), ("bf16", 128, 32, 70, 1501), ("f16", 64, 16, 1, 50003),
+                                         ("f16", 128, 8, 2500, 3), ("bf16", 64, 8, 40000, 1)])
+def test_write_and_read_many(t, D, bs, Hk, T):
+    """CTAs of many tokens, tokens of many CTAs; some of the tokens are padding."""
+    rng = np.random.RandomState(T)
+    g = torch.Generator(device=DEV).manual_seed(T)
+    NB = -(-T // bs) + 2
+    slots = rng.permutation(NB * bs)[:T]
+    slots[rng.rand(T) < 0.1] = -5
+    key, value = (torch.randn(T, Hk, D, generator=g, device=DEV).mul_(3).to(DT[t]) for _ in "kv")
+    k, v, st = cache(NB, Hk, bs, D), cache(NB, Hk, bs, D), status()
+    pkv.reshape_and_cache_q4(key, value, k, v, dev(slots), device_status=st)
+    out = [torch.full((T, Hk, D), 7.0, device=DEV) for _ in "kv"]
+    pkv.gather_cache_q4(*out, k, v, dev(slots), dtype=DT[t], device_status=st)
+    assert st.item() == 0
+    for o, x in zip(out, (key, value)):
+        want = torch.from_numpy(S.numbers(*S.quantize(x.double().cpu().numpy(), DT[t]))).float()
+        want[torch.from_numpy(slots < 0)] = 7.0
+        assert torch.equal(o.cpu(), want)
+
+
+@pytest.mark.parametrize("G", [2, 8])
+def test_long_sums_have_no_bias(G):
+    """Equal weights (q = 0) over one long context, by one CTA: an output is the mean of 60,000 numbers of both signs, far
+    below the codes' part of it.  What tensor cores cut off always goes towards zero: within a step's four products it is
+    at most 4 x 2^-23 of the codes' sum, and it must not build up over the 469 steps that a warp takes (codes of any value
+    being as likely, half of the steps cut it from the other side)."""
+    for t, D in (("f16", 128), ("bf16", 64)):
+        c = S.q4_case(18, t=t, G=G, Hk=1, D=D, bs=32, lens=(60000,), offset=0.0)
+        c["q"].zero_()
+        got, st = run_decode(c, P=60032 - 60032 % 32)
+        assert st == 0
+        ref, _, value = S.attention_reference(c)
+        assert np.abs(ref).max() < 0.1 * value.max()
+        assert abs((got - ref).mean()) < 4 * 2.0 ** -23 * value.max()
+        check(c, got)
