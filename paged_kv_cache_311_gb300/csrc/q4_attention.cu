@@ -16,20 +16,38 @@ struct Q4Cut {
     int shares, part_units;
 };
 
-// Few rows are cut as lists of blocks are, each row a cluster of up to eight
-// CTAs; rows that fill the SMs and are at most 2048 tokens long stay whole; other
-// calls are streamed, the only cut that goes by the contexts' own lengths.  (30
-// sequences of 1500 tokens, 8 kv heads: whole 19.3 us, streamed 24.0; 64 of 128 to
-// 2048, 32 kv heads: 81.6 and 86.1; 33 of up to 4095, heads of 64: 33.5 and 24.0.)
+// Rows that leave CTAs idle are divided among clusters, by each row's own length,
+// as long as all CTAs are resident at once; other short rows stay whole; the rest
+// is streamed, in shares of equal cost.  us, in that order (whole: one CTA a row):
+//   1 sequence of 4000 tokens, 8 kv heads (8 per row)     9.6   -     13.9
+//   16 of 2000 (3 per row)                               15.2   19.6   18.8
+//   30 of 2000                                             -   25.2   27.5
+//   64 of 128 to 2048, 32 kv heads                         -   81.5   82.5
+//   33 of up to 4095, heads of 64                          -   33.5   24.0
+//   16 of 8K to 16K                                        -     -    63.0
+// (Clusters of 8 whatever the rows, which come in waves: 16.8, 22.1, 82.3 for 8 of
+// 2000, 16 of 2000, 16 of 8K to 16K.)
 Q4Cut q4_cut(long long rows, long long max_context_len, int block_size, int partition_size)
 {
     Q4Cut c{};
-    const long long blocks = max_context_len > 0 ? (max_context_len + block_size - 1) / block_size : 1;
-    c.list = list_cut(rows, blocks, block_size, partition_size);
-    if (partition_size > 0)
+    if (partition_size > 0) {
+        const long long blocks = max_context_len > 0 ? (max_context_len + block_size - 1) / block_size : 1;
+        c.list = list_cut(rows, blocks, block_size, partition_size);
         c.part_units = partition_size / kQ4Unit;
-    else if (!c.list.cluster && !(c.list.np == 1 && max_context_len <= 2048))
-        c.shares = kQ4Ctas * device_sm_count();
+        return c;
+    }
+    const long long slots = (long long)kQ4Ctas * device_sm_count();
+    const long long units = (max_context_len + kQ4Unit - 1) / kQ4Unit;
+    // (clusters of CTAs on nearby SMs do not fill every slot: at 448 of 456, 64 rows
+    // of 700 tokens take 12.8 us, at 384 8.0)
+    long long np = slots * 7 / 8 / rows;
+    np = np > 8 ? 8 : np;
+    np = np > units ? units : np;
+    np = np < 1 ? 1 : np;
+    if (units > np * (np > 1 ? 32 : 64))
+        c.shares = (int)slots;
+    else
+        c.list = ListCut{0, (int)np, np > 1};
     return c;
 }
 
@@ -193,8 +211,8 @@ int pkv_paged_attention_decode_q4(void *out, int out_dtype, const void *q, int64
     l.group = num_heads / num_kv_heads;
     l.max_blocks_per_seq = max_blocks_per_seq;
     l.max_context_len = max_context_len;
-    l.np = cut.list.np;
-    l.cluster = cut.list.cluster;
+    l.np = cut.shares ? 1 : cut.list.np;
+    l.cluster = !cut.shares && cut.list.cluster;
     l.out_dtype = out_dtype;
     l.q_dtype = q_dtype;
     l.qscale = scale * 1.4426950408889634f;
