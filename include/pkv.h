@@ -665,7 +665,14 @@ int pkv_gather_cache_q4(void *key, int64_t key_stride, void *value, int64_t valu
  *              16-byte aligned (may be NULL where that is 0)
  * head_dim 64 or 128; block_size 8, 16 or 32; num_heads / num_kv_heads 1 to 8;
  * num_seqs and num_kv_heads up to 65,535.  Device errors as for
- * pkv_paged_attention_decode: the rows they concern are zero.
+ * pkv_paged_attention_decode: the rows they concern are zero.  A group of NaNs
+ * in K makes the rows of its kv head NaN, one in V its dimensions.
+ * Scores, softmax sums and accumulators are fp32.  q is multiplied in f16, each
+ * head's scaled by a power of two: elements are off by at most 2^-35 of the
+ * head's largest.  A softmax weight times a scale of V enters the product with
+ * the codes in two f16 parts: off by 2^-22 of itself and 2^-32 of the head's
+ * largest such product so far.  (For |q| below 2^100 and numbers of V below
+ * 2^90 in magnitude; beyond, small weights are lost, then sums overflow.)
  */
 int pkv_paged_attention_decode_q4(void *out, int out_dtype, const void *q, int64_t q_stride,
                                   int q_dtype, const void *k_cache, const void *v_cache,

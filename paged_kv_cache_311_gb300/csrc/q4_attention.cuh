@@ -32,6 +32,17 @@
 // largest score alone: weights are 2^(x - m) with m such that the largest
 // 2^(x - m) s, not the largest 2^(x - m), is near 2^7.
 //
+// What bounds it: instructions.  Sixteen contexts of 16K to 32K tokens with 8
+// query heads a kv head (454 MB) take 100 to 106 us, 4.3 to 4.5 TB/s or 64 to 68 %
+// of a copy's rate; one of 128K tokens with 4 heads 41 us (151 MB, 55 %); 64 of 128
+// to 2048 tokens, 32 kv heads, 83 to 88 us (56 %).  Without any loads the first
+// takes 103 us, from L2 the same.  A step of 32 tokens is some 560 warp
+// instructions, a third of them the masks and shifts that make codes operands;
+// the ALU pipe, at two cycles each, is busy 47 % of the time, the tensor pipe
+// 32 %, and more CTAs per SM (4: 111 us), fewer (2: 123, 1: 180), steps of 16
+// tokens (114), or K's products of one step among V's of the one before (118)
+// change little: the pipes' times add up rather than overlap.
+//
 // The M axes' order is free: row 2 c + e + 8 f of a tile is its token
 // 4 c + 2 f + e (so that a thread's four tokens of V are neighbours), and a
 // thread's rows of V^T are the dimensions that its words hold.
