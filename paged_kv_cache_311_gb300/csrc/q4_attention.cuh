@@ -743,6 +743,7 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
     while (left > 0) {
         // ---- the blocks of the next units; -1 behind a row's last
         int chunk = (int)min(left, (int64_t)C::CHUNK);
+        __syncthreads();   // no warp is still in the chunk before, whose last row may go on here
         for (int k = threadIdx.x; k < chunk; k += kListThreads)
             bad_row[k] = 0;
         __syncthreads();

@@ -512,3 +512,15 @@ def test_long_sums_have_no_bias(G):
         assert np.abs(ref).max() < 0.1 * value.max()
         assert abs((got - ref).mean()) < 4 * 2.0 ** -23 * value.max()
         check(c, got)
+
+
+@pytest.mark.parametrize("where", [3, 300, 700, 749])
+def test_bad_block_in_a_row_of_several_chunks(where):
+    """A CTA's part of a row is longer than what it looks up at once; the bad block lies in any piece of it.  All heads and
+    dimensions are zero, every time."""
+    c = S.q4_case(19, t="bf16", G=8, Hk=2, D=128, bs=16, lens=(12000, 5000))
+    c["tables"][0, where] = -1
+    for P in (0, 12000 // 32 * 32 + 32, 8192):
+        for _ in range(5):
+            got, st = run_decode(c, P)
+            assert st == pkv.DEV_BAD_BLOCK and (got[0] == 0).all() and (got[1] != 0).all()
