@@ -20,7 +20,8 @@ ROOT = os.path.dirname(HERE)
 LIB_DIR = os.path.join(HERE, "_lib")
 SOURCES = ["pkv_abi.cu", "pa_decode_f32.cu", "pa_decode_f16.cu", "pa_decode_bf16.cu",
            "pkv_static_ws.cu", "pkv_plan.cu", "pkv_usage.cu", "pkv_block_pool.cu",
-           "q8_cache.cu", "block_select.cu", "list_attention.cu", "q4_cache.cu", "q4_attention.cu"]
+           "q8_cache.cu", "block_select.cu", "list_attention.cu", "q4_cache.cu", "q4_attention.cu",
+           "q4_attention_f16.cu", "q4_attention_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -206,7 +206,7 @@ __device__ __forceinline__ void q4_mma_first(float (&d)[4], const uint32_t (&a)[
 
 // A wait that did not end at once: until the phase completes for every lane, or
 // one gives up.  Kept out of the loops that wait.
-__device__ __noinline__ bool q4_wait(uint64_t *bar, uint32_t phase)
+static __device__ __noinline__ bool q4_wait(uint64_t *bar, uint32_t phase)
 {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, phase));
 }

@@ -524,3 +524,24 @@ def test_bad_block_in_a_row_of_several_chunks(where):
         for _ in range(5):
             got, st = run_decode(c, P)
             assert st == pkv.DEV_BAD_BLOCK and (got[0] == 0).all() and (got[1] != 0).all()
+
+
+def test_rows_of_zeros():
+    """A fresh cache (zeros: scales, minima and codes), one whose tokens are zeros in part, and values of zeros under keys
+    that are not."""
+    for G in (3, 8):
+        c = S.q4_case(20, t="f16", G=G, Hk=2, lens=(900, 70))
+        for n in ("kv", "v", "half"):
+            for x in ("k", "v") if n == "kv" else ("v",):
+                u, s, m = (a.copy() for a in c[x + "_parts"])
+                hit = np.ones(s.shape, bool) if n != "half" else np.arange(s.shape[2])[None, None, :, None] % 3 > 0
+                s[np.broadcast_to(hit, s.shape) & ~np.isnan(s)] = 0.0
+                m[np.broadcast_to(hit, m.shape) & ~np.isnan(m)] = 0.0
+                c2 = dict(c)
+                c2[x + "_parts"], c2[x] = (u, s, m), S.pack(u, s, m, torch.float16)
+                for P in (0, 64):
+                    got, st = run_decode(c2, P)
+                    assert st == 0
+                    check(c2, got)
+                    if n == "v" or x == "v" and n == "kv":
+                        assert (got == 0).all()

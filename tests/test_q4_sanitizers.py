@@ -33,10 +33,11 @@ def test_entry_points_host_checks_are_clean_under_ubsan(tmp_path):
                         os.path.join(b.CSRC, src), "-o", obj], check=True, capture_output=True)
         return obj
 
-    # pkv_abi.cu holds what the other two share; the decode units it refers
+    # pkv_abi.cu holds what the others share; the decode units it refers
     # to are not linked in and not called (symbols are bound lazily)
-    with ThreadPoolExecutor(max_workers=3) as ex:
-        objs = list(ex.map(compile_one, ["q4_cache.cu", "q4_attention.cu", "pkv_abi.cu"]))
+    with ThreadPoolExecutor(max_workers=5) as ex:
+        objs = list(ex.map(compile_one, ["q4_cache.cu", "q4_attention.cu", "q4_attention_f16.cu", "q4_attention_bf16.cu",
+                                         "pkv_abi.cu"]))
     lib = str(tmp_path / "libq4_ubsan.so")
     subprocess.run([b.nvcc(), *b.ARCH, "-shared", "-o", lib, *objs], check=True, capture_output=True)
     env = dict(os.environ, CUDA_VISIBLE_DEVICES="", LD_PRELOAD=ubsan, UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1")
