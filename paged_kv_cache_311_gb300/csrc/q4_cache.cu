@@ -34,16 +34,20 @@ int check_rows(const Q4RowsParams &p, int head_dim, int block_size, int elem_byt
 }
 
 // Tokens per CTA: what it takes at a time (its rows over the token's, at least
-// one token), then times two while that leaves 16 CTAs per SM.
+// one token), then times two while that leaves two CTAs per SM, until a thread
+// has the `ahead` rows that it holds in flight; further while it leaves 16.  (us,
+// write and read: 8000 tokens of 8 heads of 128 10.2 and 6.9, with 16 CTAs per SM
+// from the start 13.0 and 9.4; prompts of 12.0K tokens of 40 heads 58.7 and 50.4
+// either way, 63.8 and 55.0 where four CTAs per SM are enough throughout.)
 template <typename K>
-int launch(K kern, Q4RowsParams p, int rows_per_cta, cudaStream_t stream)
+int launch(K kern, Q4RowsParams p, int rows_per_cta, int ahead, cudaStream_t stream)
 {
     const int rows = 2 * p.num_kv_heads;
     const int64_t y = ((int64_t)rows + rows_per_cta - 1) / rows_per_cta;
-    const int64_t enough = 16LL * device_sm_count();
+    const int64_t sms = device_sm_count();
     p.step = rows < rows_per_cta ? rows_per_cta / rows : 1;
     int64_t tokens = p.step;
-    while (tokens < p.num_tokens && (p.num_tokens / (2 * tokens) + 1) * y > enough)
+    while (tokens < p.num_tokens && (p.num_tokens / (2 * tokens) + 1) * y > (2 * tokens <= (int64_t)ahead * p.step ? 2 : 16) * sms)
         tokens *= 2;
     p.tokens_per_cta = (int)(tokens < p.num_tokens ? tokens : p.num_tokens);
     const unsigned x = (unsigned)((p.num_tokens + (int64_t)p.tokens_per_cta - 1) / p.tokens_per_cta);
@@ -55,9 +59,9 @@ int write_block(const Q4RowsParams &p, int bs, cudaStream_t s)
 {
     constexpr int rows = kQ4Threads / Q4Writer<T, D, 8>::LPR;
     switch (bs) {
-    case 8: return launch(reshape_and_cache_q4_kernel<T, D, 8>, p, rows, s);
-    case 16: return launch(reshape_and_cache_q4_kernel<T, D, 16>, p, rows, s);
-    default: return launch(reshape_and_cache_q4_kernel<T, D, 32>, p, rows, s);
+    case 8: return launch(reshape_and_cache_q4_kernel<T, D, 8>, p, rows, kQ4WriteAhead, s);
+    case 16: return launch(reshape_and_cache_q4_kernel<T, D, 16>, p, rows, kQ4WriteAhead, s);
+    default: return launch(reshape_and_cache_q4_kernel<T, D, 32>, p, rows, kQ4WriteAhead, s);
     }
 }
 
@@ -66,9 +70,9 @@ int gather_block(const Q4RowsParams &p, int bs, cudaStream_t s)
 {
     constexpr int rows = kQ4Threads / Q4Reader<T, O, D, 8>::LPR;
     switch (bs) {
-    case 8: return launch(gather_cache_q4_kernel<T, O, D, 8>, p, rows, s);
-    case 16: return launch(gather_cache_q4_kernel<T, O, D, 16>, p, rows, s);
-    default: return launch(gather_cache_q4_kernel<T, O, D, 32>, p, rows, s);
+    case 8: return launch(gather_cache_q4_kernel<T, O, D, 8>, p, rows, kQ4ReadAhead, s);
+    case 16: return launch(gather_cache_q4_kernel<T, O, D, 16>, p, rows, kQ4ReadAhead, s);
+    default: return launch(gather_cache_q4_kernel<T, O, D, 32>, p, rows, kQ4ReadAhead, s);
     }
 }
 

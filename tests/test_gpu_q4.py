@@ -545,3 +545,27 @@ def test_rows_of_zeros():
                     check(c2, got)
                     if n == "v" or x == "v" and n == "kv":
                         assert (got == 0).all()
+
+
+@pytest.mark.parametrize("T", [1823, 1824, 3647, 3649, 7301])
+@pytest.mark.parametrize("D,Hk", [(64, 5), (128, 8)])
+def test_write_and_read_between(D, Hk, T):
+    """Calls at which CTAs begin to take two, four and eight times their rows: the records that parts of the same
+    rows leave, and the numbers that parts of the same slots give."""
+    rng = np.random.RandomState(T + D)
+    g = torch.Generator(device=DEV).manual_seed(T)
+    NB = -(-T // 16) + 1
+    slots = rng.permutation(NB * 16)[:T]
+    slots[rng.rand(T) < 0.05] = -1
+    at = dev(slots)
+    key, value = (torch.randn(T, Hk, D, generator=g, device=DEV).to(torch.bfloat16) for _ in "kv")
+    whole, parts = [[cache(NB, Hk, 16, D) for _ in "kv"] for _ in range(2)]
+    pkv.reshape_and_cache_q4(key, value, *whole, at)
+    for i in range(0, T, 200):
+        pkv.reshape_and_cache_q4(key[i: i + 200], value[i: i + 200], *parts, at[i: i + 200])
+    assert all(torch.equal(a, b) for a, b in zip(whole, parts))
+    out, rest = [[torch.full((T, Hk, D), 7.0, dtype=torch.bfloat16, device=DEV) for _ in "kv"] for _ in range(2)]
+    pkv.gather_cache_q4(*out, *whole, at)
+    for i in range(0, T, 200):
+        pkv.gather_cache_q4(rest[0][i: i + 200], rest[1][i: i + 200], *whole, at[i: i + 200])
+    assert all(torch.equal(a, b) for a, b in zip(out, rest))
