@@ -53,6 +53,18 @@ namespace pkv {
 // there is none yet, so that 2^(-inf - reference) is 0 and not NaN.
 __device__ __forceinline__ float reference_of(float m) { return m == -INFINITY ? 0.f : m; }
 
+// What takes sums from reference m to ref, 2^(m - ref), m <= ref.  WIDE: as the
+// square of its root.  Over a 4-bit cache a reference counts the values' scales,
+// so that a sum of weights may be near 2^115 and the factor below fp32's last
+// bit while their product is an ordinary number.
+template <bool WIDE> struct Shift {
+    float f;   // WIDE: the root
+    __device__ __forceinline__ Shift(float m, float ref) : f(WIDE ? ex2_fast(fmaf(0.5f, m, -0.5f * ref)) : exp2f(m - ref)) {}
+    __device__ __forceinline__ float factor() const { return WIDE ? f * f : f; }   // for sums of values, which it may make 0
+    __device__ __forceinline__ float of(float sum) const { return WIDE ? f * (f * sum) : f * sum; }
+    __device__ __forceinline__ float add(float sum, float acc) const { return fmaf(f, WIDE ? f * sum : sum, acc); }   // acc + of(sum)
+};
+
 struct ListParams {
     void *out;
     const void *q;
@@ -210,7 +222,7 @@ struct ListResult {
 // Writes the CTA's result where it goes: the output (one partition, or a
 // cluster, which all CTAs of it have to reach) or the workspace.  All threads
 // call it after a barrier behind the result's last store.
-template <int D>
+template <int D, bool WIDE = false>
 __device__ __forceinline__ void write_result(const ListParams &p, ListResult<D> *res, int seq, int kvh, int part)
 {
     const int64_t head0 = ((int64_t)seq * p.num_kv_heads + kvh) * p.group;
@@ -244,8 +256,9 @@ __device__ __forceinline__ void write_result(const ListParams &p, ListResult<D> 
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 if (l[k] != 0.f) {   // else its sums of values were not stored
-                    const float f = exp2f(m[k] - ref);
-                    den += f * l[k];
+                    const Shift<WIDE> by(m[k], ref);
+                    const float f = by.factor();
+                    den = by.add(l[k], den);
                     num.x += f * a[k].x;
                     num.y += f * a[k].y;
                     num.z += f * a[k].z;
@@ -747,7 +760,7 @@ list_attention_kernel(const __grid_constant__ ListParams p, const __grid_constan
 // row is zero.
 constexpr int kMergeWarps = 8;
 
-template <int D>
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(kMergeWarps * 32)
 list_merge_kernel(const __grid_constant__ ListParams p, int per_head)
 {
@@ -791,16 +804,18 @@ list_merge_kernel(const __grid_constant__ ListParams p, int per_head)
             bad |= t[u].y < 0.f;
         }
         const float ref = reference_of(mn);
-        const float f0 = exp2f(mx - ref);
-        den *= f0;
+        const Shift<WIDE> before(mx, ref);
+        const float f0 = before.factor();
+        den = before.of(den);
 #pragma unroll
         for (int i = 0; i < N; ++i)
             num[i] *= f0;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (t[u].y != 0.f) {
-                const float f = exp2f(t[u].x - ref);
-                den += f * t[u].y;
+                const Shift<WIDE> by(t[u].x, ref);
+                const float f = by.factor();
+                den = by.add(t[u].y, den);
                 num[0] += f * a[u].x;
                 num[1] += f * a[u].y;
                 if constexpr (N == 4) {
@@ -839,9 +854,10 @@ list_merge_kernel(const __grid_constant__ ListParams p, int per_head)
         for (int i = 0; i < N; ++i)
             num[i] = 0.f;
         for (int w = warp; w < warp + per_head; ++w) {
-            const float f = exp2f(s_m[w] - ref);
+            const Shift<WIDE> by(s_m[w], ref);
+            const float f = by.factor();
             const V x = s_acc[w][lane];
-            den += f * s_l[w];
+            den = by.add(s_l[w], den);
             num[0] += f * x.x;
             num[1] += f * x.y;
             if constexpr (N == 4) {

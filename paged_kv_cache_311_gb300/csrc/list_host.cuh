@@ -66,11 +66,11 @@ inline bool list_layout(uint64_t seqs, uint64_t heads, uint64_t np, uint64_t hea
     return true;
 }
 
-template <int D>
+template <int D, bool WIDE = false>
 int launch_list_merge(const ListParams &p, cudaStream_t stream)
 {
     static unsigned long long merge_done = 0;
-    const int rc = ensure_smem_attr(reinterpret_cast<const void *>(list_merge_kernel<D>), 0, &merge_done);
+    const int rc = ensure_smem_attr(reinterpret_cast<const void *>(list_merge_kernel<D, WIDE>), 0, &merge_done);
     if (rc)
         return rc;
     // a warp for each head where the heads fill the GPU, else several
@@ -78,7 +78,7 @@ int launch_list_merge(const ListParams &p, cudaStream_t stream)
     int per_head = 1;
     while (per_head < kMergeWarps && per_head * 8 < p.np && heads * per_head * 2 <= 32LL * device_sm_count())
         per_head *= 2;
-    return launch_pdl(list_merge_kernel<D>, dim3((unsigned)((heads * per_head + kMergeWarps - 1) / kMergeWarps)),
+    return launch_pdl(list_merge_kernel<D, WIDE>, dim3((unsigned)((heads * per_head + kMergeWarps - 1) / kMergeWarps)),
                       dim3(kMergeWarps * 32), 0, stream, p, per_head);
 }
 

@@ -479,9 +479,10 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
         }
         t = make_float2(fmaxf(m.x, t.x), fmaxf(m.y, t.y));
         const float2 ref = make_float2(reference_of(t.x), reference_of(t.y));
-        const float2 alpha = make_float2(ex2_fast(m.x - ref.x), ex2_fast(m.y - ref.y));
+        const Shift<true> sx(m.x, ref.x), sy(m.y, ref.y);
+        const float2 alpha = make_float2(sx.factor(), sy.factor());
         m = t;
-        lsum = fmul2(lsum, alpha);
+        lsum = make_float2(sx.of(lsum.x), sy.of(lsum.y));
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
             om[j] = fmul2(om[j], alpha);
@@ -713,7 +714,7 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
                 res->l[threadIdx.x] = refused ? -1.f : 0.f;
             }
             __syncthreads();
-            write_result<D>(p, res, seq, head, blockIdx.x);
+            write_result<D, true>(p, res, seq, head, blockIdx.x);
             return;
         }
     }
@@ -894,7 +895,8 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
 #pragma unroll
                 for (int w = 0; w < NW; ++w) {
                     if (t[w].y != 0.f) {   // else the warp had no token; NaN sums stay
-                        const float f = ex2_fast(t[w].x - ref);
+                        const Shift<true> by(t[w].x, ref);
+                        const float f = by.factor();
                         const float *aw = reinterpret_cast<const float *>(smem + (w * S + slot[w]) * C::STAGE_BYTES) + r * C::AWS + d;
                         float4 x = *reinterpret_cast<const float4 *>(aw);
                         if constexpr (TWICE) {
@@ -905,7 +907,7 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
                         num.y = fmaf(f, x.y, num.y);
                         num.z = fmaf(f, x.z, num.z);
                         num.w = fmaf(f, x.w, num.w);
-                        den = fmaf(f, t[w].y, den);
+                        den = by.add(t[w].y, den);
                     }
                 }
                 if (!a.shares) {
@@ -941,7 +943,7 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
         }
     }
     if (!a.shares) {
-        write_result<D>(p, res, seq, head, blockIdx.x);
+        write_result<D, true>(p, res, seq, head, blockIdx.x);
         if (p.np > 1 && !p.cluster)
             asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     } else {
@@ -1005,8 +1007,9 @@ q4_merge_kernel(const __grid_constant__ Q4Params a)
     bool bad = false;
     auto join = [&](const float2 &t, const float4 &x, float ref) {
         if (t.y != 0.f) {
-            const float f = exp2f(t.x - ref);
-            den += f * t.y;
+            const Shift<true> by(t.x, ref);
+            const float f = by.factor();
+            den = by.add(t.y, den);
             num.x += f * x.x;
             num.y += f * x.y;
             num.z += f * x.z;
@@ -1032,8 +1035,10 @@ q4_merge_kernel(const __grid_constant__ Q4Params a)
             mn = fmaxf(mn, t[u].x);
             bad |= t[u].y < 0.f;
         }
-        const float ref = reference_of(mn), f0 = exp2f(mx - ref);
-        den *= f0;
+        const float ref = reference_of(mn);
+        const Shift<true> before(mx, ref);
+        const float f0 = before.factor();
+        den = before.of(den);
         num = make_float4(num.x * f0, num.y * f0, num.z * f0, num.w * f0);
 #pragma unroll
         for (int u = 0; u < U; ++u)

@@ -46,7 +46,7 @@ int run_q4(const Q4Params &p, cudaStream_t stream)
         const int threads = many ? kQ4MergeThreads : p.list.group * (D / 4) <= 128 ? 128 : 256;
         return launch_pdl(q4_merge_kernel<D>, dim3((unsigned)p.shares), dim3(threads), 0, stream, p);
     }
-    return p.list.np > 1 && !p.list.cluster ? launch_list_merge<D>(p.list, stream) : PKV_OK;
+    return p.list.np > 1 && !p.list.cluster ? launch_list_merge<D, true>(p.list, stream) : PKV_OK;
 }
 
 template <typename T, int D, int BS>
