@@ -223,6 +223,9 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
     static constexpr float kMost = 32768.f;      // of a weight times its scale
     static constexpr float kLift = 7.f;          // log2 of the largest one where the reference is set
     static constexpr float kLeast = 0x1p-100f;   // smaller scales count as this: weights stay below 2^115
+    // What sums of weights and of values are kept in: 2^25 such weights stay below
+    // 2^128, and one beside a scale of 2^123 (2^-116 of it) above 2^-128.
+    static constexpr float kSums = 0x1p-12f;
 
     uint32_t qf[NG][4][2];   // q^T B-fragments of head g: group, step
     // a float2 is of heads 2c, 2c + 1
@@ -230,7 +233,7 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
     float2 fm[NG];           // sum(q_j), in the same units as q . u
     float o[NG][4][4];       // O^T C-fragments: group, m-tile
     float2 om[NG];           // this lane's tokens' sums of w m
-    float2 m, lsum;          // weights' reference and sum
+    float2 m, lsum;          // weights' reference and sum, times kSums
     uint32_t nums;           // this warp's numbers in shared memory
     int kcode[2], vcode[4];  // byte offsets of this lane's tokens of K and of V in a stage's records
     int mine;                // of the pairs of the token that this lane makes numbers of
@@ -519,7 +522,7 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int n = 2 * tile + i;
-            lsum = fadd2(lsum, p[n]);
+            lsum = ffma2(p[n], make_float2(kSums, kSums), lsum);
 #pragma unroll
             for (int j = 0; j < NG; ++j) {
                 float2 s, mn;
@@ -591,8 +594,8 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
         ++steps;
     }
 
-    // This warp's reference, sum and sums of values of the heads below `group`:
-    // ml [kListMaxGroup][2], aw [kListMaxGroup][AWS].
+    // This warp's reference, sum and sums of values of the heads below `group`,
+    // the sums times kSums: ml [kListMaxGroup][2], aw [kListMaxGroup][AWS].
     __device__ __forceinline__ void finish(float2 *ml, float *aw, int group)
     {
 #pragma unroll
@@ -603,7 +606,7 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
             l += __shfl_xor_sync(0xffffffffu, l, 16);
 #pragma unroll
             for (int j = 0; j < NG; ++j) {
-                add[j] = h ? om[j].y : om[j].x;
+                add[j] = (h ? om[j].y : om[j].x) * kSums;
                 add[j] += __shfl_xor_sync(0xffffffffu, add[j], 4);
                 add[j] += __shfl_xor_sync(0xffffffffu, add[j], 8);
                 add[j] += __shfl_xor_sync(0xffffffffu, add[j], 16);
@@ -623,7 +626,7 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt)
                         *reinterpret_cast<float2 *>(dst + 64 * j + 2 * mt) =
-                            make_float2(fmaf(o[j][mt][h], 16777216.f, add[j]), fmaf(o[j][mt][2 + h], 1048576.f, add[j]));
+                            make_float2(fmaf(o[j][mt][h], 16777216.f * kSums, add[j]), fmaf(o[j][mt][2 + h], 1048576.f * kSums, add[j]));
                 }
             }
         }

@@ -139,3 +139,25 @@ def test_sizes_and_scores_of_all_kinds(seed):
         score += [rng.uniform(-16, 16)] * n
         tops += [0.0 if rng.rand() < 0.5 else 2.0 ** rng.uniform(-60, 80)] * n
     check(scored(seed, t="bf16", D=(64, 128)[seed % 2], bs=(8, 16, 32)[seed % 3], G=1 + seed, Hk=2, score=score, top=tops))
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("D,G,first", [(64, 1, 5.4375), (128, 2, 4.8125), (64, 8, 2.90625)])
+@pytest.mark.parametrize("zeros", [65536, 400000])
+def test_sums_of_many_large_weights(t, D, G, first, zeros):
+    """Tokens of zeros whose scores lie just below the step that would move the reference (7.86, log2, above the first
+    ones'; the head with the largest): the most that a weight can be, 65,536 and 400,000 times, before a token whose
+    value counts."""
+    score, tops = np.full(zeros + 1, first), np.zeros(zeros + 1)
+    score[:128] = 0.0                                       # the first unit of each warp
+    score[-1], tops[-1] = first + np.log(zeros), 1000.0
+    whole = (zeros // 32 * 32 + 32, None)
+    check(scored(zeros, t=t, D=D, bs=32, G=G, Hk=1, score=score, top=tops), [whole, (2048, None), (0, None)])
+
+
+def test_values_near_the_largest():
+    """Scales of V from 2^80 to 2^122, where a weight is next to nothing and has to stay a number: sums of weights are
+    kept scaled down."""
+    for e in (80, 100, 115, 122):
+        for n in (1, 40, 500):
+            check(scored(e, t="bf16", D=128, bs=16, G=3, Hk=2, score=np.linspace(0, 3, n), top=np.full(n, 15 * 2.0 ** e)))
