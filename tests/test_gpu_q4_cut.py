@@ -1,0 +1,91 @@
+"""Decode attention over a 4-bit cache where its work is cut: shares of several
+chunks, rows that begin and end anywhere in them, partitions of every size.  The
+rows' values have a level of their own for each stretch of tokens, the tolerance
+is checked against what a lost piece would change."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_311_gb300 as pkv
+from tests.q4_cut import UNIT, Rows, all_chunks
+from tests.test_q4_cut import RAGGED
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def check_row(rows, s, got, additions, pieces=None):
+    """Sequence s's outputs [Hk, G, D], and that they would be refused without any of its pieces: {head: [(first unit,
+    units)]}, each whole unit if none are given.  A piece that changes the exact output by more than twice the tolerance
+    is missed by an output that lacks it and is itself off by no more than the tolerance."""
+    den, num = rows.sums(s)
+    want = num.sum(2) / den.sum(2)[..., None]
+    tol = rows.tolerance(s, additions)
+    off = (got.double() - want).abs()
+    assert bool((off <= tol).all()), (s, float((off / tol).max()))
+    if den.shape[2] == 1:
+        return
+    if pieces is None:
+        without = (num.sum(2, keepdim=True) - num) / (den.sum(2, keepdim=True) - den)[..., None]
+        tells = ((without - want[:, :, None]).abs() > 2 * tol[:, :, None]).any(-1)
+        assert bool(tells[..., : rows.lens[s] // UNIT].all()), s
+        return
+    den0, num0 = (torch.nn.functional.pad(x.cumsum(2), p) for x, p in ((den, (1, 0)), (num, (0, 0, 1, 0))))
+    for h, cuts in pieces.items():
+        for u, n in cuts:
+            if n == den.shape[2]:
+                continue
+            d = den0[h, :, -1] - (den0[h, :, u + n] - den0[h, :, u])
+            x = num0[h, :, -1] - (num0[h, :, u + n] - num0[h, :, u])
+            assert bool(((x / d[:, None] - want[h]).abs() > 2 * tol[h]).any(-1).all()), (s, h, u, n)
+
+
+def ragged(dtype, D, seed):
+    return Rows(pkv, seed, RAGGED, dtype=dtype, Hk=32, G=1 if D == 128 else 3, D=D, bs=16 if D == 128 else 8)
+
+
+@pytest.mark.parametrize("dtype,D", [(torch.float16, 128), (torch.bfloat16, 128), (torch.bfloat16, 64)])
+def test_shares_of_many_short_rows(dtype, D):
+    """Shares longer than a chunk over rows shorter than one: chunks end in front of a row, rows begin in one chunk and go on
+    in the next.  Every unit of every row counts."""
+    found = [how for share in all_chunks(RAGGED, 32, sms()) for _, how in share]
+    assert found.count("row") >= 20
+    rows = ragged(dtype, D, 1)
+    got, st = rows.decode(most=2080)                        # past 2048 tokens rows are not left whole
+    assert st == 0
+    for s in range(len(RAGGED)):
+        check_row(rows, s, got[s], 64 + 16)
+
+
+@pytest.mark.parametrize("D", [128, 64])
+def test_bad_blocks_at_the_borders_of_chunks(D):
+    """Sequences with a row that goes on in the next chunk, or in front of which one ends, get a bad block in the piece
+    before the border, behind it, or at the row's end: all their rows are zero, all others as without."""
+    rows = ragged(torch.bfloat16, D, 2)
+    good, st = rows.decode(most=2080)
+    assert st == 0
+    where = {}
+    for share in all_chunks(RAGGED, 32, sms()):
+        for (pieces, how), (after, _) in zip(share, share[1:]):
+            s, h, u, n = pieces[-1]
+            s1, _, u1, n1 = after[0]
+            if (s, h) == after[0][:2]:
+                where.setdefault(s, []).extend([u + n - 1, u1, u1 + n1 - 1])
+            elif how == "row":
+                where.setdefault(s1, []).extend([0, n1 - 1])
+    assert len(where) >= 20
+    rng = np.random.RandomState(3)
+    for hurt in (sorted(where)[::3], sorted(where)[1::5]):
+        tables = rows.tables.clone()
+        for s in hurt:
+            unit = where[s][rng.randint(len(where[s]))]
+            last = -(-int(RAGGED[s]) // rows.bs) - 1
+            tables[s, min(last, unit * UNIT // rows.bs + rng.randint(UNIT // rows.bs))] = [-1, rows.NB][rng.randint(2)]
+        got, st = rows.decode(most=2080, tables=tables)
+        assert st == pkv.DEV_BAD_BLOCK
+        rest = [s for s in range(len(RAGGED)) if s not in hurt]
+        assert not got[hurt].any() and torch.equal(got[rest], good[rest])
