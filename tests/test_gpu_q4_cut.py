@@ -89,3 +89,30 @@ def test_bad_blocks_at_the_borders_of_chunks(D):
         assert st == pkv.DEV_BAD_BLOCK
         rest = [s for s in range(len(RAGGED)) if s not in hurt]
         assert not got[hurt].any() and torch.equal(got[rest], good[rest])
+
+
+@pytest.mark.parametrize("dtype,bs,G", [(torch.bfloat16, 32, 1), (torch.float16, 8, 4)])
+def test_long_rows_in_shares_of_many_chunks(dtype, bs, G):
+    """One context of 131,067 tokens, 64 kv heads: a share is some 575 units, its chunks end inside rows. A chunk's part of a
+    row would be missed, and so would a share's."""
+    L, Hk = 131067, 64
+    rows = Rows(pkv, 4, [L], dtype=dtype, Hk=Hk, G=G, D=64, bs=bs, stretch=1024)
+    got, st = rows.decode()
+    assert st == 0
+    pieces, most = {}, 0
+    for share in all_chunks([L], Hk, sms()):
+        most = max(most, sum(p[3] for c, _ in share for p in c))
+        whole = {}
+        for chunk, _ in share:
+            for _, h, u, n in chunk:
+                pieces.setdefault(h, []).append((u, n))
+                first, so_far = whole.get(h, (u, 0))
+                whole[h] = (first, so_far + n)
+        for h, (u, n) in whole.items():
+            pieces[h].append((u, n))
+    assert most > 4 * 128 and len(pieces) == Hk
+    # pieces of a few units next to a row's end tell less than a tolerance does
+    pieces = {h: [p for p in cuts if p[1] >= 64] for h, cuts in pieces.items()}
+    assert all(pieces.values())
+    # a lane adds four tokens of each fourth unit; the merge adds the parts of a row, at most eight here
+    check_row(rows, 0, got[0], most + 16, pieces)
