@@ -116,3 +116,20 @@ def test_long_rows_in_shares_of_many_chunks(dtype, bs, G):
     assert all(pieces.values())
     # a lane adds four tokens of each fourth unit; the merge adds the parts of a row, at most eight here
     check_row(rows, 0, got[0], most + 16, pieces)
+
+
+@pytest.mark.parametrize("dtype,D,bs,G", [(torch.bfloat16, 128, 8, 4), (torch.float16, 64, 32, 8), (torch.bfloat16, 128, 16, 1)])
+@pytest.mark.parametrize("lens,P", [((5000,), 0), ((5000,), 32), ((5000,), 1024), ((9000, 3), 0), ((9000, 3), 64), ((9000, 3), 4096),
+                                    ((2, 4097, 1, 2049), 0), ((2, 4097, 1, 2049), 32), ((60000,), 60000), ((60000,), 2048), ((60000,), 0)])
+def test_rows_of_thousands_of_tokens(dtype, D, bs, G, lens, P):
+    """Few long rows: clusters, partitions through the workspace, one CTA, shares. Without any partition's (or each
+    eighth of the row, where the cut is the library's) part of a row its output would be refused."""
+    rows = Rows(pkv, 5, lens, dtype=dtype, Hk=1, G=G, D=D, bs=bs, stretch=max(UNIT, (P or 256) // 4 // UNIT * UNIT))
+    got, st = rows.decode(P=P)
+    assert st == 0
+    for s, L in enumerate(lens):
+        units = -(-L // UNIT)
+        part = P // UNIT if P else -(-units // 8)
+        cuts = [(u, min(part, units - u)) for u in range(0, units, part)]
+        # a lane's additions of a part (four tokens of each fourth unit), and those of the parts
+        check_row(rows, s, got[s], part + len(cuts) + 16, {0: [c for c in cuts if c[1] * UNIT * 64 >= L]})
