@@ -774,6 +774,23 @@ int pkv_test_bounded_wait(uint64_t limit_ns, uint64_t max_polls, uint32_t *devic
 int pkv_test_select_timeout(int what, uint64_t limit_ns, int32_t *selected, int num_selected,
                             uint32_t *device_status, void *stream);
 
+/*
+ * Test hook of pkv_paged_attention_decode_q4's waits, as above: that call over
+ * a cache of PKV_BF16 with head_dim 64, blocks of 16 and up to four query heads
+ * a kv head, out PKV_F32, of which the copies of one step are never issued: the
+ * unit'th (from 0) of 32 tokens that warp `warp` (0 .. 3) of CTA `cta` (of the
+ * launch's, in their order; one that is not there: nothing is lost) takes. Its
+ * wait gives up after limit_ns (1 .. 2e9), other copies of the warp are waited
+ * for, and the rows that the CTA still has a part in become zero; *device_status
+ * (required) receives PKV_DEV_TIMEOUT | PKV_DEV_DRAIN_TIMEOUT.
+ */
+int pkv_test_q4_timeout(uint64_t limit_ns, int cta, int warp, int unit, float *out, const void *q,
+                        const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                        int max_blocks_per_seq, const int32_t *context_lens, int num_seqs,
+                        int num_heads, int num_kv_heads, int64_t num_blocks, int max_context_len,
+                        float scale, int partition_size, void *workspace, size_t workspace_bytes,
+                        uint32_t *device_status, void *stream);
+
 /* Number of kernels the last successful pkv_paged_attention_decode call on
  * this host thread enqueued (1 = single pass, 2 = partition pass + reduce). */
 int pkv_last_decode_launches(void);

@@ -40,7 +40,7 @@ __all__ = [
     "set_decode_engine", "last_decode_engine", "kv_cache_usage", "KvCacheUsage", "swap_blocks",
     "SWAP_OUT", "SWAP_IN", "BlockPool",
     "DEV_BAD_BLOCK", "DEV_BAD_SLOT", "DEV_TIMEOUT", "DEV_BAD_CONTEXT_LEN", "DEV_DRAIN_TIMEOUT",
-    "HEADER_PATH", "bounded_wait_hook", "select_timeout_hook",
+    "HEADER_PATH", "bounded_wait_hook", "select_timeout_hook", "q4_timeout_hook",
     "append_cache_q8", "summarize_blocks", "select_blocks", "paged_attention_decode_q8",
     "paged_attention_decode_selected", "paged_attention_list_workspace_bytes", "q8_scales",
     "select_blocks_workspace_bytes", "q4_cache", "reshape_and_cache_q4", "gather_cache_q4",
@@ -168,6 +168,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     L.pkv_test_select_timeout.argtypes = [i32, ctypes.c_uint64, vp, i32, vp, vp]
     L.pkv_test_select_timeout.restype = i32
     L.pkv_test_bounded_wait.restype = i32
+    L.pkv_test_q4_timeout.argtypes = [ctypes.c_uint64, i32, i32, i32, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i64, i32, f32,
+                                      i32, vp, u64, vp, vp]
+    L.pkv_test_q4_timeout.restype = i32
     if path is None:
         _lib = L
     return L
@@ -531,6 +534,24 @@ def select_timeout_hook(what: int, selected: torch.Tensor, device_status: torch.
         raise ValueError("selected must be int32")
     _check(load_library().pkv_test_select_timeout(int(what), int(limit_ns), _ptr(selected), selected.numel(),
                                                   _ptr(device_status), _stream(stream)), "pkv_test_select_timeout")
+
+
+def q4_timeout_hook(cta: int, warp: int, unit: int, out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                    v_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                    device_status: torch.Tensor, limit_ns: int, *, max_context_len: int, partition_size: int = 0,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Test hook: paged_attention_decode_q4 with a step whose copies never come
+    (see pkv_test_q4_timeout). q: bfloat16 [B, H, 64], out: float32, blocks of 16."""
+    _need_cuda(out, q, k_cache, v_cache, block_tables, context_lens, device_status)
+    B, H, D = q.shape
+    NB, Hk, bs, row = k_cache.shape
+    if q.dtype != torch.bfloat16 or out.dtype != torch.float32 or (D, bs, row) != (64, 16, 36) or v_cache.shape != k_cache.shape:
+        raise ValueError("the hook takes bfloat16, heads of 64 and blocks of 16")
+    _check(load_library().pkv_test_q4_timeout(
+        int(limit_ns), cta, warp, unit, _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+        int(block_tables.shape[1]), _ptr(context_lens), B, H, Hk, NB, int(max_context_len), float(scale), partition_size,
+        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(device_status),
+        _stream(stream)), "pkv_test_q4_timeout")
 
 
 def reshape_and_cache(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,

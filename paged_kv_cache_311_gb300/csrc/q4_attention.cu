@@ -72,30 +72,13 @@ bool q4_layout(const Q4Cut &c, uint64_t seqs, uint64_t heads, uint64_t kv_heads,
     return true;
 }
 
-}  // namespace
-}  // namespace pkv
-
-using namespace pkv;
-
-extern "C" {
-
-size_t pkv_paged_attention_q4_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
-                                              int max_context_len, int partition_size)
-{
-    if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_dim <= 0 ||
-        block_size <= 0 || block_size > 32 || max_context_len < 0 || partition_size < 0 || partition_size % kQ4Unit)
-        return 0;
-    Q4Layout lay;
-    const Q4Cut cut = q4_cut((long long)num_seqs * num_kv_heads, max_context_len, block_size, partition_size);
-    return q4_layout(cut, num_seqs, num_heads, num_kv_heads, head_dim, &lay) ? lay.total : 0;
-}
-
-int pkv_paged_attention_decode_q4(void *out, int out_dtype, const void *q, int64_t q_stride, int q_dtype,
-                                  const void *k_cache, const void *v_cache, const int32_t *block_tables,
-                                  int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_heads,
-                                  int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
-                                  int max_context_len, float scale, int partition_size, void *workspace,
-                                  size_t workspace_bytes, uint32_t *device_status, void *stream)
+// pkv_paged_attention_decode_q4; `lost`: the test hook's.
+int decode_q4(void *out, int out_dtype, const void *q, int64_t q_stride, int q_dtype,
+              const void *k_cache, const void *v_cache, const int32_t *block_tables,
+              int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_heads,
+              int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+              int max_context_len, float scale, int partition_size, void *workspace,
+              size_t workspace_bytes, uint32_t *device_status, void *stream, const Q4Lost *lost)
 {
     if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_dim <= 0 ||
         num_blocks <= 0 || num_blocks > INT32_MAX || max_blocks_per_seq <= 0 || block_size <= 0 ||
@@ -156,7 +139,55 @@ int pkv_paged_attention_decode_q4(void *out, int out_dtype, const void *q, int64
     l.qscale = scale * 1.4426950408889634f;
     p.q_stride = q_stride;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (lost) {
+        p.lost = *lost;
+        return launch_q4_lost(p, s);
+    }
     return q_dtype == PKV_F16 ? launch_q4_f16(p, head_dim, block_size, s) : launch_q4_bf16(p, head_dim, block_size, s);
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+size_t pkv_paged_attention_q4_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                              int max_context_len, int partition_size)
+{
+    if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_dim <= 0 ||
+        block_size <= 0 || block_size > 32 || max_context_len < 0 || partition_size < 0 || partition_size % kQ4Unit)
+        return 0;
+    Q4Layout lay;
+    const Q4Cut cut = q4_cut((long long)num_seqs * num_kv_heads, max_context_len, block_size, partition_size);
+    return q4_layout(cut, num_seqs, num_heads, num_kv_heads, head_dim, &lay) ? lay.total : 0;
+}
+
+int pkv_paged_attention_decode_q4(void *out, int out_dtype, const void *q, int64_t q_stride, int q_dtype,
+                                  const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                                  int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_heads,
+                                  int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                                  int max_context_len, float scale, int partition_size, void *workspace,
+                                  size_t workspace_bytes, uint32_t *device_status, void *stream)
+{
+    return decode_q4(out, out_dtype, q, q_stride, q_dtype, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                     num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, max_context_len, scale,
+                     partition_size, workspace, workspace_bytes, device_status, stream, nullptr);
+}
+
+int pkv_test_q4_timeout(uint64_t limit_ns, int cta, int warp, int unit, float *out, const void *q, const void *k_cache,
+                        const void *v_cache, const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                        int num_seqs, int num_heads, int num_kv_heads, int64_t num_blocks, int max_context_len, float scale,
+                        int partition_size, void *workspace, size_t workspace_bytes, uint32_t *device_status, void *stream)
+{
+    if (limit_ns == 0 || limit_ns > kWaitLimitNs || cta < 0 || warp < 0 || warp >= kListWarps || unit < 0 || num_kv_heads <= 0 ||
+        num_heads / num_kv_heads > 4 || !device_status || !aligned(device_status, 4))
+        return PKV_EINVAL;
+    const Q4Lost lost{limit_ns, cta, warp, unit};
+    return decode_q4(out, PKV_F32, q, (int64_t)num_heads * 64, PKV_BF16, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                     context_lens, num_seqs, num_heads, num_kv_heads, 64, 16, num_blocks, max_context_len, scale, partition_size,
+                     workspace, workspace_bytes, device_status, stream, &lost);
 }
 
 }  // extern "C"

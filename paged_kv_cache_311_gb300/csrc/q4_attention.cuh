@@ -60,12 +60,19 @@ struct Q4Share {
     int seq, head, unit, units;
 };
 
+// The test hook's: copies that are left out, and the limit of the waits.
+struct Q4Lost {
+    uint64_t limit_ns;
+    int cta, warp, unit;   // the warp's unit, counted from its first
+};
+
 struct Q4Params {
     ListParams list;             // without selected blocks and scales
     int64_t q_stride;            // elements between two sequences' rows of q
     int shares;                  // streamed: CTAs; else 0
     int part_units;              // tokens / 32 of a partition; 0: a row's, divided by list.np
     Q4Share *ws_share;           // streamed: the shares, for the merge
+    Q4Lost lost;                 // the hook's kernel only
 };
 
 constexpr int kQ4Unit = 32;      // tokens that a warp takes at a time
@@ -209,6 +216,10 @@ __device__ __forceinline__ void q4_mma_first(float (&d)[4], const uint32_t (&a)[
 static __device__ __noinline__ bool q4_wait(uint64_t *bar, uint32_t phase)
 {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, phase));
+}
+static __device__ __noinline__ bool q4_wait(uint64_t *bar, uint32_t phase, uint64_t limit_ns)
+{
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, phase, limit_ns));
 }
 
 // One warp's state.  Lane (g, c) = (lane / 4, lane % 4).
@@ -642,8 +653,9 @@ __device__ __forceinline__ void q4_zero_rows(const ListParams &p, int seq)
         store_out4(p.out, p.out_dtype, seq * heads * D + i, make_float4(0.f, 0.f, 0.f, 0.f));
 }
 
-// Grid: streamed (shares); else (partition, kv head, sequence).
-template <typename T, int D, int BS, bool TWICE>
+// Grid: streamed (shares); else (partition, kv head, sequence).  HOOK: the test
+// hook's kernel, in which a unit's copies are never issued (a.lost).
+template <typename T, int D, int BS, bool TWICE, bool HOOK>
 __global__ void __launch_bounds__(kListThreads, kQ4Ctas)
 q4_attention_kernel(const __grid_constant__ Q4Params a)
 {
@@ -741,6 +753,7 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
     bool whole = unit == 0;     // the row starts here
     int rows = 0;               // rows finished
     bool fresh = true;          // the engine has nothing of the row yet
+    int issued = 0;             // HOOK: units
     Q4Engine<T, D, BS, TWICE> eng;
     eng.nums = smem_u32(smem + C::OFF_NUM + warp * 2 * C::NUMBERS);
 
@@ -794,6 +807,11 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
         // ---- this warp's units of the chunk: warp, warp + NW, ...
         // unit k into a stage
         auto issue = [&](int k, int stage) {
+            if constexpr (HOOK) {
+                const int cta = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+                if (issued++ == a.lost.unit && cta == a.lost.cta && warp == a.lost.warp)
+                    return;
+            }
             const uint8_t *const kc = p.k_cache, *const vc = p.v_cache;
             uint8_t *kd = stages + stage * C::STAGE_BYTES;
             uint64_t *bar = &bars[stage];
@@ -835,10 +853,18 @@ q4_attention_kernel(const __grid_constant__ Q4Params a)
                 int valid = (int)min((int64_t)INT32_MAX, L - (int64_t)(unit + k - at) * kQ4Unit);
                 for (; k <= last && !dead; k += NW) {
                     // the warp gives up as one: its products and shuffles need every lane
-                    if (!__all_sync(0xffffffffu, mbar_try_wait(&bars[stage], phase)) && !q4_wait(&bars[stage], phase)) {
+                    bool came = __all_sync(0xffffffffu, mbar_try_wait(&bars[stage], phase));
+                    if (!came) {
+                        if constexpr (HOOK)
+                            came = q4_wait(&bars[stage], phase, a.lost.limit_ns);
+                        else
+                            came = q4_wait(&bars[stage], phase);
+                    }
+                    if (!came) {
                         // no CTA leaves with loads in flight
                         for (int i = 0; i < S && k + i * NW < chunk; ++i)
-                            drain_wait(&bars[(stage + i) % S], phase ^ (stage + i >= S), lane == 0 ? p.status : nullptr);
+                            drain_wait(&bars[(stage + i) % S], phase ^ (stage + i >= S), lane == 0 ? p.status : nullptr,
+                                       HOOK ? a.lost.limit_ns : kWaitLimitNs);
                         if (lane == 0) {
                             report(p.status, PKV_DEV_TIMEOUT);
                             atomicOr(flag, 1u);

@@ -9,13 +9,14 @@ namespace pkv {
 
 int launch_q4_f16(const Q4Params &p, int head_dim, int block_size, cudaStream_t stream);
 int launch_q4_bf16(const Q4Params &p, int head_dim, int block_size, cudaStream_t stream);
+int launch_q4_lost(const Q4Params &p, cudaStream_t stream);   // the test hook's: bfloat16, heads of 64, blocks of 16, groups up to 4
 
-template <typename T, int D, int BS, bool TWICE>
+template <typename T, int D, int BS, bool TWICE, bool HOOK = false>
 int run_q4(const Q4Params &p, cudaStream_t stream)
 {
     using C = Q4Cfg<D, BS>;
     static unsigned long long done = 0;
-    auto kern = q4_attention_kernel<T, D, BS, TWICE>;
+    auto kern = q4_attention_kernel<T, D, BS, TWICE, HOOK>;
     const int rc = ensure_smem_attr(reinterpret_cast<const void *>(kern), C::SMEM_BYTES, &done);
     if (rc)
         return rc;
