@@ -811,8 +811,9 @@ def reshape_and_cache_q4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.
     a scale and a minimum of its own (see pkv_reshape_and_cache_q4).
 
     key, value: [T, Hk, D] of float16 or bfloat16, which is the cache's type from
-    then on; their first dimension may have any stride (a slice of a fused
-    projection's output).  k_cache, v_cache: as q4_cache makes them."""
+    then on; contiguous but for their first dimension, whose stride is at least
+    Hk * D and a multiple of 16 bytes (a slice of a fused projection's output).
+    k_cache, v_cache: as q4_cache makes them."""
     rc = (_module or _native()).write_q4(key, value, k_cache, v_cache, slot_mapping, device_status, stream)
     if rc:
         raise PkvError(rc, "pkv_reshape_and_cache_q4")
@@ -825,9 +826,9 @@ def gather_cache_q4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tenso
     4-bit cache stand for (a negative slot leaves its rows as they are): what a
     prompt's prefill needs of a prefix that is cached.
 
-    key, value: [T, Hk, D], written; their first dimension may have any stride
-    that keeps rows apart.  Of the cache's type (what it was written from), or
-    float32 with dtype naming that type."""
+    key, value: [T, Hk, D], written; strides as for reshape_and_cache_q4.  Of the
+    cache's type (what it was written from), or float32 with dtype naming that
+    type."""
     if dtype is not None and dtype not in _DTYPE:
         raise ValueError("dtype must be float16 or bfloat16")
     rc = (_module or _native()).gather_q4(key, value, k_cache, v_cache, slot_mapping, None if dtype is None else _DTYPE[dtype],
@@ -851,8 +852,8 @@ def paged_attention_decode_q4(out: torch.Tensor, q: torch.Tensor, k_cache: torch
     """As paged_attention_decode, over a 4-bit cache that reshape_and_cache_q4 wrote.
 
     q: [B, H, D] of the cache's type (float16 or bfloat16: what it was written
-    from); its first dimension may have any stride.  out: [B, H, D], any floating
-    dtype.  max_context_len: host bound of context_lens (what the table can hold
+    from); contiguous but for its first dimension, whose stride is at least H * D
+    and a multiple of 16 bytes.  out: [B, H, D], any floating dtype.  max_context_len: host bound of context_lens (what the table can hold
     if omitted).  workspace: paged_attention_q4_workspace_bytes, allocated here if
     needed and not given."""
     rc = (_module or _native()).decode_q4(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,

@@ -89,9 +89,8 @@ template <int D, int BS> struct Q4Cfg {
     static constexpr int REC = R::template record<BS>;
     static constexpr int TOK = kQ4Unit;                        // tokens of a stage
     static constexpr int RECS = TOK / BS;
-    // from a tile's codes and pairs to the next's
+    // from a tile's codes to the next's
     static constexpr int NEXT_CODE = BS > TILE ? TILE * R::CODES : TILE / BS * REC;
-    static constexpr int NEXT_PAIR = BS > TILE ? TILE * R::PAIRS : TILE / BS * REC;
     static constexpr int STAGE_BYTES = 2 * RECS * REC;
     static constexpr int S = kQ4Ring / (kListWarps * STAGE_BYTES);
     static constexpr int CHUNK = 128;                          // units whose blocks are looked up at a time

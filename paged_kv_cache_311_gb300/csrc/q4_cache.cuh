@@ -41,7 +41,6 @@ template <int D> struct Q4Row {
     static constexpr int GROUPS = D / kQ4Group;
     static constexpr int CODES = D / 2;            // bytes of codes
     static constexpr int PAIRS = GROUPS * 4;       // bytes of (scale, minimum) pairs
-    static constexpr int WORDS = D / 8;
 
     // Byte offset of word w of row r in a record.
     __host__ __device__ __forceinline__ static int word(int r, int w)
