@@ -17,13 +17,26 @@ struct Q4Cut {
 
 // Rows that leave CTAs idle are divided among clusters, by each row's own length,
 // as long as all CTAs are resident at once; other short rows stay whole; the rest
-// is streamed, in shares of equal cost.  us, in that order (whole: one CTA a row):
-//   1 sequence of 4000 tokens, 8 kv heads (8 per row)     9.6   -     13.9
-//   16 of 2000 (3 per row)                               15.2   19.6   18.8
-//   30 of 2000                                             -   25.2   27.5
-//   64 of 128 to 2048, 32 kv heads                         -   81.5   82.5
-//   33 of up to 4095, heads of 64                          -   33.5   24.0
-//   16 of 8K to 16K                                        -     -    63.0
+// is streamed, in shares of equal cost.  us, in that order (whole: one CTA a row),
+// 8 kv heads of 128 where nothing else is said:
+//   1 sequence of 4000 tokens (8 per row)          9.6   34.2   13.5
+//   8 of 2000 (6 per row)                         11.0   19.2   14.0
+//   16 of 2000 (3 per row)                        15.3   19.8   18.1
+//   16 of 8K to 16K (3 per row)                   73.9  135.0   62.1
+//   30 of 2000                                      -    25.1   26.7
+//   57 of 2048: a row for each place               -    31.7   34.6
+//   64 of 2048                                      -    46.5   43.8
+//   75 of 2048                                      -    46.9   49.2
+//   64 of 128 to 2048, 32 kv heads                  -    82.4   83.9
+//   128 of 512 to 2048                              -    58.5   56.0
+//   256 of 512                                      -    50.0   53.2
+//   256 of 1 to 64                                  -    22.3   23.8
+//   256 of 1 to 64, 40 kv heads                     -   100.8   84.6
+//   33 of up to 4095, heads of 64                   -    34.2   23.9
+//   64 of 512 to 4000                               -    57.7   48.5
+// The rule goes by the longest length that the call names.  What it gives away is
+// in the lines where short rows come in a wave and a little, and in those of ten
+// thousand rows of one step, where either form is far from the bytes' time (9 us).
 // (Clusters of 8 whatever the rows, which come in waves: 16.8, 22.1, 82.3 for 8 of
 // 2000, 16 of 2000, 16 of 8K to 16K.)
 Q4Cut q4_cut(long long rows, long long max_context_len, int block_size, int partition_size)

@@ -32,16 +32,20 @@
 // largest score alone: weights are 2^(x - m) with m such that the largest
 // 2^(x - m) s, not the largest 2^(x - m), is near 2^7.
 //
-// What bounds it: instructions.  Sixteen contexts of 16K to 32K tokens with 8
-// query heads a kv head (454 MB) take 100 to 106 us, 4.3 to 4.5 TB/s or 64 to 68 %
-// of a copy's rate; one of 128K tokens with 4 heads 41 us (151 MB, 55 %); 64 of 128
-// to 2048 tokens, 32 kv heads, 83 to 88 us (56 %).  Without any loads the first
-// takes 103 us, from L2 the same.  A step of 32 tokens is some 560 warp
-// instructions, a third of them the masks and shifts that make codes operands;
-// the ALU pipe, at two cycles each, is busy 47 % of the time, the tensor pipe
-// 32 %, and more CTAs per SM (4: 111 us), fewer (2: 123, 1: 180), steps of 16
-// tokens (114), or K's products of one step among V's of the one before (118)
-// change little: the pipes' times add up rather than overlap.
+// What bounds it: the latency of dependent instructions, of which no unit is
+// full.  Sixteen contexts of 16K to 32K tokens with 8 query heads a kv head (454
+// MB) take 109 to 110 us, 4.1 TB/s or 62 % of a copy's rate; one of 128K tokens
+// with 4 heads 41 us (151 MB, 55 %); 64 of 128 to 2048 tokens, 32 kv heads, 82 to 88
+// us (55 to 58 %).  Of the first: 32 tokens take some 620 warp instructions, a
+// third of them the masks and shifts that make codes operands.  168 registers a
+// thread leave 12 warps an SM; a scheduler's 2.8 issue in 48 % of the cycles, the
+// ALU pipe is busy 47 % of the time, the tensor pipe 32 %.  Of the 5.5 cycles that
+// a warp takes per instruction 1.8 are fixed latencies, 1 the issue, 0.65 a pipe
+// that is busy, 0.6 another warp's issue, 0.5 reads of shared memory, 0.5 waits
+// for other memory, 0.3 dispatch, 0.2 barriers.  1, 2, 4 CTAs per SM: 175, 119,
+// 112 us.  Without any loads it took 105 us when it took 112 with them; steps of
+// 16 tokens (114) and K's products of one step among V's of the one before (118)
+// were compared with 111.
 //
 // The M axes' order is free: row 2 c + e + 8 f of a tile is its token
 // 4 c + 2 f + e (so that a thread's four tokens of V are neighbours), and a
@@ -77,8 +81,9 @@ struct Q4Params {
 
 constexpr int kQ4Unit = 32;      // tokens that a warp takes at a time
 // What a row's start and end cost a CTA, in units: shares are of equal cost.
-// (64 sequences of 128 to 2048 tokens, 32 kv heads: 90 us; with 4 units 100,
-// with none 119.)
+// (us with 0, 4, 8 and 12 units: 64 sequences of 128 to 2048 tokens, 32 kv heads,
+// in shares 112, 95.3, 84.0, 84.1; 33 of up to 4095, heads of 64 33.7, 25.5, 23.7,
+// 24.2.)
 constexpr int kQ4RowCost = 8;
 constexpr int kQ4Ring = 40960;   // ring bytes of a CTA at most
 constexpr int kQ4Ctas = 3;       // CTAs per SM
@@ -357,7 +362,9 @@ template <typename T, int D, int BS, bool TWICE> struct Q4Engine {
     // (flip: of four, the second and third) take s u + m as (m + 15 s) + (-s)
     // (15 - u): the sums stay as small as one step's, and of either sign in turn.
     // (Means over 60,000 tokens are then off by 2.6e-5 of their size; where each
-    // step only started from zero and was added rounded to nearest, by 2.0e-4.)
+    // step only started from zero and was added rounded to nearest, by 2.0e-4.
+    // Codes always from one side: 16 long contexts 109.4 us against 109.9, one of
+    // 128K tokens 40.2 against 41.0.)
     __device__ __forceinline__ float numbers(uint32_t kbase, uint32_t vbase, int nvalid) const
     {
         float top = kLeast;
