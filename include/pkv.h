@@ -671,9 +671,9 @@ int pkv_gather_cache_q4(void *key, int64_t key_stride, void *value, int64_t valu
  * head's scaled by a power of two: elements are off by at most 2^-35 of the
  * head's largest.  A softmax weight times a scale of V enters the product with
  * the codes in two f16 parts: off by 2^-22 of itself and 2^-32 of the head's
- * largest such product so far.  (For |q| below 2^100, numbers of V below
- * 2^90 in magnitude and contexts below 2^25 tokens; beyond, small weights are
- * lost, then sums overflow.)
+ * largest such product so far, in which a scale counts as 2^-100 at least.
+ * (For |q| below 2^100, numbers of V below 2^90 in magnitude and contexts below
+ * 2^25 tokens; beyond, small weights are lost, then sums overflow.)
  */
 int pkv_paged_attention_decode_q4(void *out, int out_dtype, const void *q, int64_t q_stride,
                                   int q_dtype, const void *k_cache, const void *v_cache,

@@ -853,8 +853,9 @@ def paged_attention_decode_q4(out: torch.Tensor, q: torch.Tensor, k_cache: torch
 
     q: [B, H, D] of the cache's type (float16 or bfloat16: what it was written
     from); contiguous but for its first dimension, whose stride is at least H * D
-    and a multiple of 16 bytes.  out: [B, H, D], any floating dtype.  max_context_len: host bound of context_lens (what the table can hold
-    if omitted).  workspace: paged_attention_q4_workspace_bytes, allocated here if
+    and a multiple of 16 bytes.  out: [B, H, D], any floating dtype.
+    max_context_len: host bound of context_lens (what the table can hold if
+    omitted).  workspace: paged_attention_q4_workspace_bytes, allocated here if
     needed and not given."""
     rc = (_module or _native()).decode_q4(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,
                                           partition_size, workspace, device_status, stream)
